@@ -16,6 +16,8 @@ KDA_DTYPE_FP32 = 1
 KDA_FLAG_QK_L2NORM = 1
 KDA_FLAG_GATE_SOFTPLUS = 2
 KDA_FLAG_SCALAR_GATE = 4
+KDA_SCAN_DT_SOFTPLUS = 1
+KDA_CONV_SILU = 1
 
 STATUS = {
     0: "KDA_OK", 1: "KDA_ERR_NULL_POINTER", 2: "KDA_ERR_BAD_SHAPE", 3: "KDA_ERR_UNSUPPORTED",
@@ -29,7 +31,11 @@ EXPORTS = ("kda_chunk_fwd_workspace_bytes", "kda_chunk_fwd", "kda_recurrent_fwd"
            "kda_chunk_bwd", "kda_dplr_recurrent_fwd",
            "kda_status_string", "kda_last_error", "kda_last_hip_error", "kda_abi_version", "kda_version",
            "kda_chunk_fwd_noalloc", "kda_chunk_fwd_noalloc_max_workspace_bytes", "kda_dplr_chunk_fwd",
-           "kda_dplr_chunk_fwd_workspace_bytes")
+           "kda_dplr_chunk_fwd_workspace_bytes",
+           "kda_selective_scan_fwd_workspace_bytes", "kda_selective_scan_fwd", "kda_selective_scan_step",
+           "kda_selective_scan_bwd_workspace_bytes", "kda_selective_scan_bwd", "kda_short_conv_fwd",
+           "kda_short_conv_step", "kda_short_conv_bwd_workspace_bytes", "kda_short_conv_bwd",
+           "kda_layer_norm_fwd", "kda_layer_norm_bwd_workspace_bytes", "kda_layer_norm_bwd")
 
 vp = ctypes.c_void_p
 
@@ -107,6 +113,108 @@ class DplrChunkArgs(ctypes.Structure):
     ]
 
 
+def _fields(spec: str):
+    """Fields from "type: name name ..." lines: p pointer, l int64, i int32, f float, d dtype, u flags, z size."""
+    kinds = dict(p=vp, l=ctypes.c_int64, i=ctypes.c_int32, f=ctypes.c_float, d=ctypes.c_int, u=ctypes.c_uint32,
+                 z=ctypes.c_size_t)
+    return [(name, kinds[line.split(":")[0].strip()]) for line in spec.strip().splitlines()
+            for name in line.split(":")[1].split()]
+
+
+class SelectiveScanArgs(ctypes.Structure):
+    _fields_ = _fields("""
+        u: struct_size
+        p: u dt A B C D z dt_bias initial_state final_state y cu_seqlens
+        l: u_stride dt_stride B_stride C_stride z_stride y_stride
+        i: batch T dim ds num_seqs
+        d: in_dtype out_dtype
+        p: workspace
+        z: workspace_bytes
+        p: stream
+        u: flags""")
+
+
+class SelectiveScanBwdArgs(ctypes.Structure):
+    _fields_ = _fields("""
+        u: struct_size
+        p: u dt A B C D z dt_bias initial_state grad_y grad_final_state
+        p: grad_u grad_dt grad_A grad_B grad_C grad_D grad_z grad_dt_bias grad_initial_state cu_seqlens
+        l: u_stride dt_stride B_stride C_stride z_stride grad_y_stride
+        l: grad_u_stride grad_dt_stride grad_B_stride grad_C_stride grad_z_stride
+        i: batch T dim ds num_seqs
+        d: in_dtype grad_dtype
+        p: workspace
+        z: workspace_bytes
+        p: stream
+        u: flags""")
+
+
+class ShortConvArgs(ctypes.Structure):
+    _fields_ = _fields("""
+        u: struct_size
+        p: x weight bias initial_state final_state y cu_seqlens
+        l: x_stride y_stride
+        i: batch T dim width num_seqs
+        d: in_dtype out_dtype w_dtype
+        p: stream
+        u: flags""")
+
+
+class ShortConvBwdArgs(ctypes.Structure):
+    _fields_ = _fields("""
+        u: struct_size
+        p: x weight bias initial_state grad_y grad_final_state grad_x grad_weight grad_bias grad_initial_state
+        p: cu_seqlens
+        l: x_stride grad_y_stride grad_x_stride
+        i: batch T dim width num_seqs
+        d: in_dtype grad_dtype w_dtype
+        p: workspace
+        z: workspace_bytes
+        p: stream
+        u: flags""")
+
+
+class LayerNormArgs(ctypes.Structure):
+    _fields_ = _fields("""
+        u: struct_size
+        p: x residual weight bias y residual_out
+        l: x_stride residual_stride y_stride residual_out_stride rows
+        i: dim
+        f: eps
+        d: x_dtype res_dtype w_dtype out_dtype
+        p: stream""")
+
+
+class LayerNormBwdArgs(ctypes.Structure):
+    _fields_ = _fields("""
+        u: struct_size
+        p: x grad_y weight grad_residual grad_x grad_weight grad_bias
+        l: x_stride grad_y_stride grad_residual_stride grad_x_stride rows
+        i: dim
+        f: eps
+        d: x_dtype gy_dtype res_dtype w_dtype grad_dtype
+        p: workspace
+        z: workspace_bytes
+        p: stream""")
+
+
+# The layer operators' functions: their argument struct, and whether they return a size.
+LAYER_FUNCTIONS = {
+    "kda_selective_scan_fwd_workspace_bytes": (SelectiveScanArgs, True),
+    "kda_selective_scan_fwd": (SelectiveScanArgs, False),
+    "kda_selective_scan_step": (SelectiveScanArgs, False),
+    "kda_selective_scan_bwd_workspace_bytes": (SelectiveScanBwdArgs, True),
+    "kda_selective_scan_bwd": (SelectiveScanBwdArgs, False),
+    "kda_short_conv_fwd": (ShortConvArgs, False),
+    "kda_short_conv_step": (ShortConvArgs, False),
+    "kda_short_conv_bwd_workspace_bytes": (ShortConvBwdArgs, True),
+    "kda_short_conv_bwd": (ShortConvBwdArgs, False),
+    "kda_layer_norm_fwd": (LayerNormArgs, False),
+    "kda_layer_norm_bwd_workspace_bytes": (LayerNormBwdArgs, True),
+    "kda_layer_norm_bwd": (LayerNormBwdArgs, False),
+}
+
+
 class KdaError(RuntimeError):
     def __init__(self, status: int, message: str):
         self.status = status
@@ -161,6 +269,10 @@ def load():
         lib.kda_dplr_chunk_fwd.argtypes = [ctypes.POINTER(DplrChunkArgs)]
         lib.kda_dplr_chunk_fwd_workspace_bytes.restype = ctypes.c_size_t
         lib.kda_dplr_chunk_fwd_workspace_bytes.argtypes = [ctypes.POINTER(DplrChunkArgs)]
+        for name, (struct, size) in LAYER_FUNCTIONS.items():
+            fn = getattr(lib, name)
+            fn.argtypes = [ctypes.POINTER(struct)]
+            fn.restype = ctypes.c_size_t if size else ctypes.c_int
         _lib = lib
     return _lib
 
@@ -228,3 +340,17 @@ def chunk_bwd_workspace_raw(args: RecurrentBwdArgs) -> int:
 def dplr_fwd_raw(args: DplrArgs) -> int:
     args.struct_size = ctypes.sizeof(DplrArgs)
     return load().kda_dplr_recurrent_fwd(ctypes.byref(args))
+
+
+def layer_raw(name: str, args) -> int:
+    """Calls one of LAYER_FUNCTIONS; args.struct_size is set here."""
+    args.struct_size = ctypes.sizeof(args)
+    return getattr(load(), name)(ctypes.byref(args))
+
+
+def layer_workspace(name: str, args) -> int:
+    """A LAYER_FUNCTIONS workspace query; invalid sizes raise."""
+    n = layer_raw(name, args)
+    if n == 2 ** 64 - 1:
+        raise KdaError(STATUS_CODE["KDA_ERR_BAD_SHAPE"], load().kda_last_error().decode())
+    return n

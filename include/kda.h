@@ -453,6 +453,272 @@ kda_status kda_chunk_fwd_noalloc(const kda_chunk_fwd_args *args);
 /* KDA_NOALLOC_SCRATCH_BYTES of the loaded library. */
 size_t kda_chunk_fwd_noalloc_max_workspace_bytes(void);
 
+/*
+ * ---- Layer operators around the recurrence -------------------------------
+ *
+ * A selective state space scan, its short causal convolution (which also
+ * stands in front of KDA's own q, k and v; the Kimi Linear review notes list
+ * it among the layer's parts) and layer norm, for prompts, single tokens and
+ * gradients.  The conventions of the top of this file hold, with two
+ * additions:
+ *  - Token tensors have a row stride: `x_stride` is the distance in elements
+ *    between consecutive tokens (rows) of `x`, at least its width, so that
+ *    slices of a wider projection need no copy.  Token t of sequence b of a
+ *    fixed-length batch is row b * T + t.  Token tensors need only their
+ *    elements' alignment; 16-byte aligned bases and strides run faster.
+ *    Parameters and states are contiguous.
+ *  - Packed input (cu_seqlens, N + 1 device offsets) may end before the last
+ *    row: output rows at and behind cu_seqlens[N] are left as they were.
+ * Outputs overlap neither inputs nor each other, except where an entry point
+ * says so; two strided tensors that interleave without sharing an element
+ * (column slices of one buffer) do not overlap.
+ */
+
+/* The scan's step sizes are softplus(dt + dt_bias) instead of dt + dt_bias. */
+#define KDA_SCAN_DT_SOFTPLUS 1u
+/* The convolution's output goes through x * sigmoid(x). */
+#define KDA_CONV_SILU 1u
+
+/*
+ * Selective state space scan.  Per sequence, channel d < dim and state n < ds,
+ *     delta_t = softplus?(dt_t + dt_bias),     h_t = exp(delta_t A) h_{t-1} + delta_t u_t B_t,
+ *     y_t = (sum_n C_t[n] h_t[n] + D u_t) * silu?(z_t),
+ * with the state and every sum in fp32.
+ *
+ * Shapes (rows = batch * T, N = number of sequences):
+ *   u, dt, z, y : [rows, dim]; z may be NULL (no gate)
+ *   B, C        : [rows, ds], shared by all channels
+ *   A : [dim, ds] fp32, finite, normally negative;  D, dt_bias : [dim] fp32 or NULL
+ *   initial_state, final_state : [N, dim, ds] fp32, or NULL (zeros; not wanted); may be equal
+ *   cu_seqlens  : NULL, or int32 [N + 1] offsets (then batch must be 1)
+ *   ds : 1 to 64.
+ * u, dt, B, C and z have in_dtype, y out_dtype.
+ *   workspace : kda_selective_scan_fwd_workspace_bytes() bytes.
+ *
+ * kda_selective_scan_step: one token for each of `batch` sequences (T must be
+ * 1, cu_seqlens NULL, final_state given); no workspace.  kda_selective_scan_fwd
+ * with T = 1 and no cu_seqlens gives the same bits.
+ */
+typedef struct {
+    uint32_t struct_size; /* = sizeof(kda_selective_scan_args) */
+    const void *u;
+    const void *dt;
+    const float *A;
+    const void *B;
+    const void *C;
+    const float *D;
+    const void *z;
+    const float *dt_bias;
+    const float *initial_state;
+    float *final_state;
+    void *y;
+    const int32_t *cu_seqlens;
+    int64_t u_stride, dt_stride, B_stride, C_stride, z_stride, y_stride;
+    int32_t batch, T, dim, ds, num_seqs;
+    kda_dtype in_dtype;
+    kda_dtype out_dtype;
+    void *workspace;
+    size_t workspace_bytes;
+    void *stream;
+    uint32_t flags; /* KDA_SCAN_* */
+} kda_selective_scan_args;
+
+size_t kda_selective_scan_fwd_workspace_bytes(const kda_selective_scan_args *args);
+kda_status kda_selective_scan_fwd(const kda_selective_scan_args *args);
+kda_status kda_selective_scan_step(const kda_selective_scan_args *args);
+
+/*
+ * Gradients of the scan for grad_y [rows, dim] (in_dtype) and the optional
+ * grad_final_state [N, dim, ds] fp32.  With gp = grad_y silu(z), going
+ * backwards through the tokens,
+ *     G_t = C_t gp_t + exp(delta_{t+1} A) G_{t+1},
+ *     dC_t = sum_d gp h_t,  dB_t = sum_d G_t delta u,  P = sum_n G_t B_t,  du = D gp + delta P,
+ *     ddelta = u P + sum_n A G_t (exp(delta A) h_{t-1}),  dA = sum_t delta G_t (exp(delta A) h_{t-1}),
+ *     dD = sum_t gp u,  dz = grad_y y' silu'(z),  ddt = ddelta (sigmoid(dt + dt_bias) with softplus),
+ * and the initial-state gradient is exp(delta A) G of the first token.  The
+ * forward states are recomputed from the inputs.
+ *
+ *   grad_u, grad_dt, grad_z : [rows, dim] grad_dtype (grad_z exactly where z is given)
+ *   grad_B, grad_C : [rows, ds] grad_dtype
+ *   grad_A : [dim, ds], grad_D, grad_dt_bias : [dim] fp32 (NULL to skip; grad_A is required)
+ *   grad_initial_state : [N, dim, ds] fp32 or NULL; may equal initial_state or grad_final_state
+ *   workspace : kda_selective_scan_bwd_workspace_bytes() bytes.
+ */
+typedef struct {
+    uint32_t struct_size; /* = sizeof(kda_selective_scan_bwd_args) */
+    const void *u;
+    const void *dt;
+    const float *A;
+    const void *B;
+    const void *C;
+    const float *D;
+    const void *z;
+    const float *dt_bias;
+    const float *initial_state;
+    const void *grad_y;
+    const float *grad_final_state;
+    void *grad_u;
+    void *grad_dt;
+    float *grad_A;
+    void *grad_B;
+    void *grad_C;
+    float *grad_D;
+    void *grad_z;
+    float *grad_dt_bias;
+    float *grad_initial_state;
+    const int32_t *cu_seqlens;
+    int64_t u_stride, dt_stride, B_stride, C_stride, z_stride, grad_y_stride;
+    int64_t grad_u_stride, grad_dt_stride, grad_B_stride, grad_C_stride, grad_z_stride;
+    int32_t batch, T, dim, ds, num_seqs;
+    kda_dtype in_dtype;
+    kda_dtype grad_dtype;
+    void *workspace;
+    size_t workspace_bytes;
+    void *stream;
+    uint32_t flags; /* KDA_SCAN_* */
+} kda_selective_scan_bwd_args;
+
+size_t kda_selective_scan_bwd_workspace_bytes(const kda_selective_scan_bwd_args *args);
+kda_status kda_selective_scan_bwd(const kda_selective_scan_bwd_args *args);
+
+/*
+ * Short causal depthwise convolution over time, per channel d < dim with
+ * `width` taps (2, 3 or 4):
+ *     p_t = bias + sum_j weight[d, j] x_{t - width + 1 + j},   y_t = p_t  (or silu(p_t)),
+ * where inputs before a sequence's start come from its state, the last
+ * width - 1 inputs, oldest first (zeros without one).
+ *
+ *   x, y : [rows, dim] (in_dtype, out_dtype);  weight [dim, width], bias [dim] or NULL: w_dtype
+ *   initial_state, final_state : [N, width - 1, dim] in_dtype or NULL; may be equal
+ * kda_short_conv_step: one token for each of `batch` sequences (T = 1,
+ * cu_seqlens NULL, final_state given).  kda_short_conv_fwd with T = 1 and no
+ * cu_seqlens gives the same bits.  No workspace.
+ */
+typedef struct {
+    uint32_t struct_size; /* = sizeof(kda_short_conv_args) */
+    const void *x;
+    const void *weight;
+    const void *bias;
+    const void *initial_state;
+    void *final_state;
+    void *y;
+    const int32_t *cu_seqlens;
+    int64_t x_stride, y_stride;
+    int32_t batch, T, dim, width, num_seqs;
+    kda_dtype in_dtype;
+    kda_dtype out_dtype;
+    kda_dtype w_dtype;
+    void *stream;
+    uint32_t flags; /* KDA_CONV_* */
+} kda_short_conv_args;
+
+kda_status kda_short_conv_fwd(const kda_short_conv_args *args);
+kda_status kda_short_conv_step(const kda_short_conv_args *args);
+
+/*
+ * Gradients of the convolution for grad_y [rows, dim] (in_dtype) and the
+ * optional grad_final_state [N, width - 1, dim] fp32:
+ *     gp = grad_y act'(p),  dx_t = sum_j weight[j] gp_{t + width - 1 - j} (inside the sequence),
+ *     dweight[j] = sum_t gp_t x_{t - width + 1 + j},  dbias = sum_t gp_t.
+ *   grad_x : [rows, dim] grad_dtype;  grad_weight [dim, width], grad_bias [dim] fp32 (grad_bias may be NULL)
+ *   grad_initial_state : [N, width - 1, dim] fp32 or NULL; may equal grad_final_state
+ *   workspace : kda_short_conv_bwd_workspace_bytes() bytes.
+ */
+typedef struct {
+    uint32_t struct_size; /* = sizeof(kda_short_conv_bwd_args) */
+    const void *x;
+    const void *weight;
+    const void *bias;
+    const void *initial_state;
+    const void *grad_y;
+    const float *grad_final_state;
+    void *grad_x;
+    float *grad_weight;
+    float *grad_bias;
+    float *grad_initial_state;
+    const int32_t *cu_seqlens;
+    int64_t x_stride, grad_y_stride, grad_x_stride;
+    int32_t batch, T, dim, width, num_seqs;
+    kda_dtype in_dtype;
+    kda_dtype grad_dtype;
+    kda_dtype w_dtype;
+    void *workspace;
+    size_t workspace_bytes;
+    void *stream;
+    uint32_t flags; /* KDA_CONV_* */
+} kda_short_conv_bwd_args;
+
+size_t kda_short_conv_bwd_workspace_bytes(const kda_short_conv_bwd_args *args);
+kda_status kda_short_conv_bwd(const kda_short_conv_bwd_args *args);
+
+/*
+ * Layer norm over rows of `dim` elements (1 to 16384), with an optional
+ * residual added in front:
+ *     s = x + residual,  y = (s - mean(s)) / sqrt(var(s) + eps) * weight + bias,
+ * mean and (biased) variance in fp32 over s before any rounding.  A head's
+ * output row of the recurrence (o seen as [B*T*H, dv]) and a model-width row
+ * are both rows here.
+ *   x, y : [rows, dim] (x_dtype, out_dtype);  weight, bias : [dim] w_dtype or NULL (1, 0)
+ *   residual, residual_out : [rows, dim] res_dtype, both or neither; residual_out = s rounded;
+ *                            they may be equal (same stride)
+ */
+typedef struct {
+    uint32_t struct_size; /* = sizeof(kda_layer_norm_args) */
+    const void *x;
+    const void *residual;
+    const void *weight;
+    const void *bias;
+    void *y;
+    void *residual_out;
+    int64_t x_stride, residual_stride, y_stride, residual_out_stride;
+    int64_t rows;
+    int32_t dim;
+    float eps;
+    kda_dtype x_dtype;
+    kda_dtype res_dtype;
+    kda_dtype w_dtype;
+    kda_dtype out_dtype;
+    void *stream;
+} kda_layer_norm_args;
+
+kda_status kda_layer_norm_fwd(const kda_layer_norm_args *args);
+
+/*
+ * Gradients of layer norm.  x is what was normalised (residual_out where a
+ * residual was added); mean and variance are recomputed from it.  With
+ * g = grad_y * weight and xh = (x - mean) * rstd,
+ *     grad_x = rstd (g - mean(g) - xh mean(g xh)) + grad_residual,
+ *     grad_weight = sum over rows of grad_y xh,  grad_bias = sum over rows of grad_y.
+ *   x (x_dtype), grad_y (gy_dtype), grad_residual (res_dtype, or NULL), grad_x (grad_dtype) : [rows, dim]
+ *   weight : [dim] w_dtype or NULL;  grad_weight, grad_bias : [dim] fp32, or NULL to skip
+ *   workspace : kda_layer_norm_bwd_workspace_bytes() bytes.
+ */
+typedef struct {
+    uint32_t struct_size; /* = sizeof(kda_layer_norm_bwd_args) */
+    const void *x;
+    const void *grad_y;
+    const void *weight;
+    const void *grad_residual;
+    void *grad_x;
+    float *grad_weight;
+    float *grad_bias;
+    int64_t x_stride, grad_y_stride, grad_residual_stride, grad_x_stride;
+    int64_t rows;
+    int32_t dim;
+    float eps;
+    kda_dtype x_dtype;
+    kda_dtype gy_dtype;
+    kda_dtype res_dtype;
+    kda_dtype w_dtype;
+    kda_dtype grad_dtype;
+    void *workspace;
+    size_t workspace_bytes;
+    void *stream;
+} kda_layer_norm_bwd_args;
+
+size_t kda_layer_norm_bwd_workspace_bytes(const kda_layer_norm_bwd_args *args);
+kda_status kda_layer_norm_bwd(const kda_layer_norm_bwd_args *args);
+
 /* Static text for a status code. */
 const char *kda_status_string(kda_status s);
 /* Thread-local text describing the last failure on this thread ("" if none):
