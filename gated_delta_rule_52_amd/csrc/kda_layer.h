@@ -91,8 +91,41 @@ __device__ __forceinline__ Tile find_tile(const SeqTiles &s, int64_t slot) {
     t.begin = start + static_cast<int64_t>(t.k) * s.L;
     const int left = len - t.k * s.L;
     t.len = left < s.L ? left : s.L;
+    // uniform over the workgroup: kept in scalar registers
+    t.n = __builtin_amdgcn_readfirstlane(t.n);
+    t.k = __builtin_amdgcn_readfirstlane(t.k);
+    t.count = __builtin_amdgcn_readfirstlane(t.count);
+    t.len = __builtin_amdgcn_readfirstlane(t.len);
+    t.begin = static_cast<int64_t>(static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(t.begin))));
     return t;
 }
+
+// One channel's column of a tile's rows, read or written four rows at a time by the lanes q = 0..3 of a quad:
+// a uniform address per group of four rows plus a 32-bit lane offset that stays the same, so that a step
+// costs scalar additions only.  Strides are at most 2^27 elements, which keeps 3 rows inside 32 bits.
+struct QuadColumn {
+    char *at;           // the tile's first row
+    int64_t step;       // bytes per row
+    uint32_t off, tail; // lane offset; the same in a last group of fewer than four rows, held to its last row
+    __device__ __forceinline__ QuadColumn(const Rows &r, int64_t begin, int len, int ch, int q) {
+        const int e = r.bf16 ? 2 : 4, left = (len & 3) - 1;
+        at = static_cast<char *>(r.p) + begin * r.stride * e;
+        step = r.stride * e;
+        off = (static_cast<uint32_t>(q) * static_cast<uint32_t>(r.stride) + static_cast<uint32_t>(ch)) * e;
+        const int qt = left >= 0 && q > left ? left : q;
+        tail = (static_cast<uint32_t>(qt) * static_cast<uint32_t>(r.stride) + static_cast<uint32_t>(ch)) * e;
+    }
+    // the group of rows t .. t + 3 of the tile; whole: all four exist
+    template <typename E>
+    __device__ __forceinline__ E get(int t, bool whole) const {
+        return *reinterpret_cast<const E *>(at + t * step + (whole ? off : tail));
+    }
+    __device__ __forceinline__ void put(int t, int bf16, float x) const {
+        char *p = at + t * step + off;
+        if (bf16) *reinterpret_cast<uint16_t *>(p) = f32_to_bf16(x);
+        else *reinterpret_cast<float *>(p) = x;
+    }
+};
 
 // x * sigmoid(x) and the sigmoid.
 constexpr float kLog2e = 1.4426950408889634f;

@@ -13,6 +13,10 @@
 // and block of 16 tokens in LDS (double buffered), and read as one 16-byte access per quad lane and token.
 // Inputs of the next block are in flight while one is computed.  Tokens past a tile's end count as
 // delta = 0, u = 0: decay 1, nothing added.
+//
+// Sequences too few to fill the chip are cut into tiles: a local pass walks every tile but a sequence's last
+// from a zero state, a combine chains what they reach (a tile's decay needs only its sum of delta), and the
+// output pass walks every tile from its true state.
 #include "kda_layer.h"
 
 namespace kda {
@@ -28,53 +32,73 @@ struct Raw {
     static __device__ __forceinline__ float f(T x) { return Elem<InBf16>::load(&x, 0); }
 };
 
-template <int R, bool InBf16>
+// What a tiled scan keeps between its passes, in floats.
+struct FwdSpace {
+    float *H;    // [slot][dim][ds] the local pass: state a tile reaches from zero; after the combine: state it starts from
+    float *sum;  // [slot][dim] sum of delta over the tile: its decay is exp(A sum)
+    int64_t bytes;
+};
+__host__ __device__ inline FwdSpace fwd_space(float *ws, const SeqTiles &seq, int dim, int ds) {
+    const int64_t slots = seq.slots();
+    return {ws, ws ? ws + slots * dim * ds : nullptr, slots * dim * (ds + 1) * 4};
+}
+
+enum { kOutputs, kLocal };
+
+template <int MODE, int R, bool InBf16>
 __global__ void __launch_bounds__(256) scan_kernel(ScanFwdLaunch P) {
     using E = typename Raw<InBf16>::T;
-    constexpr int NS = 4 * R, kStage = kScanBlock * NS / 256;  // staged values per thread
-    static_assert(kScanBlock * NS % 256 == 0 || NS < 16, "staging");
-    constexpr int kSt = kStage > 0 ? kStage : 1;
-    __shared__ __attribute__((aligned(16))) float sB[2][kScanBlock][NS], sC[2][kScanBlock][NS];
+    constexpr int NS = 4 * R, kSt = kScanBlock * NS / 256;  // staged values per thread
+    __shared__ __attribute__((aligned(16))) float sB[2][kScanBlock][NS], sC[MODE == kLocal ? 1 : 2][kScanBlock][NS];
 
     const int groups = (P.dim + kScanChannels - 1) / kScanChannels;
     const int64_t slot = blockIdx.x / groups;
     const Tile tl = find_tile(P.seq, slot);
-    if (!tl.valid) return;
+    if (!tl.valid || (MODE == kLocal && tl.last())) return;  // nothing follows a last tile
     const int lane = threadIdx.x & 63, q = lane & 3;
     const int ch = static_cast<int>(blockIdx.x % groups) * kScanChannels + (threadIdx.x >> 2);
     const bool live = ch < P.dim;
     const int chc = live ? ch : P.dim - 1;
+    const FwdSpace W = fwd_space(P.ws, P.seq, P.dim, P.ds);
 
     float A2[R], h[R];
     const int64_t sbase = (static_cast<int64_t>(tl.n) * P.dim + chc) * P.ds + q * R;
+    const int64_t wbase = (slot * P.dim + chc) * P.ds + q * R;
+    // A sequence's only tile starts from its initial state; of several, all start from what the combine left
+    // (the first too: the last may be writing the final state in the initial one's place).
+    const float *from = MODE == kLocal ? nullptr : tl.count > 1 ? W.H + wbase : P.h0 ? P.h0 + sbase : nullptr;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         const bool in = q * R + r < P.ds;
         A2[r] = in ? kLog2e * P.A[static_cast<int64_t>(chc) * P.ds + q * R + r] : 0.f;
-        h[r] = in && P.h0 ? P.h0[sbase + r] : 0.f;
+        h[r] = in && from ? from[r] : 0.f;
     }
     const float skip = P.D ? P.D[chc] : 0.f, bias = P.dt_bias ? P.dt_bias[chc] : 0.f;
+    const bool gated = MODE == kOutputs && P.z.p;
 
-    const E *u = static_cast<const E *>(P.u.p), *dt = static_cast<const E *>(P.dt.p);
-    const E *z = static_cast<const E *>(P.z.p);
-    const E *Bp = static_cast<const E *>(P.B.p), *Cp = static_cast<const E *>(P.C.p);
-    E ru[4], rdt[4], rz[4], rB[kSt], rC[kSt];
+    const QuadColumn cu(P.u, tl.begin, tl.len, chc, q), cd(P.dt, tl.begin, tl.len, chc, q);
+    const QuadColumn cz(P.z, tl.begin, tl.len, chc, q), cy(P.y, tl.begin, tl.len, chc, q);
+    const E *Bp = static_cast<const E *>(P.B.p) + tl.begin * P.B.stride;
+    const E *Cp = static_cast<const E *>(P.C.p) + tl.begin * P.C.stride;
+    E ru[4] = {}, rdt[4] = {}, rz[4] = {}, rB[kSt], rC[kSt];
     auto fetch = [&](int t0) {  // the block at t0 of the tile, into registers
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int t = t0 + 4 * j + q;
-            const int64_t row = tl.begin + (t < tl.len ? t : tl.len - 1);
-            rdt[j] = dt[row * P.dt.stride + chc];
-            ru[j] = u[row * P.u.stride + chc];
-            if (z) rz[j] = z[row * P.z.stride + chc];
+            const int t = t0 + 4 * j;
+            if (t >= tl.len) break;
+            const bool whole = t + 4 <= tl.len;
+            rdt[j] = cd.get<E>(t, whole);
+            ru[j] = cu.get<E>(t, whole);
+            if (gated) rz[j] = cz.get<E>(t, whole);
         }
 #pragma unroll
         for (int i = 0; i < kSt; ++i) {
-            const int e = i * 256 + threadIdx.x, t = t0 + e / NS, n = e % NS;
+            const int e = i * 256 + threadIdx.x, t = e / NS, n = e % NS;
             rB[i] = rC[i] = 0;
-            if (e < kScanBlock * NS && t < tl.len && n < P.ds) {
-                rB[i] = Bp[(tl.begin + t) * P.B.stride + n];
-                rC[i] = Cp[(tl.begin + t) * P.C.stride + n];
+            if (t0 + t < tl.len && n < P.ds) {
+                rB[i] = (Bp + t0 * P.B.stride)[static_cast<uint32_t>(t) * static_cast<uint32_t>(P.B.stride) + n];
+                if (MODE == kOutputs)
+                    rC[i] = (Cp + t0 * P.C.stride)[static_cast<uint32_t>(t) * static_cast<uint32_t>(P.C.stride) + n];
             }
         }
     };
@@ -82,13 +106,12 @@ __global__ void __launch_bounds__(256) scan_kernel(ScanFwdLaunch P) {
 #pragma unroll
         for (int i = 0; i < kSt; ++i) {
             const int e = i * 256 + threadIdx.x;
-            if (e < kScanBlock * NS) {
-                (&sB[buf][0][0])[e] = Raw<InBf16>::f(rB[i]);
-                (&sC[buf][0][0])[e] = Raw<InBf16>::f(rC[i]);
-            }
+            (&sB[buf][0][0])[e] = Raw<InBf16>::f(rB[i]);
+            if (MODE == kOutputs) (&sC[buf][0][0])[e] = Raw<InBf16>::f(rC[i]);
         }
     };
 
+    float total = 0.f;  // of delta over this lane's tokens
     if (tl.len > 0) {
         fetch(0);
         stage(0);
@@ -103,8 +126,9 @@ __global__ void __launch_bounds__(256) scan_kernel(ScanFwdLaunch P) {
             us[j] = in ? Raw<InBf16>::f(ru[j]) : 0.f;
             de[j] = in ? (P.softplus ? softplus_f(d) : d) : 0.f;
             xs[j] = de[j] * us[j];
-            zs[j] = z ? Raw<InBf16>::f(rz[j]) : 0.f;
+            zs[j] = gated ? Raw<InBf16>::f(rz[j]) : 0.f;
         }
+        if (MODE == kLocal) total += (de[0] + de[1]) + (de[2] + de[3]);
         const bool more = t0 + kScanBlock < tl.len;
         if (more) fetch(t0 + kScanBlock);
 #pragma unroll
@@ -112,12 +136,12 @@ __global__ void __launch_bounds__(256) scan_kernel(ScanFwdLaunch P) {
             if (t0 + 4 * j >= tl.len) break;
             float yp[4];
             auto token = [&](float dl, float xl, int i) {
-                const float *bt = &sB[buf][4 * j + i][q * R], *ct = &sC[buf][4 * j + i][q * R];
+                const float *bt = &sB[buf][4 * j + i][q * R], *ct = &sC[MODE == kLocal ? 0 : buf][4 * j + i][q * R];
                 float acc = 0.f;
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
                     h[r] = fmaf(__builtin_amdgcn_exp2f(dl * A2[r]), h[r], xl * bt[r]);
-                    acc = fmaf(ct[r], h[r], acc);
+                    if (MODE == kOutputs) acc = fmaf(ct[r], h[r], acc);
                 }
                 yp[i] = acc;
             };
@@ -125,18 +149,62 @@ __global__ void __launch_bounds__(256) scan_kernel(ScanFwdLaunch P) {
             token(quad_bcast<1>(de[j]), quad_bcast<1>(xs[j]), 1);
             token(quad_bcast<2>(de[j]), quad_bcast<2>(xs[j]), 2);
             token(quad_bcast<3>(de[j]), quad_bcast<3>(xs[j]), 3);
-            float y = fmaf(skip, us[j], quad_transpose_sum(yp[0], yp[1], yp[2], yp[3], q));
-            if (z) y *= zs[j] * sigmoid_f(zs[j]);
-            const int t = t0 + 4 * j + q;
-            if (live && t < tl.len) P.y.put(tl.begin + t, ch, y);
+            if (MODE == kOutputs) {
+                float y = fmaf(skip, us[j], quad_transpose_sum(yp[0], yp[1], yp[2], yp[3], q));
+                if (gated) y *= zs[j] * sigmoid_f(zs[j]);
+                if (live && t0 + 4 * j + q < tl.len) cy.put(t0 + 4 * j, P.y.bf16, y);
+            }
         }
         if (more) stage(buf ^ 1);
         __syncthreads();
     }
-    if (P.hT && live && tl.last()) {
+    if (MODE == kLocal) {
+        total = quad_sum(total);
+        if (live) {
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                if (q * R + r < P.ds) W.H[wbase + r] = h[r];
+            if (q == 0) W.sum[slot * P.dim + ch] = total;
+        }
+    } else if (P.hT && live && tl.last()) {
 #pragma unroll
         for (int r = 0; r < R; ++r)
             if (q * R + r < P.ds) P.hT[sbase + r] = h[r];
+    }
+}
+
+// Chains the tiles of every sequence that has several: a tile starts from the state its predecessor leaves,
+// exp(A sum) times what that started from plus what it reached from zero.
+__global__ void __launch_bounds__(256) scan_combine_kernel(ScanFwdLaunch P) {
+    const int n = blockIdx.y;
+    const int64_t e = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x, states = static_cast<int64_t>(P.dim) * P.ds;
+    int64_t start;
+    int len;
+    P.seq.sequence(n, start, len);
+    const int count = (len + P.seq.L - 1) / P.seq.L;
+    if (e >= states || count <= 1) return;
+    const FwdSpace W = fwd_space(P.ws, P.seq, P.dim, P.ds);
+    const int64_t first = P.seq.first_slot(n, start);
+    const int ch = static_cast<int>(e / P.ds);
+    const float A2 = kLog2e * P.A[e];
+    float carry = P.h0 ? P.h0[n * states + e] : 0.f;
+    float *H = W.H + first * states + e;
+    const float *sum = W.sum + first * P.dim + ch;
+    constexpr int U = 8;  // tiles in flight: their loads do not wait for the chain
+    for (int k = 0; k < count; k += U) {
+        float h[U], d[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const bool in = k + i + 1 < count;  // the last tile has no successor
+            h[i] = in ? H[(k + i) * states] : 0.f;
+            d[i] = in ? sum[static_cast<int64_t>(k + i) * P.dim] : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            if (k + i >= count) break;
+            H[(k + i) * states] = carry;
+            carry = fmaf(__builtin_amdgcn_exp2f(A2 * d[i]), carry, h[i]);
+        }
     }
 }
 
@@ -181,16 +249,38 @@ __global__ void __launch_bounds__(256) scan_step_kernel(ScanFwdLaunch P) {
 
 SeqTiles scan_fwd_tiles(const int32_t *cu, int N, int T, int dim, int ds) {
     SeqTiles s{cu, N, T, T > 0 ? T : 1};
+    const int64_t groups = (dim + kScanChannels - 1) / kScanChannels;
+    constexpr int64_t kGroups = 1024;  // workgroups wanted: 4 waves per SIMD
+    // Whole sequences where they fill the chip by themselves; else tiles, and a second pass over the inputs.
+    if (!cu && N * groups >= kGroups / 2) return s;
+    int64_t L = (s.rows() * groups + kGroups - 1) / kGroups;
+    L = (L + kScanBlock - 1) / kScanBlock * kScanBlock;
+    if (L < 64) L = 64;
+    if (L < T) s.L = static_cast<int>(L);
     return s;
 }
 
-size_t scan_fwd_workspace_bytes(const SeqTiles &seq, int dim, int ds) { return 0; }
+static bool tiled(const SeqTiles &s) { return s.T > s.L; }
+
+size_t scan_fwd_workspace_bytes(const SeqTiles &seq, int dim, int ds) {
+    return tiled(seq) ? fwd_space(nullptr, seq, dim, ds).bytes : 0;
+}
+
+template <int R, bool InBf16>
+static void launch_passes(const ScanFwdLaunch &P, unsigned grid) {
+    if (tiled(P.seq)) {
+        scan_kernel<kLocal, R, InBf16><<<grid, 256, 0, P.stream>>>(P);
+        const int64_t states = static_cast<int64_t>(P.dim) * P.ds;
+        scan_combine_kernel<<<dim3(static_cast<unsigned>((states + 255) / 256), P.seq.N), 256, 0, P.stream>>>(P);
+    }
+    scan_kernel<kOutputs, R, InBf16><<<grid, 256, 0, P.stream>>>(P);
+}
 
 template <bool InBf16>
 static void launch_main(const ScanFwdLaunch &P, unsigned grid) {
-    if (P.ds <= 16) scan_kernel<4, InBf16><<<grid, 256, 0, P.stream>>>(P);
-    else if (P.ds <= 32) scan_kernel<8, InBf16><<<grid, 256, 0, P.stream>>>(P);
-    else scan_kernel<16, InBf16><<<grid, 256, 0, P.stream>>>(P);
+    if (P.ds <= 16) launch_passes<4, InBf16>(P, grid);
+    else if (P.ds <= 32) launch_passes<8, InBf16>(P, grid);
+    else launch_passes<16, InBf16>(P, grid);
 }
 
 hipError_t launch_scan_fwd(const ScanFwdLaunch &P) {
