@@ -3,9 +3,16 @@
 // finishes every parameter gradient.
 #pragma once
 
+#include <type_traits>
+
 #include "kda_device.h"
 
 namespace kda {
+
+// fp32 to bf16, nearest even, by the conversion instruction.
+__device__ __forceinline__ uint16_t to_bf16(float x) {
+    return __builtin_bit_cast(uint16_t, static_cast<__bf16>(x));
+}
 
 // A [rows, width] tensor whose rows are `stride` elements apart, in bf16 or fp32.
 struct Rows {
@@ -18,7 +25,7 @@ struct Rows {
     }
     __device__ __forceinline__ void put(int64_t row, int col, float x) const {
         const int64_t i = row * stride + col;
-        if (bf16) static_cast<uint16_t *>(p)[i] = f32_to_bf16(x);
+        if (bf16) static_cast<uint16_t *>(p)[i] = to_bf16(x);
         else static_cast<float *>(p)[i] = x;
     }
 };
@@ -60,6 +67,15 @@ struct SeqTiles {
     }
 };
 
+// Tiles of 256 tokens where the rows allow about 1,024 workgroups of `groups` to a tile, down to 64: longer ones
+// leave the chip idle, shorter ones spend on the chain what they gain (1 x 8,192 x 1,024: 86 us at 128, 92 at 64
+// and 256; 16,384 x 4,096: 470 at 256, 481 at 128, 552 at 64).
+inline void tile_for(SeqTiles &s, int64_t groups) {
+    int64_t L = (s.rows() * groups / 1024 + 15) / 16 * 16;
+    L = L < 64 ? 64 : L > 256 ? 256 : L;
+    if (L < s.T) s.L = static_cast<int>(L);
+}
+
 struct Tile {
     int n, k, count;      // sequence, tile within it, tiles of it (0: an empty sequence's only slot)
     int64_t begin;        // first row
@@ -100,30 +116,52 @@ __device__ __forceinline__ Tile find_tile(const SeqTiles &s, int64_t slot) {
     return t;
 }
 
-// One channel's column of a tile's rows, read or written four rows at a time by the lanes q = 0..3 of a quad:
-// a uniform address per group of four rows plus a 32-bit lane offset that stays the same, so that a step
-// costs scalar additions only.  Strides are at most 2^27 elements, which keeps 3 rows inside 32 bits.
-struct QuadColumn {
-    char *at;           // the tile's first row
-    int64_t step;       // bytes per row
-    uint32_t off, tail; // lane offset; the same in a last group of fewer than four rows, held to its last row
-    __device__ __forceinline__ QuadColumn(const Rows &r, int64_t begin, int len, int ch, int q) {
-        const int e = r.bf16 ? 2 : 4, left = (len & 3) - 1;
-        at = static_cast<char *>(r.p) + begin * r.stride * e;
+// Where the four lanes q of a quad stand in a group of four rows, held to the tile's last row: a scalar row for the
+// group and a lane's distance from it.  Loads through it need no branch at a tile's end; what lies past the end
+// is masked where it is used.
+struct Group {
+    int row;
+    uint32_t lane;
+    __device__ __forceinline__ Group(int t, int len, int q) {
+        row = t < len ? t : len - 1;
+        const int left = len - 1 - row;
+        lane = q < left ? q : left;
+    }
+};
+// One channel's column of a tile: a uniform address per group of rows and a 32-bit lane offset, one 24-bit
+// multiply-add.  Strides are below 2^22 elements, which keeps a row's bytes within 24 bits.
+struct Column {
+    char *at;      // the tile's first row
+    int64_t step;  // bytes per row
+    uint32_t ch;   // the channel's byte in a row
+    __device__ __forceinline__ Column(const Rows &r, int64_t row, int c) {
+        const int e = r.bf16 ? 2 : 4;
+        at = static_cast<char *>(r.p) + row * r.stride * e;
         step = r.stride * e;
-        off = (static_cast<uint32_t>(q) * static_cast<uint32_t>(r.stride) + static_cast<uint32_t>(ch)) * e;
-        const int qt = left >= 0 && q > left ? left : q;
-        tail = (static_cast<uint32_t>(qt) * static_cast<uint32_t>(r.stride) + static_cast<uint32_t>(ch)) * e;
+        ch = static_cast<uint32_t>(c) * e;
     }
-    // the group of rows t .. t + 3 of the tile; whole: all four exist
+    __device__ __forceinline__ char *of(const Group &g) const {
+        return at + g.row * step + (__umul24(g.lane, static_cast<uint32_t>(step)) + ch);
+    }
     template <typename E>
-    __device__ __forceinline__ E get(int t, bool whole) const {
-        return *reinterpret_cast<const E *>(at + t * step + (whole ? off : tail));
+    __device__ __forceinline__ E get(const Group &g) const {
+        return *reinterpret_cast<const E *>(of(g));
     }
-    __device__ __forceinline__ void put(int t, int bf16, float x) const {
-        char *p = at + t * step + off;
-        if (bf16) *reinterpret_cast<uint16_t *>(p) = f32_to_bf16(x);
-        else *reinterpret_cast<float *>(p) = x;
+    // one value of each of a block's J groups, masked by the tile's end
+    template <int J>
+    __device__ __forceinline__ void put(int t0, int len, int q, bool live, int bf16, const float (&x)[J]) const {
+        if (!live) return;
+        auto all = [&](auto bf) {
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                const Group g(t0 + 4 * j, len, q);
+                if (t0 + 4 * J > len && t0 + 4 * j + q >= len) continue;
+                if constexpr (decltype(bf)::value) *reinterpret_cast<uint16_t *>(of(g)) = to_bf16(x[j]);
+                else *reinterpret_cast<float *>(of(g)) = x[j];
+            }
+        };
+        if (bf16) all(std::true_type{});
+        else all(std::false_type{});
     }
 };
 
@@ -133,34 +171,42 @@ __device__ __forceinline__ float sigmoid_f(float x) {
     return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-kLog2e * x));
 }
 
-// softplus(x) = max(x, 0) + log1p(e), e = exp(-|x|) in (0, 1].  log1p(e) = 2 atanh(r), r = e / (2 + e) <= 1/3,
-// by atanh's series to r^13 (the next term is below 1e-8 of the value): small e keep their relative precision,
-// which 1 + e would round away.
+// softplus(x) = max(x, 0) + log1p(e), e = exp(-|x|) in (0, 1].  log1p(e) is log(s), s = fl(1 + e), plus what the
+// rounding of s left out, e - (s - 1) (exact; its 1 / s is below half a rounding): small e keep their relative
+// precision, 2e-7 measured over 2^-30 .. 1, at half the cost of atanh's series.
 __device__ __forceinline__ float softplus_f(float x) {
-    const float e = __builtin_amdgcn_exp2f(-kLog2e * fabsf(x));
-    const float r = e * __builtin_amdgcn_rcpf(2.f + e), q = r * r;
-    float s = 1.f / 13.f;
-    s = fmaf(s, q, 1.f / 11.f);
-    s = fmaf(s, q, 1.f / 9.f);
-    s = fmaf(s, q, 1.f / 7.f);
-    s = fmaf(s, q, 1.f / 5.f);
-    s = fmaf(s, q, 1.f / 3.f);
-    s = fmaf(s, q, 1.f);
-    return fmaxf(x, 0.f) + 2.f * r * s;
+    const float e = __builtin_amdgcn_exp2f(-kLog2e * fabsf(x)), s = 1.f + e;
+    return fmaxf(x, 0.f) + fmaf(__builtin_amdgcn_logf(s), 0.6931471805599453f, e - (s - 1.f));
 }
 
 // A value of lane I of each quad, in all four lanes.
 template <int I>
-__device__ __forceinline__ float quad_bcast(float x) {
+__device__ __forceinline__ float lane_bcast(float x) {
     return dpp_mov<I * 0x55>(x);
 }
 // Lane q of each quad gets the quad's sum of v[q].
-__device__ __forceinline__ float quad_transpose_sum(float v0, float v1, float v2, float v3, int q) {
+__device__ __forceinline__ float transpose_sum(const float (&v)[4], int q) {
     const bool b0 = q & 1, b1 = q & 2;
-    const float r01 = (b0 ? v1 : v0) + dpp_mov<0xB1>(b0 ? v0 : v1);
-    const float r23 = (b0 ? v3 : v2) + dpp_mov<0xB1>(b0 ? v2 : v3);
+    const float r01 = (b0 ? v[1] : v[0]) + dpp_mov<0xB1>(b0 ? v[0] : v[1]);
+    const float r23 = (b0 ? v[3] : v[2]) + dpp_mov<0xB1>(b0 ? v[2] : v[3]);
     return (b1 ? r23 : r01) + dpp_mov<0x4E>(b1 ? r01 : r23);
 }
+// Sums over the 16 quads of a wave (the lanes that hold the same states of different channels) of four values.
+// permlane swaps sum pairs of values over halves and rows at once: row k of 16 lanes ends with value
+// quads_sum4_value, which two rotations sum within the row; every lane of the row has the result.
+__device__ __forceinline__ float swap_add(float a, float b, bool rows) {
+    typedef unsigned u2 __attribute__((ext_vector_type(2)));
+    const u2 r = rows ? __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(b), false, false)
+                      : __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+__device__ __forceinline__ float quads_sum4(float v0, float v1, float v2, float v3) {
+    float x = swap_add(swap_add(v0, v1, false), swap_add(v2, v3, false), true);
+    x += dpp_mov<0x124>(x);         // row rotate by 4
+    return x + dpp_mov<0x128>(x);   // by 8
+}
+// which of the four values a lane ends with: rows 0, 1, 2, 3 hold values 0, 2, 1, 3
+__device__ __forceinline__ int quads_sum4_value(int lane) { return ((lane >> 5) & 1) | ((lane >> 3) & 2); }
 
 // ---- launch structs ------------------------------------------------------------------------------------
 

@@ -65,7 +65,7 @@ kda_status check_overlaps(const Span (&ins)[NI], const Span (&outs)[NO]) {
 }
 
 kda_status check_stride(const char *name, const void *p, int64_t stride, int64_t width, int64_t rows) {
-    if (p && (stride < width || stride > (int64_t{1} << 27) || stride > (int64_t{1} << 40) / (rows > 0 ? rows : 1)))
+    if (p && (stride < width || stride >= (int64_t{1} << 22) || stride > (int64_t{1} << 40) / (rows > 0 ? rows : 1)))
         return fail(KDA_ERR_BAD_SHAPE, "%s: stride %lld for rows of %lld", name, static_cast<long long>(stride),
                     static_cast<long long>(width));
     return KDA_OK;
@@ -92,6 +92,7 @@ kda_status check_batch(const A *a) {
     if (rows > INT32_MAX) return fail(KDA_ERR_BAD_SHAPE, "%lld rows (at most %d)", static_cast<long long>(rows), INT32_MAX);
     if (rows * a->dim > (int64_t{1} << 40) || static_cast<int64_t>(a->num_seqs) * a->dim > (int64_t{1} << 32))
         return fail(KDA_ERR_BAD_SHAPE, "problem too large");
+    if (a->dim >= 1 << 22) return fail(KDA_ERR_UNSUPPORTED, "dim=%d (below 2^22)", a->dim);
     if (a->num_seqs > 65535) return fail(KDA_ERR_UNSUPPORTED, "num_seqs=%d (at most 65535)", a->num_seqs);
     return KDA_OK;
 }

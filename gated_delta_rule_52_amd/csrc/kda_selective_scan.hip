@@ -23,7 +23,7 @@ namespace kda {
 
 namespace {
 
-constexpr int kScanBlock = 16;     // tokens per LDS block
+constexpr int LPC = 4;             // lanes per channel
 constexpr int kScanChannels = 64;  // channels per workgroup of 256
 
 template <bool InBf16>
@@ -45,18 +45,21 @@ __host__ __device__ inline FwdSpace fwd_space(float *ws, const SeqTiles &seq, in
 
 enum { kOutputs, kLocal };
 
-template <int MODE, int R, bool InBf16>
+// LPC lanes per channel with R states each; tokens in groups of LPC, one per lane.  Two lanes and one were slower
+// at every size (16,384 x 4,096: 536 and 695 us against 497), four give the most waves.
+template <int MODE, int R, bool InBf16, bool GATED>
 __global__ void __launch_bounds__(256) scan_kernel(ScanFwdLaunch P) {
     using E = typename Raw<InBf16>::T;
-    constexpr int NS = 4 * R, kSt = kScanBlock * NS / 256;  // staged values per thread
-    __shared__ __attribute__((aligned(16))) float sB[2][kScanBlock][NS], sC[MODE == kLocal ? 1 : 2][kScanBlock][NS];
+    constexpr int NS = LPC * R, kTok = 16, J = kTok / LPC;  // tokens per block, per lane of it
+    constexpr int kSt = kTok * NS / 256;                    // staged values per thread
+    __shared__ __attribute__((aligned(16))) float sB[2][kTok][NS], sC[MODE == kLocal ? 1 : 2][kTok][NS];
 
     const int groups = (P.dim + kScanChannels - 1) / kScanChannels;
     const int64_t slot = blockIdx.x / groups;
     const Tile tl = find_tile(P.seq, slot);
     if (!tl.valid || (MODE == kLocal && tl.last())) return;  // nothing follows a last tile
-    const int lane = threadIdx.x & 63, q = lane & 3;
-    const int ch = static_cast<int>(blockIdx.x % groups) * kScanChannels + (threadIdx.x >> 2);
+    const int q = threadIdx.x % LPC;
+    const int ch = static_cast<int>(blockIdx.x % groups) * kScanChannels + threadIdx.x / LPC;
     const bool live = ch < P.dim;
     const int chc = live ? ch : P.dim - 1;
     const FwdSpace W = fwd_space(P.ws, P.seq, P.dim, P.ds);
@@ -74,69 +77,74 @@ __global__ void __launch_bounds__(256) scan_kernel(ScanFwdLaunch P) {
         h[r] = in && from ? from[r] : 0.f;
     }
     const float skip = P.D ? P.D[chc] : 0.f, bias = P.dt_bias ? P.dt_bias[chc] : 0.f;
-    const bool gated = MODE == kOutputs && P.z.p;
 
-    const QuadColumn cu(P.u, tl.begin, tl.len, chc, q), cd(P.dt, tl.begin, tl.len, chc, q);
-    const QuadColumn cz(P.z, tl.begin, tl.len, chc, q), cy(P.y, tl.begin, tl.len, chc, q);
+    const Column cu(P.u, tl.begin, chc), cd(P.dt, tl.begin, chc), cz(P.z, tl.begin, chc), cy(P.y, tl.begin, chc);
     const E *Bp = static_cast<const E *>(P.B.p) + tl.begin * P.B.stride;
     const E *Cp = static_cast<const E *>(P.C.p) + tl.begin * P.C.stride;
-    E ru[4] = {}, rdt[4] = {}, rz[4] = {}, rB[kSt], rC[kSt];
+    E ru[J], rdt[J], rz[J], rB[kSt], rC[kSt];
     auto fetch = [&](int t0) {  // the block at t0 of the tile, into registers
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int t = t0 + 4 * j;
-            if (t >= tl.len) break;
-            const bool whole = t + 4 <= tl.len;
-            rdt[j] = cd.get<E>(t, whole);
-            ru[j] = cu.get<E>(t, whole);
-            if (gated) rz[j] = cz.get<E>(t, whole);
+        for (int j = 0; j < J; ++j) {
+            const Group g(t0 + LPC * j, tl.len, q);
+            rdt[j] = cd.get<E>(g);
+            ru[j] = cu.get<E>(g);
+            if (GATED) rz[j] = cz.get<E>(g);
         }
 #pragma unroll
         for (int i = 0; i < kSt; ++i) {
-            const int e = i * 256 + threadIdx.x, t = e / NS, n = e % NS;
-            rB[i] = rC[i] = 0;
-            if (t0 + t < tl.len && n < P.ds) {
-                rB[i] = (Bp + t0 * P.B.stride)[static_cast<uint32_t>(t) * static_cast<uint32_t>(P.B.stride) + n];
-                if (MODE == kOutputs)
-                    rC[i] = (Cp + t0 * P.C.stride)[static_cast<uint32_t>(t) * static_cast<uint32_t>(P.C.stride) + n];
-            }
+            const int e = i * 256 + threadIdx.x, n = e % NS < P.ds ? e % NS : P.ds - 1;
+            const int left = tl.len - 1 - t0, t = e / NS < left ? e / NS : left;
+            rB[i] = (Bp + t0 * P.B.stride)[static_cast<uint32_t>(t) * static_cast<uint32_t>(P.B.stride) + n];
+            if (MODE == kOutputs)
+                rC[i] = (Cp + t0 * P.C.stride)[static_cast<uint32_t>(t) * static_cast<uint32_t>(P.C.stride) + n];
         }
     };
-    auto stage = [&](int buf) {
+    auto stage = [&](int t0, int buf) {
 #pragma unroll
         for (int i = 0; i < kSt; ++i) {
             const int e = i * 256 + threadIdx.x;
-            (&sB[buf][0][0])[e] = Raw<InBf16>::f(rB[i]);
-            if (MODE == kOutputs) (&sC[buf][0][0])[e] = Raw<InBf16>::f(rC[i]);
+            const bool in = t0 + e / NS < tl.len && e % NS < P.ds;
+            (&sB[buf][0][0])[e] = in ? Raw<InBf16>::f(rB[i]) : 0.f;
+            if (MODE == kOutputs) (&sC[buf][0][0])[e] = in ? Raw<InBf16>::f(rC[i]) : 0.f;
         }
     };
 
     float total = 0.f;  // of delta over this lane's tokens
     if (tl.len > 0) {
         fetch(0);
-        stage(0);
+        stage(0, 0);
         __syncthreads();
     }
-    for (int t0 = 0, buf = 0; t0 < tl.len; t0 += kScanBlock, buf ^= 1) {
-        float de[4], xs[4], us[4], zs[4];
+    for (int t0 = 0, buf = 0; t0 < tl.len; t0 += kTok, buf ^= 1) {
+        float de[J], xs[J], us[J], y[J] = {};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const bool in = t0 + 4 * j + q < tl.len;
-            const float d = Raw<InBf16>::f(rdt[j]) + bias;
-            us[j] = in ? Raw<InBf16>::f(ru[j]) : 0.f;
-            de[j] = in ? (P.softplus ? softplus_f(d) : d) : 0.f;
-            xs[j] = de[j] * us[j];
-            zs[j] = gated ? Raw<InBf16>::f(rz[j]) : 0.f;
+        for (int j = 0; j < J; ++j) de[j] = Raw<InBf16>::f(rdt[j]) + bias;
+        if (P.softplus) {
+#pragma unroll
+            for (int j = 0; j < J; ++j) de[j] = softplus_f(de[j]);
         }
-        if (MODE == kLocal) total += (de[0] + de[1]) + (de[2] + de[3]);
-        const bool more = t0 + kScanBlock < tl.len;
-        if (more) fetch(t0 + kScanBlock);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if (t0 + 4 * j >= tl.len) break;
-            float yp[4];
+        for (int j = 0; j < J; ++j) {
+            const bool in = t0 + LPC * j + q < tl.len;
+            de[j] = in ? de[j] : 0.f;
+            us[j] = in ? Raw<InBf16>::f(ru[j]) : 0.f;
+            xs[j] = de[j] * us[j];
+            if (GATED) {
+                const float z = Raw<InBf16>::f(rz[j]);
+                y[j] = z * sigmoid_f(z);
+            }
+            if (MODE == kLocal) total += de[j];
+        }
+        const bool more = t0 + kTok < tl.len;
+        if (more) fetch(t0 + kTok);
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            // Also ends the basic block: across it the scheduler pulls every token's lane moves and loads to the
+            // front of the unrolled block and pays in registers (134 against 56 in the local pass).
+            if (t0 + LPC * j >= tl.len) break;
+            float yp[LPC];
             auto token = [&](float dl, float xl, int i) {
-                const float *bt = &sB[buf][4 * j + i][q * R], *ct = &sC[MODE == kLocal ? 0 : buf][4 * j + i][q * R];
+                const float *bt = &sB[buf][LPC * j + i][q * R], *ct = &sC[MODE == kLocal ? 0 : buf][LPC * j + i][q * R];
                 float acc = 0.f;
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
@@ -145,17 +153,17 @@ __global__ void __launch_bounds__(256) scan_kernel(ScanFwdLaunch P) {
                 }
                 yp[i] = acc;
             };
-            token(quad_bcast<0>(de[j]), quad_bcast<0>(xs[j]), 0);
-            token(quad_bcast<1>(de[j]), quad_bcast<1>(xs[j]), 1);
-            token(quad_bcast<2>(de[j]), quad_bcast<2>(xs[j]), 2);
-            token(quad_bcast<3>(de[j]), quad_bcast<3>(xs[j]), 3);
+            token(lane_bcast<0>(de[j]), lane_bcast<0>(xs[j]), 0);
+            token(lane_bcast<1>(de[j]), lane_bcast<1>(xs[j]), 1);
+            token(lane_bcast<2>(de[j]), lane_bcast<2>(xs[j]), 2);
+            token(lane_bcast<3>(de[j]), lane_bcast<3>(xs[j]), 3);
             if (MODE == kOutputs) {
-                float y = fmaf(skip, us[j], quad_transpose_sum(yp[0], yp[1], yp[2], yp[3], q));
-                if (gated) y *= zs[j] * sigmoid_f(zs[j]);
-                if (live && t0 + 4 * j + q < tl.len) cy.put(t0 + 4 * j, P.y.bf16, y);
+                const float sum = fmaf(skip, us[j], transpose_sum(yp, q));
+                y[j] = GATED ? sum * y[j] : sum;
             }
         }
-        if (more) stage(buf ^ 1);
+        if (MODE == kOutputs) cy.put(t0, tl.len, q, live, P.y.bf16, y);
+        if (more) stage(t0 + kTok, buf ^ 1);
         __syncthreads();
     }
     if (MODE == kLocal) {
@@ -247,16 +255,13 @@ __global__ void __launch_bounds__(256) scan_step_kernel(ScanFwdLaunch P) {
 
 }  // namespace
 
+// Whole sequences where they fill the chip by themselves, one pass; else tiles, and a second pass over the inputs.
+// On MI355X, bf16: 8 x 1,024 x 4,096 (512 workgroups) 185 us whole and 240 tiled, 12 x 1,024 x 2,048 (384) 181
+// and 184, 8 x 2,048 x 2,048 (256) 275 and 252, 2 x 4,096 x 4,096 (128) 544 and 246.
 SeqTiles scan_fwd_tiles(const int32_t *cu, int N, int T, int dim, int ds) {
     SeqTiles s{cu, N, T, T > 0 ? T : 1};
     const int64_t groups = (dim + kScanChannels - 1) / kScanChannels;
-    constexpr int64_t kGroups = 1024;  // workgroups wanted: 4 waves per SIMD
-    // Whole sequences where they fill the chip by themselves; else tiles, and a second pass over the inputs.
-    if (!cu && N * groups >= kGroups / 2) return s;
-    int64_t L = (s.rows() * groups + kGroups - 1) / kGroups;
-    L = (L + kScanBlock - 1) / kScanBlock * kScanBlock;
-    if (L < 64) L = 64;
-    if (L < T) s.L = static_cast<int>(L);
+    if (cu || N * groups < 384) tile_for(s, groups);
     return s;
 }
 
@@ -267,28 +272,28 @@ size_t scan_fwd_workspace_bytes(const SeqTiles &seq, int dim, int ds) {
 }
 
 template <int R, bool InBf16>
-static void launch_passes(const ScanFwdLaunch &P, unsigned grid) {
+static void launch_passes(const ScanFwdLaunch &P) {
+    const unsigned grid = static_cast<unsigned>(P.seq.slots() * ((P.dim + kScanChannels - 1) / kScanChannels));
+    if (grid == 0) return;
     if (tiled(P.seq)) {
-        scan_kernel<kLocal, R, InBf16><<<grid, 256, 0, P.stream>>>(P);
+        scan_kernel<kLocal, R, InBf16, false><<<grid, 256, 0, P.stream>>>(P);
         const int64_t states = static_cast<int64_t>(P.dim) * P.ds;
         scan_combine_kernel<<<dim3(static_cast<unsigned>((states + 255) / 256), P.seq.N), 256, 0, P.stream>>>(P);
     }
-    scan_kernel<kOutputs, R, InBf16><<<grid, 256, 0, P.stream>>>(P);
+    if (P.z.p) scan_kernel<kOutputs, R, InBf16, true><<<grid, 256, 0, P.stream>>>(P);
+    else scan_kernel<kOutputs, R, InBf16, false><<<grid, 256, 0, P.stream>>>(P);
 }
 
 template <bool InBf16>
-static void launch_main(const ScanFwdLaunch &P, unsigned grid) {
-    if (P.ds <= 16) launch_passes<4, InBf16>(P, grid);
-    else if (P.ds <= 32) launch_passes<8, InBf16>(P, grid);
-    else launch_passes<16, InBf16>(P, grid);
+static void launch_main(const ScanFwdLaunch &P) {
+    if (P.ds <= 16) launch_passes<4, InBf16>(P);
+    else if (P.ds <= 32) launch_passes<8, InBf16>(P);
+    else launch_passes<16, InBf16>(P);
 }
 
 hipError_t launch_scan_fwd(const ScanFwdLaunch &P) {
-    const int groups = (P.dim + kScanChannels - 1) / kScanChannels;
-    const unsigned grid = static_cast<unsigned>(P.seq.slots() * groups);
-    if (grid == 0) return hipSuccess;
-    if (P.u.bf16) launch_main<true>(P, grid);
-    else launch_main<false>(P, grid);
+    if (P.u.bf16) launch_main<true>(P);
+    else launch_main<false>(P);
     return hipGetLastError();
 }
 

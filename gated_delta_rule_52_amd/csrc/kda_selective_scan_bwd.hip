@@ -5,9 +5,10 @@
 //     ddelta = u P + sum_n A G c,  dA = sum_t delta G c,       c_t = exp(delta_t A) h_{t-1}
 // (c is kept from the recomputed forward step; taking it as h - delta u B would cancel).
 //
-// Passes: scan_states_kernel walks each tile forwards and stores the state every kCkpt tokens; the gradient
-// kernel takes the blocks of kCkpt tokens in reverse, recomputes a block's states from its stored one into
-// registers and walks it backwards.  dB and dC sum over channels: in the wave, then over the workgroup's
+// Passes: scan_states_kernel walks each tile forwards and stores the state every 8 tokens; the gradient
+// kernel takes the blocks of 8 tokens in reverse, recomputes a block's states from its stored one into
+// registers and walks it backwards.  Sequences too few to fill the chip are cut into tiles, which a combine
+// chains both ways.  dB and dC sum over channels: in the wave, then over the workgroup's
 // waves in LDS, then over workgroups by a last kernel, always in the same order.  Parameter gradients leave
 // one partial per tile, summed by the column sum.
 #include <type_traits>
@@ -30,11 +31,15 @@ struct Raw {
 
 // Workspace, in floats.
 struct BwdSpace {
-    float *ck;  // [block][dim][ds] states entering each block of tokens; block = row / ckpt + slot + index
-    float *pA;  // [slot][dim][ds]
-    float *pD;  // [slot][dim]
-    float *pb;  // [slot][dim]
-    float *pBC; // [channel group][rows][2][ds]
+    float *ck;   // [block][dim][4 R] states entering each block of tokens, from the tile's start; block = row / ckpt + slot + index
+    float *cum;  // [block][dim] sum of delta from the tile's start to the block
+    float *H;    // [slot][dim][ds] state a tile reaches from zero, then the one it starts from
+    float *G;    // [slot][dim][ds] state gradient at a tile's start from its own outputs, then the one behind its end
+    float *sum;  // [slot][dim] sum of delta over a tile
+    float *pA;   // [slot][dim][ds]
+    float *pD;   // [slot][dim]
+    float *pb;   // [slot][dim]
+    float *pBC;  // [channel group][rows][2][ds]
     int64_t bytes;
 };
 
@@ -44,61 +49,90 @@ __device__ __forceinline__ int64_t first_block(const Tile &t, int64_t slot) {
     return t.begin / ckpt_of(R) + slot;
 }
 
-template <int R, bool InBf16>
+// One walk over a tile: states at every block, and for sequences of several tiles what the two chains need,
+// the state reached from zero and the gradient that the tile's outputs send to its start,
+//     sum_t (prod_{s <= t} a_s) C_t gp_t,
+// which the forward order gives with a running product.
+template <int R, bool InBf16, bool TILED, bool GATED>
 __global__ void __launch_bounds__(256) scan_states_kernel(ScanBwdLaunch P, BwdSpace W) {
     using E = typename Raw<InBf16>::T;
     constexpr int NS = 4 * R, kSt = kBlock * NS / 256, kCkpt = ckpt_of(R);
-    __shared__ __attribute__((aligned(16))) float sB[2][kBlock][NS];
+    __shared__ __attribute__((aligned(16))) float sB[2][kBlock][NS], sC[TILED ? 2 : 1][kBlock][NS];
     const int groups = (P.dim + 63) / 64;
     const int64_t slot = blockIdx.x / groups;
     const Tile tl = find_tile(P.seq, slot);
     if (!tl.valid || tl.len <= 0) return;
     const int q = threadIdx.x & 3;
     const int ch = static_cast<int>(blockIdx.x % groups) * 64 + (threadIdx.x >> 2);
-    const bool live = ch < P.dim;
+    const bool live = ch < P.dim, chained = TILED && tl.count > 1;
     const int chc = live ? ch : P.dim - 1;
-    float A2[R], h[R];
+    float A2[R], h[R], prod[R], acc[R];
     const int64_t sbase = (static_cast<int64_t>(tl.n) * P.dim + chc) * P.ds + q * R;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         const bool in = q * R + r < P.ds;
         A2[r] = in ? kLog2e * P.A[static_cast<int64_t>(chc) * P.ds + q * R + r] : 0.f;
-        h[r] = in && P.h0 ? P.h0[sbase + r] : 0.f;
+        h[r] = in && P.h0 && !chained ? P.h0[sbase + r] : 0.f;
+        prod[r] = 1.f;
+        acc[r] = 0.f;
     }
     const float bias = P.dt_bias ? P.dt_bias[chc] : 0.f;
-    const E *u = static_cast<const E *>(P.u.p), *dt = static_cast<const E *>(P.dt.p);
-    const E *Bp = static_cast<const E *>(P.B.p);
-    E ru[4], rdt[4], rB[kSt];
+    const Column cu(P.u, tl.begin, chc), cd(P.dt, tl.begin, chc), cz(P.z, tl.begin, chc), cg(P.gy, tl.begin, chc);
+    const E *Bp = static_cast<const E *>(P.B.p) + tl.begin * P.B.stride;
+    const E *Cp = static_cast<const E *>(P.C.p) + tl.begin * P.C.stride;
+    E ru[4], rdt[4], rz[4], rg[4], rB[kSt], rC[kSt];
     auto fetch = [&](int t0) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int t = t0 + 4 * j + q;
-            const int64_t row = tl.begin + (t < tl.len ? t : tl.len - 1);
-            rdt[j] = dt[row * P.dt.stride + chc];
-            ru[j] = u[row * P.u.stride + chc];
+            const Group g(t0 + 4 * j, tl.len, q);
+            rdt[j] = cd.get<E>(g);
+            ru[j] = cu.get<E>(g);
+            if (TILED) rg[j] = cg.get<E>(g);
+            if (TILED && GATED) rz[j] = cz.get<E>(g);
         }
 #pragma unroll
         for (int i = 0; i < kSt; ++i) {
-            const int e = i * 256 + threadIdx.x, t = t0 + e / NS, n = e % NS;
-            rB[i] = t < tl.len && n < P.ds ? Bp[(tl.begin + t) * P.B.stride + n] : static_cast<E>(0);
+            const int e = i * 256 + threadIdx.x, n = e % NS < P.ds ? e % NS : P.ds - 1;
+            const int left = tl.len - 1 - t0, t = e / NS < left ? e / NS : left;
+            rB[i] = (Bp + t0 * P.B.stride)[static_cast<uint32_t>(t) * static_cast<uint32_t>(P.B.stride) + n];
+            if (TILED) rC[i] = (Cp + t0 * P.C.stride)[static_cast<uint32_t>(t) * static_cast<uint32_t>(P.C.stride) + n];
         }
     };
-    auto stage = [&](int buf) {
+    auto stage = [&](int t0, int buf) {
 #pragma unroll
-        for (int i = 0; i < kSt; ++i) (&sB[buf][0][0])[i * 256 + threadIdx.x] = Raw<InBf16>::f(rB[i]);
+        for (int i = 0; i < kSt; ++i) {
+            const int e = i * 256 + threadIdx.x;
+            const bool in = t0 + e / NS < tl.len && e % NS < P.ds;
+            (&sB[buf][0][0])[e] = in ? Raw<InBf16>::f(rB[i]) : 0.f;
+            if (TILED) (&sC[buf][0][0])[e] = in ? Raw<InBf16>::f(rC[i]) : 0.f;
+        }
     };
     fetch(0);
-    stage(0);
+    stage(0, 0);
     __syncthreads();
-    float *ck = W.ck + (first_block<R>(tl, slot) * P.dim + chc) * P.ds + q * R;
+    int64_t at = first_block<R>(tl, slot) * P.dim + chc;
+    float total = 0.f;
     for (int t0 = 0, buf = 0; t0 < tl.len; t0 += kBlock, buf ^= 1) {
-        float de[4], xs[4];
+        float de[4], xs[4], gp[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) de[j] = Raw<InBf16>::f(rdt[j]) + bias;
+        if (P.softplus) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) de[j] = softplus_f(de[j]);
+        }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const bool in = t0 + 4 * j + q < tl.len;
-            const float d = Raw<InBf16>::f(rdt[j]) + bias;
-            de[j] = in ? (P.softplus ? softplus_f(d) : d) : 0.f;
+            de[j] = in ? de[j] : 0.f;
             xs[j] = in ? de[j] * Raw<InBf16>::f(ru[j]) : 0.f;
+            if (TILED) {
+                gp[j] = Raw<InBf16>::f(rg[j]);
+                if (GATED) {
+                    const float z = Raw<InBf16>::f(rz[j]);
+                    gp[j] *= z * sigmoid_f(z);
+                }
+                gp[j] = in ? gp[j] : 0.f;
+            }
         }
         const bool more = t0 + kBlock < tl.len;
         if (more) fetch(t0 + kBlock);
@@ -107,198 +141,267 @@ __global__ void __launch_bounds__(256) scan_states_kernel(ScanBwdLaunch P, BwdSp
             if (t0 + 4 * j >= tl.len) break;
             if (j % (kCkpt / 4) == 0) {
                 if (live) {
+                    float4 *c = reinterpret_cast<float4 *>(W.ck + at * NS + q * R);
 #pragma unroll
-                    for (int r = 0; r < R; ++r)
-                        if (q * R + r < P.ds) ck[r] = h[r];
+                    for (int r = 0; r < R; r += 4) c[r / 4] = make_float4(h[r], h[r + 1], h[r + 2], h[r + 3]);
                 }
-                ck += static_cast<int64_t>(P.dim) * P.ds;
+                if (TILED) {
+                    const float before = quad_sum(total);
+                    if (live && q == 0) W.cum[at] = before;
+                }
+                at += P.dim;
             }
-            auto token = [&](float dl, float xl, int i) {
-                const float *bt = &sB[buf][4 * j + i][q * R];
+            if (TILED) total += de[j];
+            auto token = [&](float dl, float xl, float g, int i) {
+                const float *bt = &sB[buf][4 * j + i][q * R], *ct = &sC[TILED ? buf : 0][4 * j + i][q * R];
 #pragma unroll
-                for (int r = 0; r < R; ++r)
-                    h[r] = fmaf(__builtin_amdgcn_exp2f(dl * A2[r]), h[r], xl * bt[r]);
+                for (int r = 0; r < R; ++r) {
+                    const float a = __builtin_amdgcn_exp2f(dl * A2[r]);
+                    h[r] = fmaf(a, h[r], xl * bt[r]);
+                    if (TILED) {
+                        prod[r] *= a;
+                        acc[r] = fmaf(prod[r], ct[r] * g, acc[r]);
+                    }
+                }
             };
-            token(quad_bcast<0>(de[j]), quad_bcast<0>(xs[j]), 0);
-            token(quad_bcast<1>(de[j]), quad_bcast<1>(xs[j]), 1);
-            token(quad_bcast<2>(de[j]), quad_bcast<2>(xs[j]), 2);
-            token(quad_bcast<3>(de[j]), quad_bcast<3>(xs[j]), 3);
+            token(lane_bcast<0>(de[j]), lane_bcast<0>(xs[j]), lane_bcast<0>(TILED ? gp[j] : 0.f), 0);
+            token(lane_bcast<1>(de[j]), lane_bcast<1>(xs[j]), lane_bcast<1>(TILED ? gp[j] : 0.f), 1);
+            token(lane_bcast<2>(de[j]), lane_bcast<2>(xs[j]), lane_bcast<2>(TILED ? gp[j] : 0.f), 2);
+            token(lane_bcast<3>(de[j]), lane_bcast<3>(xs[j]), lane_bcast<3>(TILED ? gp[j] : 0.f), 3);
         }
-        if (more) stage(buf ^ 1);
+        if (more) stage(t0 + kBlock, buf ^ 1);
         __syncthreads();
+    }
+    if (chained) {
+        total = quad_sum(total);
+        const int64_t w = slot * P.dim + chc;
+        if (live) {
+            if (q == 0) W.sum[w] = total;
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                if (q * R + r < P.ds) {
+                    W.H[w * P.ds + q * R + r] = h[r];
+                    W.G[w * P.ds + q * R + r] = acc[r];
+                }
+        }
     }
 }
 
-// Sum over the 16 lanes of a wave that hold the same states of different channels (lane = 4 c + q).
-__device__ __forceinline__ float channel_sum(float x) {
-    x += dpp_mov<0x124>(x);  // row rotate by 4
-    x += dpp_mov<0x128>(x);  // row rotate by 8
-    x += __shfl_xor(x, 16, kWave);
-    return x + __shfl_xor(x, 32, kWave);
+// Chains the tiles of every sequence that has several, both ways: H becomes the state each tile starts from,
+// G the gradient of the state each tile leaves.
+__global__ void __launch_bounds__(256) scan_bwd_combine_kernel(ScanBwdLaunch P, BwdSpace W) {
+    const int n = blockIdx.y;
+    const int64_t e = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x, states = static_cast<int64_t>(P.dim) * P.ds;
+    int64_t start;
+    int len;
+    P.seq.sequence(n, start, len);
+    const int count = (len + P.seq.L - 1) / P.seq.L;
+    if (e >= states || count <= 1) return;
+    const int64_t first = P.seq.first_slot(n, start);
+    const float A2 = kLog2e * P.A[e];
+    float ahead = P.h0 ? P.h0[n * states + e] : 0.f, back = P.dhT ? P.dhT[n * states + e] : 0.f;
+    float *H = W.H + first * states + e, *G = W.G + first * states + e;
+    const float *sum = W.sum + first * P.dim + static_cast<int>(e / P.ds);
+    constexpr int U = 4;  // tiles in flight: their loads do not wait for the chains
+    for (int k = 0; k < count; k += U) {
+        float h[U], g[U], dh[U], dg[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const bool in = k + i < count;
+            const int64_t f = k + i, b = count - 1 - f;
+            h[i] = in ? H[f * states] : 0.f;
+            g[i] = in ? G[b * states] : 0.f;
+            dh[i] = in ? sum[f * P.dim] : 0.f;
+            dg[i] = in ? sum[b * P.dim] : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            if (k + i >= count) break;
+            H[(k + i) * states] = ahead;
+            ahead = fmaf(__builtin_amdgcn_exp2f(A2 * dh[i]), ahead, h[i]);
+            G[(count - 1 - k - i) * states] = back;
+            back = fmaf(__builtin_amdgcn_exp2f(A2 * dg[i]), back, g[i]);
+        }
+    }
 }
 
-// M channels per quad: a wave holds 16 M channels (c, c + 16, ...), a workgroup 64 M.
-template <int R, int M, bool InBf16>
+template <int R, bool InBf16, bool TILED, bool GATED>
 __global__ void __launch_bounds__(256) scan_grad_kernel(ScanBwdLaunch P, BwdSpace W) {
     using E = typename Raw<InBf16>::T;
-    constexpr int kCkpt = ckpt_of(R), NS = 4 * R, J = kCkpt / 4, kSt = (kCkpt * NS + 255) / 256;
-    __shared__ __attribute__((aligned(16))) float sB[2][kCkpt][NS], sC[2][kCkpt][NS];
+    constexpr int kCkpt = ckpt_of(R), NS = 4 * R, J = kCkpt / 4, kSt = 2 * kCkpt * NS / 256;
+    static_assert(R % 4 == 0, "the channel sums take four states at a time");
+    static_assert(2 * kCkpt * NS % 256 == 0, "staging");
+    __shared__ __attribute__((aligned(16))) float sBC[2][2][kCkpt][NS];
     __shared__ float sR[2][4][kCkpt][2 * NS];  // per wave: dB, dC of each token
-    const int groups = (P.dim + 64 * M - 1) / (64 * M);
+    const int groups = (P.dim + 63) / 64;
     const int64_t slot = blockIdx.x / groups;
     const int group = static_cast<int>(blockIdx.x % groups);
     const Tile tl = find_tile(P.seq, slot);
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, q = lane & 3;
-    int chn[M], chc[M];
-    bool live[M];
-#pragma unroll
-    for (int m = 0; m < M; ++m) {
-        chn[m] = group * 64 * M + wave * 16 * M + 16 * m + (lane >> 2);
-        live[m] = chn[m] < P.dim;
-        chc[m] = live[m] ? chn[m] : P.dim - 1;
-    }
-    float A2[M][R], G[M][R], dA[M][R], skip[M], bias[M], dD[M], db[M];
-#pragma unroll
-    for (int m = 0; m < M; ++m) {
-        skip[m] = P.D ? P.D[chc[m]] : 0.f;
-        bias[m] = P.dt_bias ? P.dt_bias[chc[m]] : 0.f;
-        dD[m] = db[m] = 0.f;
-        const int64_t sb = (static_cast<int64_t>(tl.n) * P.dim + chc[m]) * P.ds + q * R;
+    const int ch = group * 64 + (threadIdx.x >> 2);
+    const bool chained = TILED && tl.count > 1, live = ch < P.dim;
+    const int chc = live ? ch : P.dim - 1;
+    float A2[R], G[R], from[R], dA[R], dD = 0.f, db = 0.f;
+    const float skip = P.D ? P.D[chc] : 0.f, bias = P.dt_bias ? P.dt_bias[chc] : 0.f;
+    {
+        const int64_t sb = (static_cast<int64_t>(tl.n) * P.dim + chc) * P.ds + q * R;
+        const int64_t wb = (slot * P.dim + chc) * P.ds + q * R;
+        const float *g = !tl.valid ? nullptr : chained ? W.G + wb : P.dhT ? P.dhT + sb : nullptr;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             const bool in = q * R + r < P.ds;
-            A2[m][r] = in ? kLog2e * P.A[static_cast<int64_t>(chc[m]) * P.ds + q * R + r] : 0.f;
-            G[m][r] = in && tl.valid && P.dhT ? P.dhT[sb + r] : 0.f;
-            dA[m][r] = 0.f;
+            A2[r] = in ? kLog2e * P.A[static_cast<int64_t>(chc) * P.ds + q * R + r] : 0.f;
+            G[r] = in && g ? g[r] : 0.f;
+            from[r] = in && chained && tl.valid ? W.H[wb + r] : 0.f;
+            dA[r] = 0.f;
         }
     }
     if (tl.valid && tl.len > 0) {
-        const E *u = static_cast<const E *>(P.u.p), *dt = static_cast<const E *>(P.dt.p);
-        const E *z = static_cast<const E *>(P.z.p), *gy = static_cast<const E *>(P.gy.p);
-        const E *Bp = static_cast<const E *>(P.B.p), *Cp = static_cast<const E *>(P.C.p);
-        E ru[M][J], rdt[M][J], rz[M][J], rg[M][J], rB[kSt], rC[kSt];
-        float ck[M][R];
         const int blocks = (tl.len + kCkpt - 1) / kCkpt;
+        const Column cu(P.u, tl.begin, chc), cd(P.dt, tl.begin, chc), cz(P.z, tl.begin, chc), cg(P.gy, tl.begin, chc);
+        const Column ou(P.du, tl.begin, chc), od(P.ddt, tl.begin, chc), oz(P.dz, tl.begin, chc);
+        const E *Bp = static_cast<const E *>(P.B.p) + tl.begin * P.B.stride;
+        const E *Cp = static_cast<const E *>(P.C.p) + tl.begin * P.C.stride;
+        E ru[J], rdt[J], rz[J], rg[J], rBC[kSt];
+        float4 ck[R / 4];
+        float cum = 0.f;
+        // a thread stages B or C of one token and state
+        const E *half[kSt];
+        uint32_t halfstep[kSt];
+#pragma unroll
+        for (int i = 0; i < kSt; ++i) {
+            const bool second = i * 256 + threadIdx.x >= kCkpt * NS;
+            const int n = (i * 256 + threadIdx.x) % NS;
+            half[i] = (second ? Cp : Bp) + (n < P.ds ? n : P.ds - 1);
+            halfstep[i] = static_cast<uint32_t>(second ? P.C.stride : P.B.stride);
+        }
         auto fetch = [&](int b) {
+            const int t0 = b * kCkpt;
 #pragma unroll
-            for (int m = 0; m < M; ++m) {
-#pragma unroll
-                for (int j = 0; j < J; ++j) {
-                    const int t = b * kCkpt + 4 * j + q;
-                    const int64_t row = tl.begin + (t < tl.len ? t : tl.len - 1);
-                    rdt[m][j] = dt[row * P.dt.stride + chc[m]];
-                    ru[m][j] = u[row * P.u.stride + chc[m]];
-                    rg[m][j] = gy[row * P.gy.stride + chc[m]];
-                    if (z) rz[m][j] = z[row * P.z.stride + chc[m]];
-                }
-                const float *c = W.ck + ((first_block<R>(tl, slot) + b) * P.dim + chc[m]) * P.ds + q * R;
-#pragma unroll
-                for (int r = 0; r < R; ++r) ck[m][r] = q * R + r < P.ds ? c[r] : 0.f;
+            for (int j = 0; j < J; ++j) {
+                const Group g(t0 + 4 * j, tl.len, q);
+                rdt[j] = cd.get<E>(g);
+                ru[j] = cu.get<E>(g);
+                rg[j] = cg.get<E>(g);
+                if (GATED) rz[j] = cz.get<E>(g);
             }
+            const int64_t at = (first_block<R>(tl, slot) + b) * P.dim;
+            const float4 *c = reinterpret_cast<const float4 *>(W.ck + at * NS) + (static_cast<uint32_t>(chc) * NS + q * R) / 4;
+#pragma unroll
+            for (int r = 0; r < R / 4; ++r) ck[r] = c[r];
+            if (TILED) cum = (W.cum + at)[static_cast<uint32_t>(chc)];
 #pragma unroll
             for (int i = 0; i < kSt; ++i) {
-                const int e = i * 256 + threadIdx.x, t = b * kCkpt + e / NS, n = e % NS;
-                rB[i] = rC[i] = 0;
-                if (e < kCkpt * NS && t < tl.len && n < P.ds) {
-                    rB[i] = Bp[(tl.begin + t) * P.B.stride + n];
-                    rC[i] = Cp[(tl.begin + t) * P.C.stride + n];
-                }
+                const int left = tl.len - 1, row = t0 + (i * 256 + static_cast<int>(threadIdx.x)) / NS % kCkpt;
+                rBC[i] = half[i][static_cast<int64_t>(row < left ? row : left) * halfstep[i]];
             }
         };
-        auto stage = [&](int buf) {
+        auto stage = [&](int b, int buf) {
 #pragma unroll
             for (int i = 0; i < kSt; ++i) {
                 const int e = i * 256 + threadIdx.x;
-                if (e < kCkpt * NS) {
-                    (&sB[buf][0][0])[e] = Raw<InBf16>::f(rB[i]);
-                    (&sC[buf][0][0])[e] = Raw<InBf16>::f(rC[i]);
-                }
+                const bool in = b * kCkpt + e / NS % kCkpt < tl.len && e % NS < P.ds;
+                (&sBC[buf][0][0][0])[e] = in ? Raw<InBf16>::f(rBC[i]) : 0.f;
             }
         };
         fetch(blocks - 1);
-        stage(0);
+        stage(blocks - 1, 0);
         __syncthreads();
         int buf = 0;
+        const int mine = quads_sum4_value(lane);  // which of four states this lane's row sums
+        float *pBC = W.pBC + (static_cast<int64_t>(group) * P.seq.rows() + tl.begin) * 2 * P.ds;
         for (int b = blocks - 1; b >= 0; --b, buf ^= 1) {
-            float de[M][J], sl[M][J], us[M][J], xs[M][J], gp[M][J], gv[M][J], zs[M][J], h[M][R];
+            float de[J], sl[J], us[J], xs[J], gp[J], gv[J], h[R], yv[J], gu[J], gd[J];
 #pragma unroll
-            for (int m = 0; m < M; ++m) {
+            for (int j = 0; j < J; ++j) {
+                de[j] = Raw<InBf16>::f(rdt[j]) + bias;
+                sl[j] = 1.f;
+            }
+            if (P.softplus) {
 #pragma unroll
                 for (int j = 0; j < J; ++j) {
-                    const bool in = live[m] && b * kCkpt + 4 * j + q < tl.len;
-                    const float d = Raw<InBf16>::f(rdt[m][j]) + bias[m];
-                    de[m][j] = in ? (P.softplus ? softplus_f(d) : d) : 0.f;
-                    sl[m][j] = P.softplus ? sigmoid_f(d) : 1.f;
-                    us[m][j] = in ? Raw<InBf16>::f(ru[m][j]) : 0.f;
-                    xs[m][j] = de[m][j] * us[m][j];
-                    gv[m][j] = in ? Raw<InBf16>::f(rg[m][j]) : 0.f;
-                    zs[m][j] = in && z ? Raw<InBf16>::f(rz[m][j]) : 0.f;
-                    gp[m][j] = z ? gv[m][j] * (zs[m][j] * sigmoid_f(zs[m][j])) : gv[m][j];
+                    sl[j] = sigmoid_f(de[j]);
+                    de[j] = softplus_f(de[j]);
                 }
+            }
 #pragma unroll
-                for (int r = 0; r < R; ++r) h[m][r] = ck[m][r];
+            for (int j = 0; j < J; ++j) {
+                const bool in = live && b * kCkpt + 4 * j + q < tl.len;
+                de[j] = in ? de[j] : 0.f;
+                us[j] = in ? Raw<InBf16>::f(ru[j]) : 0.f;
+                gv[j] = in ? Raw<InBf16>::f(rg[j]) : 0.f;
+                xs[j] = de[j] * us[j];
+                gp[j] = gv[j];
+                if (GATED) {
+                    const float z = in ? Raw<InBf16>::f(rz[j]) : 0.f, sg = sigmoid_f(z);
+                    gp[j] *= z * sg;
+                    gv[j] *= sg * fmaf(z, 1.f - sg, 1.f);  // what dz takes of the output
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                h[r] = reinterpret_cast<const float *>(ck)[r];
+                if (TILED) {  // a sequence's only tile has its true states stored
+                    const float shifted = fmaf(__builtin_amdgcn_exp2f(cum * A2[r]), from[r], h[r]);
+                    h[r] = chained ? shifted : h[r];
+                }
             }
             if (b > 0) fetch(b - 1);
-            // forwards: decay a, carried state c = a h and the output sum of every token of the block
-            float ha[kCkpt][M][R], hc[kCkpt][M][R], yp[M][kCkpt], dA8[M][R];
+            // forwards: decay a and carried state c = a h of every token of the block, and its output sum
+            float ha[kCkpt][R], hc[kCkpt][R], dA8[R], part[4];
             auto ahead = [&](auto jc, auto ic) {
                 constexpr int j = decltype(jc)::value, i = decltype(ic)::value, t = 4 * j + i;
-                const float *bt = &sB[buf][t][q * R], *ct = &sC[buf][t][q * R];
-#pragma unroll
-                for (int m = 0; m < M; ++m) {
-                    const float dl = quad_bcast<i>(de[m][j]), xl = quad_bcast<i>(xs[m][j]);
-                    float acc = 0.f;
-#pragma unroll
-                    for (int r = 0; r < R; ++r) {
-                        const float a = __builtin_amdgcn_exp2f(dl * A2[m][r]), c = a * h[m][r];
-                        h[m][r] = fmaf(xl, bt[r], c);
-                        ha[t][m][r] = a;
-                        hc[t][m][r] = c;
-                        acc = fmaf(ct[r], h[m][r], acc);
-                    }
-                    yp[m][t] = acc;
-                }
-            };
-            // backwards
-            float Pn[M][kCkpt], Sn[M][kCkpt];
-            auto back = [&](auto jc, auto ic) {
-                constexpr int j = decltype(jc)::value, i = decltype(ic)::value, t = 4 * j + i;
-                const float *bt = &sB[buf][t][q * R], *ct = &sC[buf][t][q * R];
-                float dB[R], dC[R];
-#pragma unroll
-                for (int r = 0; r < R; ++r) dB[r] = dC[r] = 0.f;
-#pragma unroll
-                for (int m = 0; m < M; ++m) {
-                    const float dl = quad_bcast<i>(de[m][j]), xl = quad_bcast<i>(xs[m][j]), g = quad_bcast<i>(gp[m][j]);
-                    float pn = 0.f, sn = 0.f;
-#pragma unroll
-                    for (int r = 0; r < R; ++r) {
-                        const float gg = fmaf(ct[r], g, G[m][r]), c = hc[t][m][r];
-                        dC[r] = fmaf(fmaf(xl, bt[r], c), g, dC[r]);
-                        dB[r] = fmaf(gg, xl, dB[r]);
-                        pn = fmaf(gg, bt[r], pn);
-                        const float e = gg * c;
-                        sn = fmaf(e, A2[m][r], sn);
-                        dA8[m][r] = fmaf(e, dl, dA8[m][r]);
-                        G[m][r] = ha[t][m][r] * gg;
-                    }
-                    Pn[m][t] = pn;
-                    Sn[m][t] = sn;
-                }
+                const float *bt = &sBC[buf][0][t][q * R], *ct = &sBC[buf][1][t][q * R];
+                const float dl = lane_bcast<i>(de[j]), xl = lane_bcast<i>(xs[j]);
+                float acc = 0.f;
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
-                    const float sb = channel_sum(dB[r]), sc = channel_sum(dC[r]);
-                    if (lane < 4) {
-                        sR[buf][wave][t][q * R + r] = sb;
-                        sR[buf][wave][t][NS + q * R + r] = sc;
-                    }
+                    const float a = __builtin_amdgcn_exp2f(dl * A2[r]), c = a * h[r];
+                    h[r] = fmaf(xl, bt[r], c);
+                    ha[t][r] = a;
+                    hc[t][r] = c;
+                    if (GATED) acc = fmaf(ct[r], h[r], acc);
                 }
+                part[i] = acc;
+                if (GATED && i == 3) yv[j] = transpose_sum(part, q);
+            };
+            // backwards
+            float Pn[4], Sn[4];
+            auto back = [&](auto jc, auto ic) {
+                constexpr int j = decltype(jc)::value, i = decltype(ic)::value, t = 4 * j + i;
+                const float *bt = &sBC[buf][0][t][q * R], *ct = &sBC[buf][1][t][q * R];
+                const float dl = lane_bcast<i>(de[j]), xl = lane_bcast<i>(xs[j]), g = lane_bcast<i>(gp[j]);
+                float dB[R], dC[R], pn = 0.f, sn = 0.f;
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const float gg = fmaf(ct[r], g, G[r]), c = hc[t][r], e = gg * c;
+                    dC[r] = fmaf(xl, bt[r], c) * g;
+                    dB[r] = gg * xl;
+                    pn = fmaf(gg, bt[r], pn);
+                    sn = fmaf(e, A2[r], sn);
+                    dA8[r] = fmaf(e, dl, dA8[r]);
+                    G[r] = ha[t][r] * gg;
+                }
+                Pn[i] = pn;
+                Sn[i] = sn;
+#pragma unroll
+                for (int r = 0; r < R; r += 4) {
+                    const float sb = quads_sum4(dB[r], dB[r + 1], dB[r + 2], dB[r + 3]);
+                    const float sc = quads_sum4(dC[r], dC[r + 1], dC[r + 2], dC[r + 3]);
+                    // every quad of a row has the sums: one writes dB's, another dC's
+                    if (!(lane & 8)) sR[buf][wave][t][(lane & 4 ? NS : 0) + q * R + r + mine] = lane & 4 ? sc : sb;
+                }
+                if (i > 0) return;
+                const float p = transpose_sum(Pn, q), s = transpose_sum(Sn, q);
+                gd[j] = sl[j] * fmaf(us[j], p, 0.6931471805599453f * s);  // s carries A log2(e)
+                gu[j] = fmaf(skip, gp[j], de[j] * p);
+                if (GATED) yv[j] = gv[j] * fmaf(skip, us[j], yv[j]);
+                dD = fmaf(gp[j], us[j], dD);
+                db += live && b * kCkpt + 4 * j + q < tl.len ? gd[j] : 0.f;
             };
 #define KDA_I(v) std::integral_constant<int, v>{}
 #pragma unroll
-            for (int m = 0; m < M; ++m)
-#pragma unroll
-                for (int r = 0; r < R; ++r) dA8[m][r] = 0.f;
+            for (int r = 0; r < R; ++r) dA8[r] = 0.f;
             ahead(KDA_I(0), KDA_I(0)); ahead(KDA_I(0), KDA_I(1)); ahead(KDA_I(0), KDA_I(2)); ahead(KDA_I(0), KDA_I(3));
             if constexpr (J > 1) {
                 ahead(KDA_I(1), KDA_I(0)); ahead(KDA_I(1), KDA_I(1)); ahead(KDA_I(1), KDA_I(2)); ahead(KDA_I(1), KDA_I(3));
@@ -307,59 +410,35 @@ __global__ void __launch_bounds__(256) scan_grad_kernel(ScanBwdLaunch P, BwdSpac
             back(KDA_I(0), KDA_I(3)); back(KDA_I(0), KDA_I(2)); back(KDA_I(0), KDA_I(1)); back(KDA_I(0), KDA_I(0));
 #undef KDA_I
 #pragma unroll
-            for (int m = 0; m < M; ++m) {
-#pragma unroll
-                for (int r = 0; r < R; ++r) dA[m][r] += dA8[m][r];
-#pragma unroll
-                for (int j = 0; j < J; ++j) {
-                    const int t = b * kCkpt + 4 * j + q;
-                    const int64_t row = tl.begin + t;
-                    const float pn = quad_transpose_sum(Pn[m][4 * j], Pn[m][4 * j + 1], Pn[m][4 * j + 2], Pn[m][4 * j + 3], q);
-                    const float sn = quad_transpose_sum(Sn[m][4 * j], Sn[m][4 * j + 1], Sn[m][4 * j + 2], Sn[m][4 * j + 3], q);
-                    // sn carries A log2(e)
-                    const float dd = sl[m][j] * fmaf(us[m][j], pn, 0.6931471805599453f * sn);
-                    const float du = fmaf(skip[m], gp[m][j], de[m][j] * pn);
-                    if (z) {
-                        const float yv = fmaf(skip[m], us[m][j],
-                                              quad_transpose_sum(yp[m][4 * j], yp[m][4 * j + 1], yp[m][4 * j + 2], yp[m][4 * j + 3], q));
-                        const float sg = sigmoid_f(zs[m][j]);
-                        if (live[m] && t < tl.len)
-                            P.dz.put(row, chn[m], gv[m][j] * yv * (sg * fmaf(zs[m][j], 1.f - sg, 1.f)));
-                    }
-                    dD[m] = fmaf(gp[m][j], us[m][j], dD[m]);
-                    if (live[m] && t < tl.len) {
-                        db[m] += dd;
-                        P.du.put(row, chn[m], du);
-                        P.ddt.put(row, chn[m], dd);
-                    }
-                }
-            }
-            if (b > 0) stage(buf ^ 1);
+            for (int r = 0; r < R; ++r) dA[r] += dA8[r];
+            ou.put(b * kCkpt, tl.len, q, live, P.du.bf16, gu);
+            od.put(b * kCkpt, tl.len, q, live, P.ddt.bf16, gd);
+            if (GATED) oz.put(b * kCkpt, tl.len, q, live, P.dz.bf16, yv);
+            if (b > 0) stage(b - 1, buf ^ 1);
             __syncthreads();
-            for (int e = threadIdx.x; e < kCkpt * 2 * NS; e += 256) {
-                const int t = e / (2 * NS), n = e % (2 * NS), half = n / NS, s = n % NS;
+#pragma unroll
+            for (int i = 0; i < kSt; ++i) {
+                const int e = i * 256 + threadIdx.x, t = e / (2 * NS), n = e % (2 * NS), half = n / NS, s = n % NS;
                 if (b * kCkpt + t < tl.len && s < P.ds)
-                    W.pBC[((static_cast<int64_t>(group) * P.seq.rows() + tl.begin + b * kCkpt + t) * 2 + half) * P.ds + s] =
+                    (pBC + static_cast<int64_t>(b) * kCkpt * 2 * P.ds)[static_cast<uint32_t>((t * 2 + half) * P.ds + s)] =
                         (sR[buf][0][t][n] + sR[buf][1][t][n]) + (sR[buf][2][t][n] + sR[buf][3][t][n]);
             }
         }
     }
+    dD = quad_sum(dD);
+    db = quad_sum(db);
+    if (!live) return;
+    const int64_t pb = slot * P.dim + ch;
+    if (q == 0) {
+        W.pD[pb] = dD;
+        W.pb[pb] = db;
+    }
 #pragma unroll
-    for (int m = 0; m < M; ++m) {
-        const float d = quad_sum(dD[m]), bsum = quad_sum(db[m]);
-        if (!live[m]) continue;
-        const int64_t pb = slot * P.dim + chn[m];
-        if (q == 0) {
-            W.pD[pb] = d;
-            W.pb[pb] = bsum;
-        }
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            if (q * R + r >= P.ds) continue;
-            W.pA[pb * P.ds + q * R + r] = dA[m][r];
-            if (P.dh0 && tl.valid && tl.k == 0)
-                P.dh0[(static_cast<int64_t>(tl.n) * P.dim + chn[m]) * P.ds + q * R + r] = G[m][r];
-        }
+    for (int r = 0; r < R; ++r) {
+        if (q * R + r >= P.ds) continue;
+        W.pA[pb * P.ds + q * R + r] = dA[r];
+        if (P.dh0 && tl.valid && tl.k == 0)
+            P.dh0[(static_cast<int64_t>(tl.n) * P.dim + ch) * P.ds + q * R + r] = G[r];
     }
 }
 
@@ -375,11 +454,11 @@ __global__ void __launch_bounds__(256) scan_bc_sum_kernel(ScanBwdLaunch P, const
     (half ? P.dC : P.dB).put(row, s, a);
 }
 
-int channels_per_quad(int ds) { return ds <= 16 ? 2 : 1; }
+bool tiled(const SeqTiles &s) { return s.T > s.L; }
 
 BwdSpace space(float *ws, const SeqTiles &seq, int dim, int ds) {
-    const int64_t slots = seq.slots(), rows = seq.rows(), wide = 64 * channels_per_quad(ds);
-    const int64_t groups = (dim + wide - 1) / wide, blocks = rows / (ds <= 32 ? 8 : 4) + slots + 1;
+    const int64_t slots = seq.slots(), rows = seq.rows(), groups = (dim + 63) / 64;
+    const int64_t padded = ds <= 16 ? 16 : ds <= 32 ? 32 : 64, blocks = rows / (ds <= 32 ? 8 : 4) + slots + 1;
     BwdSpace w{};
     int64_t at = 0;
     auto take = [&](int64_t n) {
@@ -387,7 +466,13 @@ BwdSpace space(float *ws, const SeqTiles &seq, int dim, int ds) {
         at += (n + 3) & ~int64_t{3};
         return p;
     };
-    w.ck = take(blocks * dim * ds);
+    w.ck = take(blocks * dim * padded);
+    if (tiled(seq)) {
+        w.cum = take(blocks * dim);
+        w.H = take(slots * dim * ds);
+        w.G = take(slots * dim * ds);
+        w.sum = take(slots * dim);
+    }
     w.pA = take(slots * dim * ds);
     w.pD = take(slots * dim);
     w.pb = take(slots * dim);
@@ -396,28 +481,47 @@ BwdSpace space(float *ws, const SeqTiles &seq, int dim, int ds) {
     return w;
 }
 
-template <int R, int M, bool InBf16>
+template <int R, bool InBf16, bool GATED>
 void launch_grad(const ScanBwdLaunch &P, const BwdSpace &w) {
     const int64_t slots = P.seq.slots();
     if (slots == 0) return;
-    const int g1 = (P.dim + 63) / 64, g2 = (P.dim + 64 * M - 1) / (64 * M);
-    scan_states_kernel<R, InBf16><<<static_cast<unsigned>(slots * g1), 256, 0, P.stream>>>(P, w);
-    scan_grad_kernel<R, M, InBf16><<<static_cast<unsigned>(slots * g2), 256, 0, P.stream>>>(P, w);
+    const int groups = (P.dim + 63) / 64;
+    const unsigned grid = static_cast<unsigned>(slots * groups);
+    if (tiled(P.seq)) {
+        scan_states_kernel<R, InBf16, true, GATED><<<grid, 256, 0, P.stream>>>(P, w);
+        const int64_t states = static_cast<int64_t>(P.dim) * P.ds;
+        scan_bwd_combine_kernel<<<dim3(static_cast<unsigned>((states + 255) / 256), P.seq.N), 256, 0, P.stream>>>(P, w);
+        scan_grad_kernel<R, InBf16, true, GATED><<<grid, 256, 0, P.stream>>>(P, w);
+    } else {
+        scan_states_kernel<R, InBf16, false, false><<<grid, 256, 0, P.stream>>>(P, w);
+        scan_grad_kernel<R, InBf16, false, GATED><<<grid, 256, 0, P.stream>>>(P, w);
+    }
     const int64_t n = P.seq.rows() * 2 * P.ds;
-    if (n > 0) scan_bc_sum_kernel<<<static_cast<unsigned>((n + 255) / 256), 256, 0, P.stream>>>(P, w.pBC, g2);
+    if (n > 0) scan_bc_sum_kernel<<<static_cast<unsigned>((n + 255) / 256), 256, 0, P.stream>>>(P, w.pBC, groups);
+}
+
+template <int R, bool InBf16>
+void launch_gated(const ScanBwdLaunch &P, const BwdSpace &w) {
+    if (P.z.p) launch_grad<R, InBf16, true>(P, w);
+    else launch_grad<R, InBf16, false>(P, w);
 }
 
 template <bool InBf16>
 void launch_any(const ScanBwdLaunch &P, const BwdSpace &w) {
-    if (P.ds <= 16) launch_grad<4, 2, InBf16>(P, w);
-    else if (P.ds <= 32) launch_grad<8, 1, InBf16>(P, w);
-    else launch_grad<16, 1, InBf16>(P, w);
+    if (P.ds <= 16) launch_gated<4, InBf16>(P, w);
+    else if (P.ds <= 32) launch_gated<8, InBf16>(P, w);
+    else launch_gated<16, InBf16>(P, w);
 }
 
 }  // namespace
 
+// Whole sequences where they give two waves per SIMD, which is what the gradient kernel's registers allow, by
+// themselves; else tiles.  On MI355X, bf16: 16 x 1,024 x 4,096 (1,024 workgroups) 1,257 us whole and 1,410
+// tiled, 8 x 1,024 x 4,096 (512) 783 and 904, 12 x 1,024 x 2,048 (384) 757 and 672.
 SeqTiles scan_bwd_tiles(const int32_t *cu, int N, int T, int dim, int ds) {
     SeqTiles s{cu, N, T, T > 0 ? T : 1};
+    const int64_t groups = (dim + 63) / 64;
+    if (cu || N * groups < 512) tile_for(s, groups);
     return s;
 }
 

@@ -463,7 +463,7 @@ size_t kda_chunk_fwd_noalloc_max_workspace_bytes(void);
  * additions:
  *  - Token tensors have a row stride: `x_stride` is the distance in elements
  *    between consecutive tokens (rows) of `x`, at least its width, so that
- *    slices of a wider projection need no copy, and at most 2^27.  Token t of sequence b of a
+ *    slices of a wider projection need no copy, and below 2^22.  Token t of sequence b of a
  *    fixed-length batch is row b * T + t.  Token tensors need only their
  *    elements' alignment; 16-byte aligned bases and strides run faster.
  *    Parameters and states are contiguous.
