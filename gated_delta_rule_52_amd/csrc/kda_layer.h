@@ -267,7 +267,7 @@ struct ConvBwdLaunch {
     float *ws;
     hipStream_t stream;
 };
-size_t conv_bwd_workspace_bytes(int64_t rows, int dim, int width);
+size_t conv_bwd_workspace_bytes(int64_t rows, int dim, int width, bool bf16);
 hipError_t launch_conv_bwd(const ConvBwdLaunch &P);
 
 struct NormFwdLaunch {
@@ -295,7 +295,12 @@ struct NormBwdLaunch {
 size_t norm_bwd_workspace_bytes(int64_t rows, int dim);
 hipError_t launch_norm_bwd(const NormBwdLaunch &P);
 
-// out[c] = sum over p < parts of in[p * ld + c] for c < cols, in a fixed order (kda_layer_norm.hip).
-void launch_column_sum(const float *in, int64_t ld, int parts, int64_t cols, float *out, hipStream_t stream);
+// Sums parts rows of `in`, ld apart, in a fixed order, into up to three outputs that take consecutive runs of the
+// columns (a null output's run is skipped) (kda_layer_norm.hip).
+struct ColumnSums {
+    float *out[3];
+    int64_t cols[3];
+};
+void launch_column_sum(const float *in, int64_t ld, int parts, const ColumnSums &to, hipStream_t stream);
 
 }  // namespace kda

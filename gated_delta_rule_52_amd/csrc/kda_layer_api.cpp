@@ -191,8 +191,8 @@ kda_status check_conv_sizes(const A *a) {
     if (!valid_dtype(a->in_dtype) || !valid_dtype(a->w_dtype))
         return fail(KDA_ERR_UNSUPPORTED, "in_dtype=%d w_dtype=%d", a->in_dtype, a->w_dtype);
     if (a->flags & ~KDA_CONV_SILU) return fail(KDA_ERR_UNSUPPORTED, "unknown flags 0x%x", a->flags);
-    const int64_t rows = static_cast<int64_t>(a->batch) * a->T, cb = (a->dim + 255) / 256;
-    KDA_TRY(check_grid((rows + 31) / 32 * cb * 256));
+    const int64_t rows = static_cast<int64_t>(a->batch) * a->T, cb = (a->dim + 255) / 256;  // at least any launch's
+    KDA_TRY(check_grid((rows + 7) / 8 * cb * 256));
     return check_grid(static_cast<int64_t>(a->num_seqs) * cb * 256);
 }
 
@@ -366,7 +366,7 @@ kda_status kda_short_conv_step(const kda_short_conv_args *a) {
 
 size_t kda_short_conv_bwd_workspace_bytes(const kda_short_conv_bwd_args *a) {
     if (check_conv_sizes(a) != KDA_OK) return static_cast<size_t>(-1);
-    return kda::conv_bwd_workspace_bytes(static_cast<int64_t>(a->batch) * a->T, a->dim, a->width);
+    return kda::conv_bwd_workspace_bytes(static_cast<int64_t>(a->batch) * a->T, a->dim, a->width, a->in_dtype == KDA_DTYPE_BF16);
 }
 
 kda_status kda_short_conv_bwd(const kda_short_conv_bwd_args *a) {
@@ -379,7 +379,7 @@ kda_status kda_short_conv_bwd(const kda_short_conv_bwd_args *a) {
     KDA_TRY(check_stride("x", a->x, a->x_stride, a->dim, rows));
     KDA_TRY(check_stride("grad_y", a->grad_y, a->grad_y_stride, a->dim, rows));
     KDA_TRY(check_stride("grad_x", a->grad_x, a->grad_x_stride, a->dim, rows));
-    const size_t need = kda::conv_bwd_workspace_bytes(rows, a->dim, a->width);
+    const size_t need = kda::conv_bwd_workspace_bytes(rows, a->dim, a->width, a->in_dtype == KDA_DTYPE_BF16);
     if (a->workspace_bytes < need || (need > 0 && !a->workspace))
         return fail(KDA_ERR_WORKSPACE_TOO_SMALL, "workspace %zu < %zu bytes", a->workspace_bytes, need);
     const int64_t states = static_cast<int64_t>(a->num_seqs) * (a->width - 1) * a->dim;
@@ -427,7 +427,7 @@ kda_status kda_layer_norm_fwd(const kda_layer_norm_args *a) {
     KDA_TRY(check_stride("y", a->y, a->y_stride, a->dim, a->rows));
     KDA_TRY(check_stride("residual", a->residual, a->residual_stride, a->dim, a->rows));
     KDA_TRY(check_stride("residual_out", a->residual_out, a->residual_out_stride, a->dim, a->rows));
-    KDA_TRY(check_grid(a->rows * (a->dim <= 2048 ? 64 : a->dim <= 8192 ? 256 : 1024)));
+    KDA_TRY(check_grid(a->rows * (a->dim <= 1024 ? 64 : a->dim <= 4096 ? 256 : 1024)));
     const int64_t param = a->dim * dsize(a->w_dtype);
     const bool in_place = a->residual == a->residual_out && a->residual_stride == a->residual_out_stride;
     const Span ins[] = {strided("x", a->x, a->rows, a->dim, a->x_stride, a->x_dtype),

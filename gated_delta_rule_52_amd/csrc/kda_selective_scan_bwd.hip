@@ -36,9 +36,7 @@ struct BwdSpace {
     float *H;    // [slot][dim][ds] state a tile reaches from zero, then the one it starts from
     float *G;    // [slot][dim][ds] state gradient at a tile's start from its own outputs, then the one behind its end
     float *sum;  // [slot][dim] sum of delta over a tile
-    float *pA;   // [slot][dim][ds]
-    float *pD;   // [slot][dim]
-    float *pb;   // [slot][dim]
+    float *par;  // [slot][dim ds + 2 dim] partial gradients of A, D and the bias
     float *pBC;  // [channel group][rows][2][ds]
     int64_t bytes;
 };
@@ -428,15 +426,15 @@ __global__ void __launch_bounds__(256) scan_grad_kernel(ScanBwdLaunch P, BwdSpac
     dD = quad_sum(dD);
     db = quad_sum(db);
     if (!live) return;
-    const int64_t pb = slot * P.dim + ch;
+    float *par = W.par + slot * P.dim * (P.ds + 2);
     if (q == 0) {
-        W.pD[pb] = dD;
-        W.pb[pb] = db;
+        par[static_cast<int64_t>(P.dim) * P.ds + ch] = dD;
+        par[static_cast<int64_t>(P.dim) * (P.ds + 1) + ch] = db;
     }
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         if (q * R + r >= P.ds) continue;
-        W.pA[pb * P.ds + q * R + r] = dA[r];
+        par[static_cast<int64_t>(ch) * P.ds + q * R + r] = dA[r];
         if (P.dh0 && tl.valid && tl.k == 0)
             P.dh0[(static_cast<int64_t>(tl.n) * P.dim + ch) * P.ds + q * R + r] = G[r];
     }
@@ -473,9 +471,7 @@ BwdSpace space(float *ws, const SeqTiles &seq, int dim, int ds) {
         w.G = take(slots * dim * ds);
         w.sum = take(slots * dim);
     }
-    w.pA = take(slots * dim * ds);
-    w.pD = take(slots * dim);
-    w.pb = take(slots * dim);
+    w.par = take(slots * dim * (ds + 2));
     w.pBC = take(groups * rows * 2 * ds);
     w.bytes = at * 4;
     return w;
@@ -531,10 +527,9 @@ hipError_t launch_scan_bwd(const ScanBwdLaunch &P) {
     const BwdSpace w = space(P.ws, P.seq, P.dim, P.ds);
     if (P.u.bf16) launch_any<true>(P, w);
     else launch_any<false>(P, w);
-    const int slots = static_cast<int>(P.seq.slots());
-    launch_column_sum(w.pA, static_cast<int64_t>(P.dim) * P.ds, slots, static_cast<int64_t>(P.dim) * P.ds, P.dA, P.stream);
-    if (P.dD) launch_column_sum(w.pD, P.dim, slots, P.dim, P.dD, P.stream);
-    if (P.ddt_bias) launch_column_sum(w.pb, P.dim, slots, P.dim, P.ddt_bias, P.stream);
+    const int64_t states = static_cast<int64_t>(P.dim) * P.ds;
+    launch_column_sum(w.par, states + 2 * P.dim, static_cast<int>(P.seq.slots()),
+                      {{P.dA, P.dD, P.ddt_bias}, {states, P.dim, P.dim}}, P.stream);
     return hipGetLastError();
 }
 

@@ -3,8 +3,8 @@
 //     p_t = bias + sum_j w[j] x_{t-W+1+j},   y = p or p sigmoid(p)
 //
 // Bound by HBM: x read and y written once (plus W - 1 rows of each tile's past, which the neighbour tile has
-// just read).  A thread holds V adjacent channels (one 16-byte access) and walks a tile of tokens with the
-// last W - 1 inputs in registers, so every input is loaded once.  A sequence's first W - 1 outputs take
+// just read).  A thread holds V adjacent channels and walks a tile of tokens with the last W - 1 inputs in
+// registers, so every input is loaded once, four rows in flight.  A sequence's first W - 1 outputs take
 // their past from its state; tiles cut the rows without regard to sequences, and the walk reloads the window
 // where a sequence starts.
 #include "kda_layer.h"
@@ -31,15 +31,28 @@ __device__ __forceinline__ void bounds_of(const int32_t *cu, int N, int T, int n
     e = s + len;
 }
 
+// V adjacent channels: one, or 4 or 8 in accesses of up to 16 bytes, which the hardware takes at any element's
+// alignment.  Where the width is no multiple of V the last thread's channels are moved back inside: it computes
+// some of its neighbour's again and stores the same values.
+typedef uint32_t any4 __attribute__((ext_vector_type(4), aligned(2)));
 template <int V, bool InBf16>
 __device__ __forceinline__ void load_v(const void *p, int64_t at, float *x) {
+    using E = typename Elem<InBf16>::T;
+    const E *e = static_cast<const E *>(p) + at;
     if constexpr (V == 1) {
-        x[0] = Elem<InBf16>::load(static_cast<const typename Elem<InBf16>::T *>(p), at);
+        x[0] = Elem<InBf16>::load(e, 0);
     } else {
+        constexpr int words = V * static_cast<int>(sizeof(E)) / 4;
+        typedef uint32_t some __attribute__((ext_vector_type(words), aligned(2)));
+        const some v = *reinterpret_cast<const some *>(e);
 #pragma unroll
-        for (int i = 0; i < V; i += 4) {
-            const float4 f = Elem<InBf16>::load4(static_cast<const typename Elem<InBf16>::T *>(p), at + i);
-            x[i] = f.x; x[i + 1] = f.y; x[i + 2] = f.z; x[i + 3] = f.w;
+        for (int i = 0; i < words; ++i) {
+            if constexpr (InBf16) {
+                x[2 * i] = __uint_as_float(v[i] << 16);
+                x[2 * i + 1] = __uint_as_float(v[i] & 0xffff0000u);
+            } else {
+                x[i] = __uint_as_float(v[i]);
+            }
         }
     }
 }
@@ -49,27 +62,63 @@ __device__ __forceinline__ void store_v(const Rows &r, int64_t row, int col, con
         r.put(row, col, x[0]);
     } else {
         const int64_t at = row * r.stride + col;
+        if (r.bf16) {
+            typedef uint32_t some __attribute__((ext_vector_type(V / 2), aligned(2)));
+            some v;
 #pragma unroll
-        for (int i = 0; i < V; i += 4) {
-            const float4 f = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
-            if (r.bf16) Elem<true>::store4(static_cast<uint16_t *>(r.p), at + i, f);
-            else Elem<false>::store4(static_cast<float *>(r.p), at + i, f);
+            for (int i = 0; i < V / 2; ++i) v[i] = to_bf16(x[2 * i]) | static_cast<uint32_t>(to_bf16(x[2 * i + 1])) << 16;
+            *reinterpret_cast<some *>(static_cast<uint16_t *>(r.p) + at) = v;
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; i += 4) {
+                any4 v;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v[k] = __float_as_uint(x[i + k]);
+                *reinterpret_cast<any4 *>(static_cast<float *>(r.p) + at + i) = v;
+            }
         }
     }
+}
+template <int V>
+__device__ __forceinline__ int first_channel(int thread, int dim) {
+    const int c = thread * V;
+    return c + V > dim && c < dim ? dim - V : c;
 }
 
 template <int W, int V>
 struct Taps {
     float w[W][V], b[V];
     __device__ __forceinline__ Taps(const void *wp, const void *bp, int bf16, int c0) {
+        auto all = [&](auto bf) {
+            using E = Elem<decltype(bf)::value>;
+            const auto *p = static_cast<const typename E::T *>(wp) + static_cast<int64_t>(c0) * W;
+            const auto *q = static_cast<const typename E::T *>(bp) + c0;
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
+            for (int v = 0; v < V; ++v) {
 #pragma unroll
-            for (int j = 0; j < W; ++j) w[j][v] = param(wp, bf16, static_cast<int64_t>(c0 + v) * W + j);
-            b[v] = bp ? param(bp, bf16, c0 + v) : 0.f;
-        }
+                for (int j = 0; j < W; ++j) w[j][v] = E::load(p, v * W + j);
+                b[v] = bp ? E::load(q, v) : 0.f;
+            }
+        };
+        if (bf16) all(std::true_type{});
+        else all(std::false_type{});
+    }
+    __device__ __forceinline__ float at(int v, const float (&win)[W - 1][V], const float *x) const {
+        float p = b[v];
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) p = fmaf(w[j][v], win[j][v], p);
+        return fmaf(w[W - 1][v], x[v], p);
     }
 };
+template <int W, int V>
+__device__ __forceinline__ void shift(float (&win)[W - 1][V], const float *x) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+#pragma unroll
+        for (int j = 0; j + 1 < W - 1; ++j) win[j][v] = win[j + 1][v];
+        win[W - 2][v] = x[v];
+    }
+}
 
 // Fills win (the W - 1 inputs before row t of the sequence from row `s` on, oldest first).
 template <int W, int V, bool InBf16>
@@ -90,13 +139,13 @@ __device__ __forceinline__ void window(const Rows &x, const void *h0, int dim, i
     }
 }
 
-constexpr int kConvTile = 32;  // rows per thread
+constexpr int kAhead = 4;      // rows loaded together
 
 template <int W, int V, bool InBf16>
-__global__ void __launch_bounds__(256) conv_kernel(ConvLaunch P, int64_t rows, int cblocks) {
-    const int c0 = (static_cast<int>(blockIdx.x % cblocks) * 256 + threadIdx.x) * V;
-    int64_t t = static_cast<int64_t>(blockIdx.x / cblocks) * kConvTile;
-    const int64_t end = t + kConvTile < rows ? t + kConvTile : rows;
+__global__ void __launch_bounds__(256) conv_kernel(ConvLaunch P, int64_t rows, int cblocks, int tile) {
+    const int c0 = first_channel<V>(static_cast<int>(blockIdx.x % cblocks) * 256 + threadIdx.x, P.dim);
+    int64_t t = static_cast<int64_t>(blockIdx.x / cblocks) * tile;
+    const int64_t end = t + tile < rows ? t + tile : rows;
     int n = sequence_of(P.cu, P.N, P.T, t);
     if (c0 >= P.dim || n >= P.N) return;
     const Taps<W, V> k(P.w, P.bias, P.w_bf16, c0);
@@ -108,24 +157,31 @@ __global__ void __launch_bounds__(256) conv_kernel(ConvLaunch P, int64_t rows, i
             continue;
         }
         if (s > t) t = s;
-        float win[W - 1][V], x[V], y[V];
+        if (t >= end) return;
+        float win[W - 1][V], x[kAhead][V];
         window<W, V, InBf16>(P.x, P.h0, P.dim, n, s, t, c0, win);
         const int64_t stop = e < end ? e : end;
-        for (; t < stop; ++t) {
-            load_v<V, InBf16>(P.x.p, t * P.x.stride + c0, x);
+        auto output = [&](int64_t row, const float (&x)[V]) {
+            float y[V];
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                float p = k.b[v];
-#pragma unroll
-                for (int j = 0; j < W - 1; ++j) p = fmaf(k.w[j][v], win[j][v], p);
-                p = fmaf(k.w[W - 1][v], x[v], p);
+                const float p = k.at(v, win, x);
                 y[v] = P.silu ? p * sigmoid_f(p) : p;
-#pragma unroll
-                for (int j = 0; j + 1 < W - 1; ++j) win[j][v] = win[j + 1][v];
-                win[W - 2][v] = x[v];
             }
-            store_v<V>(P.y, t, c0, y);
+            shift<W, V>(win, x);
+            store_v<V>(P.y, row, c0, y);
+        };
+        for (; t + kAhead <= stop; t += kAhead) {
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) load_v<V, InBf16>(P.x.p, (t + i) * P.x.stride + c0, x[i]);
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) output(t + i, x[i]);
         }
+        for (; t < stop; ++t) {
+            load_v<V, InBf16>(P.x.p, t * P.x.stride + c0, x[0]);
+            output(t, x[0]);
+        }
+        t = stop;
         if (++n >= P.N) return;
     }
 }
@@ -154,7 +210,7 @@ __global__ void __launch_bounds__(256) conv_state_kernel(ConvLaunch P, int cbloc
 // One token per sequence: output and shifted state in one pass.
 template <int W, int V, bool InBf16>
 __global__ void __launch_bounds__(256) conv_step_kernel(ConvLaunch P, int cblocks) {
-    const int c0 = (static_cast<int>(blockIdx.x % cblocks) * 256 + threadIdx.x) * V, n = blockIdx.x / cblocks;
+    const int c0 = first_channel<V>(static_cast<int>(blockIdx.x % cblocks) * 256 + threadIdx.x, P.dim), n = blockIdx.x / cblocks;
     if (c0 >= P.dim) return;
     const Taps<W, V> k(P.w, P.bias, P.w_bf16, c0);
     float win[W - 1][V], x[V], y[V];
@@ -162,10 +218,7 @@ __global__ void __launch_bounds__(256) conv_step_kernel(ConvLaunch P, int cblock
     load_v<V, InBf16>(P.x.p, n * P.x.stride + c0, x);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        float p = k.b[v];
-#pragma unroll
-        for (int j = 0; j < W - 1; ++j) p = fmaf(k.w[j][v], win[j][v], p);
-        p = fmaf(k.w[W - 1][v], x[v], p);
+        const float p = k.at(v, win, x);
         y[v] = P.silu ? p * sigmoid_f(p) : p;
     }
     store_v<V>(P.y, n, c0, y);
@@ -179,7 +232,8 @@ __global__ void __launch_bounds__(256) conv_step_kernel(ConvLaunch P, int cblock
 
 // ---- gradients -----------------------------------------------------------------------------------------
 
-constexpr int kGradTile = 64;
+constexpr int kGradSubs = 8;   // tiles per workgroup, of 256 / kGradSubs threads each
+constexpr int kGradAhead = 2;  // rows loaded together
 
 // d silu(p) / dp times g.
 __device__ __forceinline__ float silu_grad(float g, float p) {
@@ -187,15 +241,19 @@ __device__ __forceinline__ float silu_grad(float g, float p) {
     return g * (s * fmaf(p, 1.f - s, 1.f));
 }
 
-// dx of a tile's rows and the tile's share of dweight and dbias.  dx_t needs gp of the W - 1 rows behind it,
+// dx of a tile's rows and the workgroup's share of dweight and dbias.  dx_t needs gp of the W - 1 rows behind it,
 // so the walk runs W - 1 rows past the tile's end (inside the sequence) and those rows' gp is computed twice.
 template <int W, int V, bool InBf16>
-__global__ void __launch_bounds__(256) conv_grad_kernel(ConvBwdLaunch P, int64_t rows, int cblocks) {
-    const int c0 = (static_cast<int>(blockIdx.x % cblocks) * 256 + threadIdx.x) * V;
-    const int64_t tile = blockIdx.x / cblocks;
-    int64_t t = tile * kGradTile;
-    const int64_t end = t + kGradTile < rows ? t + kGradTile : rows;
-    if (c0 >= P.dim) return;
+__global__ void __launch_bounds__(256) conv_grad_kernel(ConvBwdLaunch P, int64_t rows, int cblocks, int tile) {
+    constexpr int LANES = 256 / kGradSubs;
+    __shared__ float fold[kGradSubs][V][LANES];
+    const int lane = threadIdx.x % LANES, sub = threadIdx.x / LANES;
+    int c0 = first_channel<V>(static_cast<int>(blockIdx.x % cblocks) * LANES + lane, P.dim);
+    const bool live = c0 < P.dim;
+    if (!live) c0 = 0;  // walks no rows, but stays for the barriers
+    const int64_t part = blockIdx.x / cblocks;
+    int64_t t = (part * kGradSubs + sub) * tile;
+    const int64_t end = !live ? t : t + tile < rows ? t + tile : rows;
     const Taps<W, V> k(P.w, P.bias, P.w_bf16, c0);
     float dw[W][V], db[V];
 #pragma unroll
@@ -210,71 +268,99 @@ __global__ void __launch_bounds__(256) conv_grad_kernel(ConvBwdLaunch P, int64_t
         if (e <= t) continue;
         if (s > t) t = s;
         if (t >= end) break;
-        float win[W - 1][V], x[V], g[V], gp[W][V];  // gp[j]: of row i - (W - 1) + j
+        float win[W - 1][V], gp[W - 1][V];  // gp[j]: of the row W - 1 - j behind the next
         window<W, V, InBf16>(P.x, P.h0, P.dim, n, s, t, c0, win);
 #pragma unroll
         for (int v = 0; v < V; ++v)
 #pragma unroll
-            for (int j = 0; j < W; ++j) gp[j][v] = 0.f;
-        const int64_t stop = e < end ? e : end, first = t;
-        for (int64_t i = t; i < stop + W - 1; ++i) {
+            for (int j = 0; j < W - 1; ++j) gp[j][v] = 0.f;
+        const int64_t stop = e < end ? e : end, first = t, over = stop + W - 1;
+        // row i's pre-activation gradient in g's place, and its share of dweight and dbias if it is the tile's
+        auto gradient = [&](const float (&x)[V], float (&g)[V], bool own) {
 #pragma unroll
-            for (int v = 0; v < V; ++v)
+            for (int v = 0; v < V; ++v) {
+                if (P.silu) g[v] = silu_grad(g[v], k.at(v, win, x));
+                if (!own) continue;
 #pragma unroll
-                for (int j = 0; j < W - 1; ++j) gp[j][v] = gp[j + 1][v];
+                for (int j = 0; j < W - 1; ++j) dw[j][v] = fmaf(g[v], win[j][v], dw[j][v]);
+                dw[W - 1][v] = fmaf(g[v], x[v], dw[W - 1][v]);
+                db[v] += g[v];
+            }
+            shift<W, V>(win, x);
+        };
+        // the gradient of row i - (W - 1), complete with row i's g
+        auto finish = [&](int64_t i, const float (&g)[V], bool last) {
+            const int64_t o = i - (W - 1);
+            float d[V];
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                d[v] = k.w[0][v] * g[v];
+#pragma unroll
+                for (int j = 0; j < W - 1; ++j) d[v] = fmaf(k.w[W - 1 - j][v], gp[j][v], d[v]);
+            }
+            if (last && P.dhT && e - o <= W - 1) {  // the row is also row W - 1 - (e - o) of the final state
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    d[v] += P.dhT[(static_cast<int64_t>(n) * (W - 1) + W - 1 - (e - o)) * P.dim + c0 + v];
+            }
+            store_v<V>(P.dx, o, c0, d);
+            shift<W, V>(gp, g);
+        };
+        float x[kGradAhead][V], g[kGradAhead][V];
+        auto load = [&](int64_t i, float (&x)[V], float (&g)[V]) {
+            load_v<V, InBf16>(P.x.p, i * P.x.stride + c0, x);
+            load_v<V, InBf16>(P.gy.p, i * P.gy.stride + c0, g);
+        };
+        int64_t i = t;
+        for (; i < stop && i < first + W - 1; ++i) {
+            load(i, x[0], g[0]);
+            gradient(x[0], g[0], true);
+            shift<W, V>(gp, g[0]);
+        }
+        for (; i + kGradAhead <= stop; i += kGradAhead) {  // nothing to ask here
+#pragma unroll
+            for (int a = 0; a < kGradAhead; ++a) load(i + a, x[a], g[a]);
+#pragma unroll
+            for (int a = 0; a < kGradAhead; ++a) {
+                gradient(x[a], g[a], true);
+                finish(i + a, g[a], false);
+            }
+        }
+        for (; i < stop; ++i) {
+            load(i, x[0], g[0]);
+            gradient(x[0], g[0], true);
+            finish(i, g[0], false);
+        }
+        for (; i < over; ++i) {
             if (i < e) {
-                load_v<V, InBf16>(P.x.p, i * P.x.stride + c0, x);
-                load_v<V, InBf16>(P.gy.p, i * P.gy.stride + c0, g);
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    if (P.silu) {
-                        float p = k.b[v];
-#pragma unroll
-                        for (int j = 0; j < W - 1; ++j) p = fmaf(k.w[j][v], win[j][v], p);
-                        p = fmaf(k.w[W - 1][v], x[v], p);
-                        g[v] = silu_grad(g[v], p);
-                    }
-                    gp[W - 1][v] = g[v];
-                    if (i < stop) {
-#pragma unroll
-                        for (int j = 0; j < W - 1; ++j) dw[j][v] = fmaf(g[v], win[j][v], dw[j][v]);
-                        dw[W - 1][v] = fmaf(g[v], x[v], dw[W - 1][v]);
-                        db[v] += g[v];
-                    }
-#pragma unroll
-                    for (int j = 0; j + 1 < W - 1; ++j) win[j][v] = win[j + 1][v];
-                    win[W - 2][v] = x[v];
-                }
+                load(i, x[0], g[0]);
+                gradient(x[0], g[0], false);
             } else {
 #pragma unroll
-                for (int v = 0; v < V; ++v) gp[W - 1][v] = 0.f;
+                for (int v = 0; v < V; ++v) g[0][v] = 0.f;
             }
-            const int64_t o = i - (W - 1);  // the row whose gradient is complete
-            if (o >= first) {
-                float d[V];
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    d[v] = 0.f;
-#pragma unroll
-                    for (int j = 0; j < W; ++j) d[v] = fmaf(k.w[W - 1 - j][v], gp[j][v], d[v]);
-                }
-                const int64_t back = e - o;  // the row is also row W - 1 - back of the final state
-                if (P.dhT && back <= W - 1) {
-#pragma unroll
-                    for (int v = 0; v < V; ++v)
-                        d[v] += P.dhT[(static_cast<int64_t>(n) * (W - 1) + W - 1 - back) * P.dim + c0 + v];
-                }
-                store_v<V>(P.dx, o, c0, d);
-            }
+            if (i - (W - 1) >= first) finish(i, g[0], true);
+            else shift<W, V>(gp, g[0]);
         }
         t = stop;
     }
-    float *part = P.ws + tile * static_cast<int64_t>(W + 1) * P.dim;
+    float *out = P.ws + part * static_cast<int64_t>(W + 1) * P.dim;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
+    for (int j = 0; j <= W; ++j) {
+        __syncthreads();
 #pragma unroll
-        for (int j = 0; j < W; ++j) part[static_cast<int64_t>(c0 + v) * W + j] = dw[j][v];
-        part[static_cast<int64_t>(W) * P.dim + c0 + v] = db[v];
+        for (int v = 0; v < V; ++v) fold[sub][v][lane] = j < W ? dw[j < W ? j : 0][v] : db[v];
+        __syncthreads();
+        if (!live) continue;
+#pragma unroll
+        for (int i = 0; i < V / kGradSubs + (V % kGradSubs != 0); ++i) {
+            const int v = i * kGradSubs + sub;
+            if (v >= V) break;
+            float sum = fold[0][v][lane];
+#pragma unroll
+            for (int f = 1; f < kGradSubs; ++f) sum += fold[f][v][lane];
+            out[j < W ? static_cast<int64_t>(c0 + v) * W + j : static_cast<int64_t>(W) * P.dim + c0 + v] = sum;
+        }
     }
 }
 
@@ -300,50 +386,41 @@ __global__ void __launch_bounds__(256) conv_state_grad_kernel(ConvBwdLaunch P, i
         if (s + o >= e) break;
         load_v<1, InBf16>(P.x.p, (s + o) * P.x.stride + c, x);
         float g = P.gy.get(s + o, c);
-        if (P.silu) {
-            float p = k.b[0];
-#pragma unroll
-            for (int j = 0; j < W - 1; ++j) p = fmaf(k.w[j][0], win[j][0], p);
-            g = silu_grad(g, fmaf(k.w[W - 1][0], x[0], p));
-        }
+        if (P.silu) g = silu_grad(g, k.at(0, win, x));
 #pragma unroll
         for (int i = o; i < W - 1; ++i) d[i] = fmaf(k.w[i - o][0], g, d[i]);
-#pragma unroll
-        for (int j = 0; j + 1 < W - 1; ++j) win[j][0] = win[j + 1][0];
-        win[W - 2][0] = x[0];
+        shift<W, 1>(win, x);
     }
 #pragma unroll
     for (int i = 0; i < W - 1; ++i) P.dh0[(static_cast<int64_t>(n) * (W - 1) + i) * P.dim + c] = d[i];
 }
 
-bool aligned(const Rows &r, int V) {
-    const int64_t e = r.bf16 ? 2 : 4, a = V * e < 16 ? V * e : 16;
-    return !r.p || (reinterpret_cast<uintptr_t>(r.p) % a == 0 && (r.stride * e) % a == 0);
+// Rows per thread: `most`, or down to 8 where that leaves fewer than 512 workgroups of `lanes` threads across the
+// channels, whose walks would then be what the call waits for.
+int tile_of(int64_t rows, int dim, int V, int lanes, int most) {
+    const int64_t across = (dim + lanes * V - 1) / (lanes * V), tiles = 256 / lanes;
+    int tile = most;
+    while (tile > 8 && (rows + tile * tiles - 1) / (tile * tiles) * across < 512) tile /= 2;
+    return tile;
 }
 
-// Channels per thread: 4 where every access of 4 is aligned, else 1.
-int vector_of(int dim, const Rows *r, int count, const void *h0, const void *hT, bool in_bf16) {
-    bool ok = dim % 4 == 0;
-    for (int i = 0; i < count; ++i) ok = ok && aligned(r[i], 4);
-    const Rows s0{const_cast<void *>(h0), dim, in_bf16}, s1{const_cast<void *>(hT), dim, in_bf16};
-    return ok && aligned(s0, 4) && aligned(s1, 4) ? 4 : 1;
-}
+// Channels per thread where the width has as many.  Forward 4: 32,768 x 4,096 bf16 128 us against 144 with 8,
+// whose taps cost the waves.  Gradients 8 for bf16.
+int vector_of(int dim, int most) { return dim >= most ? most : 1; }
 
-#define KDA_CONV_PICK(KERNEL, GRID, ...)                                                          \
+// KERNEL<W, V, bf16> for the call's width, VB or VF channels per thread (bf16, fp32) or one, and type.
+#define KDA_CONV_PICK(KERNEL, VB, VF, GRID, ...)                                                  \
     do {                                                                                          \
-        if (P.x.bf16) KDA_CONV_W(KERNEL, true, GRID, __VA_ARGS__);                                \
-        else KDA_CONV_W(KERNEL, false, GRID, __VA_ARGS__);                                        \
+        if (P.width == 2) KDA_CONV_W(KERNEL, 2, VB, VF, GRID, __VA_ARGS__);                       \
+        else if (P.width == 3) KDA_CONV_W(KERNEL, 3, VB, VF, GRID, __VA_ARGS__);                  \
+        else KDA_CONV_W(KERNEL, 4, VB, VF, GRID, __VA_ARGS__);                                    \
     } while (0)
-#define KDA_CONV_W(KERNEL, BF, GRID, ...)                                                         \
+#define KDA_CONV_W(KERNEL, W, VB, VF, GRID, ...)                                                  \
     do {                                                                                          \
-        if (P.width == 2) KDA_CONV_V(KERNEL, 2, BF, GRID, __VA_ARGS__);                           \
-        else if (P.width == 3) KDA_CONV_V(KERNEL, 3, BF, GRID, __VA_ARGS__);                      \
-        else KDA_CONV_V(KERNEL, 4, BF, GRID, __VA_ARGS__);                                        \
-    } while (0)
-#define KDA_CONV_V(KERNEL, W, BF, GRID, ...)                                                      \
-    do {                                                                                          \
-        if (V == 4) KERNEL<W, 4, BF><<<GRID, 256, 0, P.stream>>>(__VA_ARGS__);                    \
-        else KERNEL<W, 1, BF><<<GRID, 256, 0, P.stream>>>(__VA_ARGS__);                           \
+        if (P.x.bf16 && V > 1) KERNEL<W, VB, true><<<GRID, 256, 0, P.stream>>>(__VA_ARGS__);      \
+        else if (P.x.bf16) KERNEL<W, 1, true><<<GRID, 256, 0, P.stream>>>(__VA_ARGS__);           \
+        else if (V > 1) KERNEL<W, VF, false><<<GRID, 256, 0, P.stream>>>(__VA_ARGS__);            \
+        else KERNEL<W, 1, false><<<GRID, 256, 0, P.stream>>>(__VA_ARGS__);                        \
     } while (0)
 
 template <typename T>
@@ -370,11 +447,10 @@ int64_t conv_rows(const int32_t *cu, int N, int T) { return cu ? T : static_cast
 
 hipError_t launch_conv_fwd(const ConvLaunch &P) {
     const int64_t rows = conv_rows(P.cu, P.N, P.T);
-    const Rows r[] = {P.x, P.y};
-    const int V = vector_of(P.dim, r, 2, P.h0, nullptr, P.x.bf16);
-    const int cb = (P.dim + 256 * V - 1) / (256 * V);
-    const unsigned grid = static_cast<unsigned>((rows + kConvTile - 1) / kConvTile * cb);
-    if (rows > 0) KDA_CONV_PICK(conv_kernel, grid, P, rows, cb);
+    const int V = vector_of(P.dim, 4), cb = (P.dim + 256 * V - 1) / (256 * V);
+    const int tile = tile_of(rows, P.dim, V, 256, 32);
+    const unsigned grid = static_cast<unsigned>((rows + tile - 1) / tile * cb);
+    if (rows > 0) KDA_CONV_PICK(conv_kernel, 4, 4, grid, P, rows, cb, tile);
     if (P.hT) {
         if (P.x.bf16) launch_state<uint16_t>(P);
         else launch_state<float>(P);
@@ -383,28 +459,37 @@ hipError_t launch_conv_fwd(const ConvLaunch &P) {
 }
 
 hipError_t launch_conv_step(const ConvLaunch &P) {
-    const Rows r[] = {P.x, P.y};
-    const int V = vector_of(P.dim, r, 2, P.h0, P.hT, P.x.bf16);
-    const int cb = (P.dim + 256 * V - 1) / (256 * V);
+    // whole vectors only: a thread moved back over its neighbour's channels could read a state that the neighbour
+    // has already shifted in place
+    const int V = P.dim % 4 == 0 ? 4 : 1, cb = (P.dim + 256 * V - 1) / (256 * V);
     const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(P.N) * cb);
-    KDA_CONV_PICK(conv_step_kernel, grid, P, cb);
+    KDA_CONV_PICK(conv_step_kernel, 4, 4, grid, P, cb);
     return hipGetLastError();
 }
 
-size_t conv_bwd_workspace_bytes(int64_t rows, int dim, int width) {
-    return static_cast<size_t>((rows + kGradTile - 1) / kGradTile) * (width + 1) * dim * 4;
+// How the gradient kernel cuts its rows: 64 to a thread for bf16, 8 channels wide, 16,384 x 4,096 112 us (32: 131).
+struct ConvCut {
+    int V, tile;
+    int64_t parts;  // workgroups along the rows
+};
+static ConvCut conv_cut(int64_t rows, int dim, bool bf16) {
+    const int V = vector_of(dim, bf16 ? 8 : 4), tile = tile_of(rows, dim, V, 256 / kGradSubs, 64);
+    return {V, tile, (rows + tile * kGradSubs - 1) / (tile * kGradSubs)};
+}
+
+size_t conv_bwd_workspace_bytes(int64_t rows, int dim, int width, bool bf16) {
+    return static_cast<size_t>(conv_cut(rows, dim, bf16).parts) * (width + 1) * dim * 4;
 }
 
 hipError_t launch_conv_bwd(const ConvBwdLaunch &P) {
-    const int64_t rows = conv_rows(P.cu, P.N, P.T), tiles = (rows + kGradTile - 1) / kGradTile;
-    const Rows r[] = {P.x, P.gy, P.dx};
-    const int V = vector_of(P.dim, r, 3, P.h0, nullptr, P.x.bf16);
-    const int cb = (P.dim + 256 * V - 1) / (256 * V);
-    if (rows > 0) KDA_CONV_PICK(conv_grad_kernel, static_cast<unsigned>(tiles * cb), P, rows, cb);
+    const int64_t rows = conv_rows(P.cu, P.N, P.T);
+    const ConvCut cut = conv_cut(rows, P.dim, P.x.bf16);
+    const int V = cut.V, cb = (P.dim + 256 / kGradSubs * V - 1) / (256 / kGradSubs * V);
+    if (rows > 0)
+        KDA_CONV_PICK(conv_grad_kernel, 8, 4, static_cast<unsigned>(cut.parts * cb), P, rows, cb, cut.tile);
     const int64_t ld = static_cast<int64_t>(P.width + 1) * P.dim;
-    launch_column_sum(P.ws, ld, static_cast<int>(tiles), static_cast<int64_t>(P.width) * P.dim, P.dw, P.stream);
-    if (P.db)
-        launch_column_sum(P.ws + static_cast<int64_t>(P.width) * P.dim, ld, static_cast<int>(tiles), P.dim, P.db, P.stream);
+    launch_column_sum(P.ws, ld, static_cast<int>(cut.parts), {{P.dw, P.db, nullptr}, {static_cast<int64_t>(P.width) * P.dim, P.dim, 0}},
+                      P.stream);
     if (P.dh0) {
         if (P.x.bf16) launch_state_grad<true>(P);
         else launch_state_grad<false>(P);
