@@ -16,10 +16,11 @@ __all__ += _LAYER
 
 
 def __getattr__(name):
+    if name not in __all__:
+        raise AttributeError(name)
     if name in _LAYER:
-        from . import layer_ops
-        return getattr(layer_ops, name)
-    if name in __all__:
-        from . import ops
-        return getattr(ops, name)
-    raise AttributeError(name)
+        from . import layer_ops as module
+    else:
+        from . import ops as module
+    value = globals()[name] = getattr(module, name)  # found here from now on
+    return value

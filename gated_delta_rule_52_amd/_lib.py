@@ -345,12 +345,15 @@ def dplr_fwd_raw(args: DplrArgs) -> int:
 def layer_raw(name: str, args) -> int:
     """Calls one of LAYER_FUNCTIONS; args.struct_size is set here."""
     args.struct_size = ctypes.sizeof(args)
-    return getattr(load(), name)(ctypes.byref(args))
+    return layer_function(name)(ctypes.byref(args))
 
 
-def layer_workspace(name: str, args) -> int:
-    """A LAYER_FUNCTIONS workspace query; invalid sizes raise."""
-    n = layer_raw(name, args)
-    if n == 2 ** 64 - 1:
-        raise KdaError(STATUS_CODE["KDA_ERR_BAD_SHAPE"], load().kda_last_error().decode())
-    return n
+_layer_functions = {}
+
+
+def layer_function(name: str):
+    """The loaded library's function of this name, looked up once."""
+    fn = _layer_functions.get(name)
+    if fn is None:
+        fn = _layer_functions[name] = getattr(load(), name)
+    return fn

@@ -334,7 +334,7 @@ int rows_of(int dim) {
     return dim <= 128 ? 16 : dim <= 256 ? 8 : dim <= 1024 ? 4 : 1;
 }
 int64_t bwd_groups(int64_t rows, int dim) {
-    const int64_t whole = (rows + rows_of(dim) - 1) / rows_of(dim), most = dim <= 4096 ? 512 : 256;
+    const int64_t whole = (rows + rows_of(dim) - 1) / rows_of(dim), most = dim <= 1024 ? 1024 : dim <= 4096 ? 512 : 256;
     return whole < most ? whole : most;
 }
 

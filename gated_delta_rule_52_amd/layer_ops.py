@@ -4,41 +4,71 @@ state space scan, short causal convolution and layer norm.
 As in ops.py, torch supplies device memory and the current HIP stream and every
 step runs in libkda.so.  Token tensors may be column slices of wider ones: the
 last dimension must be dense and the rows equally spaced.
+
+A decode step's kernels take a few microseconds, so the checks here look at a
+tensor once, in one condition, and work out what was wrong only where it fails;
+argument structs are filled by position, in the order of their fields.
 """
 from __future__ import annotations
 
-import contextlib
+import ctypes
 from typing import Optional
 
 import torch
 
 from . import _lib
-from .ops import _DT, _need, _ptr, _stream
+from .ops import _DT
 
 F32 = torch.float32
+_TOO_BIG = 2 ** 64 - 1
 
 
-def _dtype(t: torch.Tensor, name: str) -> torch.dtype:
-    if t.dtype not in _DT:
-        raise ValueError(f"unsupported {name} dtype {t.dtype}")
-    return t.dtype
-
-
-def _rows(t: torch.Tensor, name: str, shape, dtype=None, device=None) -> int:
-    """Checks a token tensor and returns the distance between its rows in elements."""
+def _refuse(t, name, shape, dtype, device):
+    """The reason why a tensor failed its check."""
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} must be a tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
-    if device is not None and t.device != device:
+    if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if t.shape != tuple(shape):
+    if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if dtype is not None and t.dtype != dtype:
+    if t.dtype != dtype:
         raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    width, strides = shape[-1], t.stride()
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _kind(t, name: str) -> int:
+    """The C dtype of a tensor, or of None as fp32."""
+    if t is None:
+        return _lib.KDA_DTYPE_FP32
+    kind = _DT.get(t.dtype)
+    if kind is None:
+        raise ValueError(f"unsupported {name} dtype {t.dtype}")
+    return kind
+
+
+def _first(t, name: str, dims) -> torch.device:
+    """Checks the tensor that sets a call's device."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.dim() not in dims:
+        raise ValueError(f"{name} has {t.dim()} dimensions, expected {' or '.join(map(str, dims))}")
+    return t.device
+
+
+def _step(t, name, shape, dtype, device) -> int:
+    """Checks a token tensor (None: 0) and returns the distance between its rows in elements."""
+    if t is None:
+        return 0
+    if t.dtype is not dtype or t.shape != shape or t.device != device:
+        _refuse(t, name, shape, dtype, device)
+    width = shape[-1]
+    if t.is_contiguous():
+        return width
+    strides = t.stride()
     if width != 1 and strides[-1] != 1:
         raise ValueError(f"{name} must be dense along its last dimension")
-    if t.numel() == 0:
-        return width
     step, span = 0, 1  # of the innermost leading dimension with more than one entry, and the rows inside
     for size, stride in zip(reversed(shape[:-1]), reversed(strides[:-1])):
         if size == 1:
@@ -51,93 +81,118 @@ def _rows(t: torch.Tensor, name: str, shape, dtype=None, device=None) -> int:
     return step if span > 1 else width
 
 
-def _opt(t, name, shape, dtype, device) -> int:
-    return 0 if t is None else _rows(t, name, shape, dtype, device)
+def _at(t, name, shape, dtype, device):
+    """Checks a contiguous tensor (or None) and returns its address."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or tuple(t.shape) != shape or t.device != device or not t.is_contiguous():
+        _refuse(t, name, shape, dtype, device)
+    return t.data_ptr()
 
 
-def _param(t: Optional[torch.Tensor], name, shape, dtype, device):
-    if t is not None:
-        _need(t, name, shape, dtype)
-        if t.device != device:
-            raise ValueError(f"{name} is on {t.device}, expected {device}")
+def _ptr(t):
+    return None if t is None else t.data_ptr()
 
 
-def _on(device):
-    """Makes `device` current for a launch where it is not."""
-    return contextlib.nullcontext() if torch.cuda.current_device() == device.index else torch.cuda.device(device)
-
-
-def _sequences(x, cu_seqlens, device) -> int:
+def _sequences(batch: int, cu_seqlens, device):
+    """(number of sequences, address of the offsets)"""
     if cu_seqlens is None:
-        return x.shape[0]
-    _need(cu_seqlens, "cu_seqlens", (cu_seqlens.numel(),), torch.int32)
-    if cu_seqlens.device != device:
-        raise ValueError(f"cu_seqlens is on {cu_seqlens.device}, expected {device}")
-    return cu_seqlens.numel() - 1
+        return batch, None
+    return cu_seqlens.numel() - 1, _at(cu_seqlens, "cu_seqlens", (cu_seqlens.numel(),), torch.int32, device)
 
 
-def _workspace(given, need: int, device):
-    if need > 0 and (given is None or given.numel() * given.element_size() < need):
-        return torch.empty(need, dtype=torch.uint8, device=device)
-    return given
+def _stream(device) -> int:
+    # the address alone, without a Stream object around it (1.8 us of a decode step's 14)
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _call(name: str, args, device):
-    args.stream = _stream(device)
-    with _on(device):
-        _lib.check(_lib.layer_raw(name, args))
+    if torch.cuda.current_device() == device.index:
+        status = _lib.layer_function(name)(ctypes.byref(args))
+    else:  # a launch goes to the current device
+        with torch.cuda.device(device):
+            status = _lib.layer_function(name)(ctypes.byref(args))
+    if status:
+        _lib.check(status)
+
+
+def _size(name: str, args) -> int:
+    """A workspace query; invalid sizes raise."""
+    need = _lib.layer_function(name)(ctypes.byref(args))
+    if need == _TOO_BIG:
+        raise _lib.KdaError(_lib.STATUS_CODE["KDA_ERR_BAD_SHAPE"], _lib.load().kda_last_error().decode())
+    return need
+
+
+def _give_workspace(name: str, args, workspace, device):
+    """Puts a workspace of the size the call asks for into args; returns what holds it."""
+    need = _size(name, args)
+    if need:
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        elif workspace.device != device or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on the call's device")
+        elif workspace.numel() * workspace.element_size() < need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        args.workspace, args.workspace_bytes = workspace.data_ptr(), need
+    return workspace
+
+
+def _grad_dtype(dtype) -> int:
+    kind = _DT.get(dtype)
+    if kind is None:
+        raise ValueError(f"unsupported grad_dtype {dtype}")
+    return kind
 
 
 # ---- selective scan ------------------------------------------------------------------------------------
 
-def _scan_shapes(u, A, B):
-    if u.dim() not in (2, 3) or A.dim() != 2:
-        raise ValueError("u must be [B,T,D] (or [N,D] for a step) and A [D,ds]")
-    return tuple(u.shape), (*u.shape[:-1], A.shape[1]), u.shape[-1], A.shape[1]
-
-
-def _scan_args(a, u, dt, A, B, C, D, z, dt_bias, initial_state, cu_seqlens, dt_softplus):
-    """Checks and fills what the scan's three entry points share; returns (device, N, dim, ds)."""
-    wide, narrow, dim, ds = _scan_shapes(u, A, B)
-    dtype, device = _dtype(u, "u"), u.device
-    a.u_stride = _rows(u, "u", wide)
-    a.dt_stride = _rows(dt, "dt", wide, dtype, device)
-    a.B_stride = _rows(B, "B", narrow, dtype, device)
-    a.C_stride = _rows(C, "C", narrow, dtype, device)
-    a.z_stride = _opt(z, "z", wide, dtype, device)
-    _param(A, "A", (dim, ds), F32, device)
-    _param(D, "D", (dim,), F32, device)
-    _param(dt_bias, "dt_bias", (dim,), F32, device)
-    N = _sequences(u, cu_seqlens, device)
-    _param(initial_state, "initial_state", (N, dim, ds), F32, device)
-    a.u, a.dt, a.A, a.B, a.C = _ptr(u), _ptr(dt), _ptr(A), _ptr(B), _ptr(C)
-    a.D, a.z, a.dt_bias = _ptr(D), _ptr(z), _ptr(dt_bias)
-    a.initial_state, a.cu_seqlens = _ptr(initial_state), _ptr(cu_seqlens)
-    a.batch, a.T = wide[0], wide[1] if len(wide) == 3 else 1
-    a.dim, a.ds, a.num_seqs = dim, ds, N
-    a.in_dtype = _DT[dtype]
-    a.flags = _lib.KDA_SCAN_DT_SOFTPLUS if dt_softplus else 0
-    return device, N, dim, ds
-
-
-def _scan_sizes(a, u, ds, cu_seqlens):
-    a.batch, a.T, a.dim, a.ds = u.shape[0], u.shape[1], u.shape[2], ds
-    a.num_seqs = u.shape[0] if cu_seqlens is None else cu_seqlens.numel() - 1
-    a.cu_seqlens = _ptr(cu_seqlens)
-    a.in_dtype = _DT[_dtype(u, "u")]
+def _scan_sizes(struct, u, ds, cu_seqlens):
+    device = _first(u, "u", (3,))
+    N, cu = _sequences(u.shape[0], cu_seqlens, device)
+    a = struct()
+    a.struct_size, a.cu_seqlens = ctypes.sizeof(struct), cu
+    a.batch, a.T, a.dim, a.ds, a.num_seqs = u.shape[0], u.shape[1], u.shape[2], ds, N
+    a.in_dtype = _kind(u, "u")
     return a
 
 
 def selective_scan_fwd_workspace_bytes(u: torch.Tensor, ds: int, cu_seqlens: Optional[torch.Tensor] = None) -> int:
     """Bytes that ``selective_scan_fwd`` needs for u [B,T,D] and ds states per channel."""
-    return _lib.layer_workspace("kda_selective_scan_fwd_workspace_bytes",
-                                _scan_sizes(_lib.SelectiveScanArgs(), u, ds, cu_seqlens))
+    return _size("kda_selective_scan_fwd_workspace_bytes", _scan_sizes(_lib.SelectiveScanArgs, u, ds, cu_seqlens))
 
 
 def selective_scan_bwd_workspace_bytes(u: torch.Tensor, ds: int, cu_seqlens: Optional[torch.Tensor] = None) -> int:
     """Bytes that ``selective_scan_bwd`` needs for u [B,T,D] and ds states per channel."""
-    return _lib.layer_workspace("kda_selective_scan_bwd_workspace_bytes",
-                                _scan_sizes(_lib.SelectiveScanBwdArgs(), u, ds, cu_seqlens))
+    return _size("kda_selective_scan_bwd_workspace_bytes", _scan_sizes(_lib.SelectiveScanBwdArgs, u, ds, cu_seqlens))
+
+
+def _scan(u, dt, A, B, C, D, z, dt_bias, initial_state, cu_seqlens, dt_softplus, out_dtype, final_state,
+          output_final_state, y):
+    """Checks and fills the arguments of the scan's forward and step; returns (args, y, final state, device)."""
+    device = _first(u, "u", (2, 3))
+    shape, dtype = u.shape, u.dtype
+    kind = _kind(u, "u")
+    if A.dim() != 2:
+        raise ValueError("A must be [D,ds]")
+    dim, ds = shape[-1], A.shape[1]
+    narrow = shape[:-1] + (ds,)
+    N, cu = _sequences(shape[0], cu_seqlens, device)
+    if final_state is None and output_final_state:
+        final_state = torch.empty((N, dim, ds), dtype=F32, device=device)
+    if y is None:
+        y = torch.empty(shape, dtype=out_dtype or dtype, device=device)
+    a = _lib.SelectiveScanArgs(
+        ctypes.sizeof(_lib.SelectiveScanArgs), u.data_ptr(), dt.data_ptr(), _at(A, "A", (dim, ds), F32, device),
+        B.data_ptr(), C.data_ptr(), _at(D, "D", (dim,), F32, device), _ptr(z),
+        _at(dt_bias, "dt_bias", (dim,), F32, device), _at(initial_state, "initial_state", (N, dim, ds), F32, device),
+        _at(final_state, "final_state", (N, dim, ds), F32, device), y.data_ptr(), cu,
+        _step(u, "u", shape, dtype, device), _step(dt, "dt", shape, dtype, device),
+        _step(B, "B", narrow, dtype, device), _step(C, "C", narrow, dtype, device),
+        _step(z, "z", shape, dtype, device), _step(y, "y", shape, out_dtype or y.dtype, device),
+        shape[0], shape[1] if len(shape) == 3 else 1, dim, ds, N, kind, _kind(y, "y"), None, 0, _stream(device),
+        _lib.KDA_SCAN_DT_SOFTPLUS if dt_softplus else 0)
+    return a, y, final_state, device
 
 
 def selective_scan_fwd(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.Tensor, C: torch.Tensor,
@@ -157,20 +212,11 @@ def selective_scan_fwd(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: to
     tensor for packed input (B == 1); rows at and behind its last offset are
     left as they were.  ``final_state`` may be ``initial_state``.  Returns
     (y [B,T,D], final_state or None)."""
-    a = _lib.SelectiveScanArgs()
     if u.dim() != 3:
         raise ValueError("u must be [B,T,D]")
-    device, N, dim, ds = _scan_args(a, u, dt, A, B, C, D, z, dt_bias, initial_state, cu_seqlens, dt_softplus)
-    if final_state is None and output_final_state:
-        final_state = torch.empty((N, dim, ds), dtype=F32, device=device)
-    _param(final_state, "final_state", (N, dim, ds), F32, device)
-    if y is None:
-        y = torch.empty(u.shape, dtype=out_dtype or u.dtype, device=device)
-    a.y_stride = _rows(y, "y", u.shape, out_dtype, device)
-    a.y, a.final_state, a.out_dtype = _ptr(y), _ptr(final_state), _DT[_dtype(y, "y")]
-    need = _lib.layer_workspace("kda_selective_scan_fwd_workspace_bytes", a)
-    workspace = _workspace(workspace, need, device)
-    a.workspace, a.workspace_bytes = (_ptr(workspace), need) if need else (None, 0)
+    a, y, final_state, device = _scan(u, dt, A, B, C, D, z, dt_bias, initial_state, cu_seqlens, dt_softplus, out_dtype,
+                                      final_state, output_final_state, y)
+    held = _give_workspace("kda_selective_scan_fwd_workspace_bytes", a, workspace, device)  # noqa: F841
     _call("kda_selective_scan_fwd", a, device)
     return y, final_state
 
@@ -183,19 +229,13 @@ def selective_scan_step(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: t
     """One token of ``selective_scan_fwd`` for N sequences: u, dt, z [N,D], B, C
     [N,ds], state [N,D,ds] fp32 (or None for zeros).  The new state is written
     to ``final_state`` (default: ``state`` itself, in place).  Returns y [N,D]."""
-    a = _lib.SelectiveScanArgs()
     if u.dim() != 2:
         raise ValueError("u must be [N,D]")
-    device, N, dim, ds = _scan_args(a, u, dt, A, B, C, D, z, dt_bias, state, None, dt_softplus)
     if final_state is None:
         if state is None:
             raise ValueError("final_state is required when state is None")
         final_state = state
-    _param(final_state, "final_state", (N, dim, ds), F32, device)
-    if y is None:
-        y = torch.empty(u.shape, dtype=out_dtype or u.dtype, device=device)
-    a.y_stride = _rows(y, "y", u.shape, out_dtype, device)
-    a.y, a.final_state, a.out_dtype = _ptr(y), _ptr(final_state), _DT[_dtype(y, "y")]
+    a, y, _, device = _scan(u, dt, A, B, C, D, z, dt_bias, state, None, dt_softplus, out_dtype, final_state, False, y)
     _call("kda_selective_scan_step", a, device)
     return y
 
@@ -214,60 +254,69 @@ def selective_scan_bwd(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: to
     du, ddt, dB, dC, dz (their rows may be strided, as column slices of one
     buffer); ``grad_initial_state`` may be ``initial_state`` or
     ``grad_final_state``."""
-    a = _lib.SelectiveScanBwdArgs()
-    if u.dim() != 3:
-        raise ValueError("u must be [B,T,D]")
-    device, N, dim, ds = _scan_args(a, u, dt, A, B, C, D, z, dt_bias, initial_state, cu_seqlens, dt_softplus)
-    a.grad_y_stride = _rows(grad_y, "grad_y", u.shape, u.dtype, device)
-    _param(grad_final_state, "grad_final_state", (N, dim, ds), F32, device)
+    device = _first(u, "u", (3,))
+    shape, dtype = u.shape, u.dtype
+    kind, grad_kind = _kind(u, "u"), _grad_dtype(grad_dtype)
+    if A.dim() != 2:
+        raise ValueError("A must be [D,ds]")
+    dim, ds = shape[-1], A.shape[1]
+    narrow = shape[:-1] + (ds,)
+    N, cu = _sequences(shape[0], cu_seqlens, device)
+    states = (N, dim, ds)
     if grad_initial_state is None and output_grad_initial_state:
-        grad_initial_state = torch.empty((N, dim, ds), dtype=F32, device=device)
-    _param(grad_initial_state, "grad_initial_state", (N, dim, ds), F32, device)
-    if grad_dtype not in _DT:
-        raise ValueError(f"unsupported grad_dtype {grad_dtype}")
-    got = {}
-    for name, like in (("du", u), ("ddt", u), ("dB", B), ("dC", B), ("dz", z)):
-        if like is None:
-            got[name] = None
-            continue
-        t = out[name] if out is not None else torch.empty(like.shape, dtype=grad_dtype, device=device)
-        got[name] = t
-        stride = _rows(t, name, like.shape, grad_dtype, device)
-        field = "grad_" + name[1:]
-        setattr(a, field, t.data_ptr())
-        setattr(a, field + "_stride", stride)
-    got["dA"] = torch.empty((dim, ds), dtype=F32, device=device)
-    got["dD"] = None if D is None else torch.empty((dim,), dtype=F32, device=device)
-    got["ddt_bias"] = None if dt_bias is None else torch.empty((dim,), dtype=F32, device=device)
-    got["dh0"] = grad_initial_state
-    a.grad_y, a.grad_final_state, a.grad_initial_state = _ptr(grad_y), _ptr(grad_final_state), _ptr(grad_initial_state)
-    a.grad_A, a.grad_D, a.grad_dt_bias = _ptr(got["dA"]), _ptr(got["dD"]), _ptr(got["ddt_bias"])
-    a.grad_dtype = _DT[grad_dtype]
-    need = _lib.layer_workspace("kda_selective_scan_bwd_workspace_bytes", a)
-    workspace = _workspace(workspace, need, device)
-    a.workspace, a.workspace_bytes = _ptr(workspace), need
+        grad_initial_state = torch.empty(states, dtype=F32, device=device)
+    if out is None:
+        new = lambda s: torch.empty(s, dtype=grad_dtype, device=device)  # noqa: E731
+        out = dict(du=new(shape), ddt=new(shape), dB=new(narrow), dC=new(narrow), dz=None if z is None else new(shape))
+    got = dict(du=out["du"], ddt=out["ddt"], dB=out["dB"], dC=out["dC"], dz=None if z is None else out["dz"],
+               dA=torch.empty((dim, ds), dtype=F32, device=device),
+               dD=None if D is None else torch.empty((dim,), dtype=F32, device=device),
+               ddt_bias=None if dt_bias is None else torch.empty((dim,), dtype=F32, device=device),
+               dh0=grad_initial_state)
+    grads = (got["du"], got["ddt"], got["dB"], got["dC"], got["dz"])
+    steps = [_step(t, n, s, grad_dtype, device) for t, n, s in
+             zip(grads, ("du", "ddt", "dB", "dC", "dz"), (shape, shape, narrow, narrow, shape))]
+    a = _lib.SelectiveScanBwdArgs(
+        ctypes.sizeof(_lib.SelectiveScanBwdArgs), u.data_ptr(), dt.data_ptr(), _at(A, "A", (dim, ds), F32, device),
+        B.data_ptr(), C.data_ptr(), _at(D, "D", (dim,), F32, device), _ptr(z),
+        _at(dt_bias, "dt_bias", (dim,), F32, device), _at(initial_state, "initial_state", states, F32, device),
+        grad_y.data_ptr(), _at(grad_final_state, "grad_final_state", states, F32, device),
+        got["du"].data_ptr(), got["ddt"].data_ptr(), got["dA"].data_ptr(), got["dB"].data_ptr(), got["dC"].data_ptr(),
+        _ptr(got["dD"]), _ptr(got["dz"]), _ptr(got["ddt_bias"]),
+        _at(grad_initial_state, "grad_initial_state", states, F32, device), cu,
+        _step(u, "u", shape, dtype, device), _step(dt, "dt", shape, dtype, device),
+        _step(B, "B", narrow, dtype, device), _step(C, "C", narrow, dtype, device),
+        _step(z, "z", shape, dtype, device), _step(grad_y, "grad_y", shape, dtype, device), *steps,
+        shape[0], shape[1], dim, ds, N, kind, grad_kind, None, 0, _stream(device),
+        _lib.KDA_SCAN_DT_SOFTPLUS if dt_softplus else 0)
+    held = _give_workspace("kda_selective_scan_bwd_workspace_bytes", a, workspace, device)  # noqa: F841
     _call("kda_selective_scan_bwd", a, device)
     return got
 
 
 # ---- short convolution ---------------------------------------------------------------------------------
 
-def _conv_args(a, x, weight, bias, initial_state, cu_seqlens, silu):
-    if x.dim() not in (2, 3) or weight.dim() != 2:
-        raise ValueError("x must be [B,T,D] (or [N,D] for a step) and weight [D,W]")
-    dtype, device, dim, width = _dtype(x, "x"), x.device, x.shape[-1], weight.shape[1]
-    a.x_stride = _rows(x, "x", x.shape)
-    _param(weight, "weight", (dim, width), _dtype(weight, "weight"), device)
-    _param(bias, "bias", (dim,), weight.dtype, device)
-    N = _sequences(x, cu_seqlens, device)
-    _param(initial_state, "initial_state", (N, width - 1, dim), dtype, device)
-    a.x, a.weight, a.bias = _ptr(x), _ptr(weight), _ptr(bias)
-    a.initial_state, a.cu_seqlens = _ptr(initial_state), _ptr(cu_seqlens)
-    a.batch, a.T = x.shape[0], x.shape[1] if x.dim() == 3 else 1
-    a.dim, a.width, a.num_seqs = dim, width, N
-    a.in_dtype, a.w_dtype = _DT[dtype], _DT[weight.dtype]
-    a.flags = _lib.KDA_CONV_SILU if silu else 0
-    return device, N, dim, width
+def _conv(x, weight, bias, initial_state, cu_seqlens, silu, out_dtype, final_state, output_final_state, y):
+    """Checks and fills the arguments of the convolution's forward and step; returns (args, y, final state, device)."""
+    device = _first(x, "x", (2, 3))
+    shape, dtype = x.shape, x.dtype
+    kind = _kind(x, "x")
+    if weight.dim() != 2:
+        raise ValueError("weight must be [D,W]")
+    dim, width = shape[-1], weight.shape[1]
+    N, cu = _sequences(shape[0], cu_seqlens, device)
+    states = (N, width - 1, dim)
+    if final_state is None and output_final_state:
+        final_state = torch.empty(states, dtype=dtype, device=device)
+    if y is None:
+        y = torch.empty(shape, dtype=out_dtype or dtype, device=device)
+    a = _lib.ShortConvArgs(
+        ctypes.sizeof(_lib.ShortConvArgs), x.data_ptr(), _at(weight, "weight", (dim, width), weight.dtype, device),
+        _at(bias, "bias", (dim,), weight.dtype, device), _at(initial_state, "initial_state", states, dtype, device),
+        _at(final_state, "final_state", states, dtype, device), y.data_ptr(), cu, _step(x, "x", shape, dtype, device),
+        _step(y, "y", shape, out_dtype or y.dtype, device), shape[0], shape[1] if len(shape) == 3 else 1, dim, width, N,
+        kind, _kind(y, "y"), _kind(weight, "weight"), _stream(device), _lib.KDA_CONV_SILU if silu else 0)
+    return a, y, final_state, device
 
 
 def short_conv_fwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None,
@@ -281,17 +330,10 @@ def short_conv_fwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.T
     inputs, oldest first (None: zeros).  cu_seqlens as in
     ``selective_scan_fwd``.  ``final_state`` may be ``initial_state``.  Returns
     (y, final_state or None)."""
-    a = _lib.ShortConvArgs()
     if x.dim() != 3:
         raise ValueError("x must be [B,T,D]")
-    device, N, dim, width = _conv_args(a, x, weight, bias, initial_state, cu_seqlens, silu)
-    if final_state is None and output_final_state:
-        final_state = torch.empty((N, width - 1, dim), dtype=x.dtype, device=device)
-    _param(final_state, "final_state", (N, width - 1, dim), x.dtype, device)
-    if y is None:
-        y = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=device)
-    a.y_stride = _rows(y, "y", x.shape, out_dtype, device)
-    a.y, a.final_state, a.out_dtype = _ptr(y), _ptr(final_state), _DT[_dtype(y, "y")]
+    a, y, final_state, device = _conv(x, weight, bias, initial_state, cu_seqlens, silu, out_dtype, final_state,
+                                      output_final_state, y)
     _call("kda_short_conv_fwd", a, device)
     return y, final_state
 
@@ -303,31 +345,26 @@ def short_conv_step(x: torch.Tensor, weight: torch.Tensor, state: Optional[torch
     """One token of ``short_conv_fwd`` for N sequences: x [N,D], state [N,W-1,D]
     (or None for zeros).  The shifted state is written to ``final_state``
     (default: ``state`` itself, in place).  Returns y [N,D]."""
-    a = _lib.ShortConvArgs()
     if x.dim() != 2:
         raise ValueError("x must be [N,D]")
-    device, N, dim, width = _conv_args(a, x, weight, bias, state, None, silu)
     if final_state is None:
         if state is None:
             raise ValueError("final_state is required when state is None")
         final_state = state
-    _param(final_state, "final_state", (N, width - 1, dim), x.dtype, device)
-    if y is None:
-        y = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=device)
-    a.y_stride = _rows(y, "y", x.shape, out_dtype, device)
-    a.y, a.final_state, a.out_dtype = _ptr(y), _ptr(final_state), _DT[_dtype(y, "y")]
+    a, y, _, device = _conv(x, weight, bias, state, None, silu, out_dtype, final_state, False, y)
     _call("kda_short_conv_step", a, device)
     return y
 
 
 def short_conv_bwd_workspace_bytes(x: torch.Tensor, width: int, cu_seqlens: Optional[torch.Tensor] = None) -> int:
     """Bytes that ``short_conv_bwd`` needs for x [B,T,D] and `width` taps."""
+    device = _first(x, "x", (3,))
     a = _lib.ShortConvBwdArgs()
+    a.struct_size = ctypes.sizeof(a)
+    a.num_seqs, a.cu_seqlens = _sequences(x.shape[0], cu_seqlens, device)
     a.batch, a.T, a.dim, a.width = x.shape[0], x.shape[1], x.shape[2], width
-    a.num_seqs = x.shape[0] if cu_seqlens is None else cu_seqlens.numel() - 1
-    a.cu_seqlens = _ptr(cu_seqlens)
-    a.in_dtype = _DT[_dtype(x, "x")]
-    return _lib.layer_workspace("kda_short_conv_bwd_workspace_bytes", a)
+    a.in_dtype = _kind(x, "x")
+    return _size("kda_short_conv_bwd_workspace_bytes", a)
 
 
 def short_conv_bwd(x: torch.Tensor, weight: torch.Tensor, grad_y: torch.Tensor, bias: Optional[torch.Tensor] = None,
@@ -340,27 +377,29 @@ def short_conv_bwd(x: torch.Tensor, weight: torch.Tensor, grad_y: torch.Tensor, 
     ``grad_dtype`` (``out`` may supply it), dweight, dbias (None without a bias)
     and dh0 [N,W-1,D] in fp32 (``grad_initial_state`` may be
     ``grad_final_state``)."""
-    a = _lib.ShortConvBwdArgs()
-    if x.dim() != 3:
-        raise ValueError("x must be [B,T,D]")
-    device, N, dim, width = _conv_args(a, x, weight, bias, initial_state, cu_seqlens, silu)
-    a.grad_y_stride = _rows(grad_y, "grad_y", x.shape, x.dtype, device)
-    _param(grad_final_state, "grad_final_state", (N, width - 1, dim), F32, device)
+    device = _first(x, "x", (3,))
+    shape, dtype = x.shape, x.dtype
+    kind, grad_kind = _kind(x, "x"), _grad_dtype(grad_dtype)
+    if weight.dim() != 2:
+        raise ValueError("weight must be [D,W]")
+    dim, width = shape[-1], weight.shape[1]
+    N, cu = _sequences(shape[0], cu_seqlens, device)
+    states = (N, width - 1, dim)
     if grad_initial_state is None and output_grad_initial_state:
-        grad_initial_state = torch.empty((N, width - 1, dim), dtype=F32, device=device)
-    _param(grad_initial_state, "grad_initial_state", (N, width - 1, dim), F32, device)
-    if grad_dtype not in _DT:
-        raise ValueError(f"unsupported grad_dtype {grad_dtype}")
-    dx = out["dx"] if out is not None else torch.empty(x.shape, dtype=grad_dtype, device=device)
-    a.grad_x_stride = _rows(dx, "dx", x.shape, grad_dtype, device)
+        grad_initial_state = torch.empty(states, dtype=F32, device=device)
+    dx = out["dx"] if out is not None else torch.empty(shape, dtype=grad_dtype, device=device)
     got = dict(dx=dx, dweight=torch.empty((dim, width), dtype=F32, device=device),
                dbias=None if bias is None else torch.empty((dim,), dtype=F32, device=device), dh0=grad_initial_state)
-    a.grad_y, a.grad_final_state, a.grad_initial_state = _ptr(grad_y), _ptr(grad_final_state), _ptr(grad_initial_state)
-    a.grad_x, a.grad_weight, a.grad_bias = _ptr(dx), _ptr(got["dweight"]), _ptr(got["dbias"])
-    a.grad_dtype = _DT[grad_dtype]
-    need = _lib.layer_workspace("kda_short_conv_bwd_workspace_bytes", a)
-    workspace = _workspace(workspace, need, device)
-    a.workspace, a.workspace_bytes = _ptr(workspace), need
+    a = _lib.ShortConvBwdArgs(
+        ctypes.sizeof(_lib.ShortConvBwdArgs), x.data_ptr(), _at(weight, "weight", (dim, width), weight.dtype, device),
+        _at(bias, "bias", (dim,), weight.dtype, device), _at(initial_state, "initial_state", states, dtype, device),
+        grad_y.data_ptr(), _at(grad_final_state, "grad_final_state", states, F32, device), dx.data_ptr(),
+        got["dweight"].data_ptr(), _ptr(got["dbias"]),
+        _at(grad_initial_state, "grad_initial_state", states, F32, device), cu, _step(x, "x", shape, dtype, device),
+        _step(grad_y, "grad_y", shape, dtype, device), _step(dx, "dx", shape, grad_dtype, device), shape[0], shape[1],
+        dim, width, N, kind, grad_kind, _kind(weight, "weight"), None, 0, _stream(device),
+        _lib.KDA_CONV_SILU if silu else 0)
+    held = _give_workspace("kda_short_conv_bwd_workspace_bytes", a, workspace, device)  # noqa: F841
     _call("kda_short_conv_bwd", a, device)
     return got
 
@@ -375,26 +414,22 @@ def layer_norm_fwd(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias:
     bias [D] share a dtype.  With ``residual`` [..., D] (bf16 or fp32) x +
     residual is normalised and also returned, in the residual's dtype
     (``residual_out`` may be ``residual``).  Returns y, or (y, residual_out)."""
-    a = _lib.LayerNormArgs()
-    dtype, device, dim = _dtype(x, "x"), x.device, x.shape[-1]
-    a.x_stride = _rows(x, "x", x.shape)
+    device = _first(x, "x", range(1, 9))
+    shape, dtype, dim = x.shape, x.dtype, x.shape[-1]
+    kind = _kind(x, "x")
     w = weight if weight is not None else bias
-    wd = F32 if w is None else _dtype(w, "weight")
-    _param(weight, "weight", (dim,), wd, device)
-    _param(bias, "bias", (dim,), wd, device)
+    wd = F32 if w is None else w.dtype
     if y is None:
-        y = torch.empty(x.shape, dtype=out_dtype or dtype, device=device)
-    a.y_stride = _rows(y, "y", x.shape, out_dtype, device)
-    if residual is not None:
-        rd = _dtype(residual, "residual")
-        a.residual_stride = _rows(residual, "residual", x.shape, rd, device)
-        if residual_out is None:
-            residual_out = torch.empty(x.shape, dtype=rd, device=device)
-        a.residual_out_stride = _rows(residual_out, "residual_out", x.shape, rd, device)
-        a.residual, a.residual_out, a.res_dtype = _ptr(residual), _ptr(residual_out), _DT[rd]
-    a.x, a.weight, a.bias, a.y = _ptr(x), _ptr(weight), _ptr(bias), _ptr(y)
-    a.rows, a.dim, a.eps = x.numel() // dim if dim else 0, dim, eps
-    a.x_dtype, a.w_dtype, a.out_dtype = _DT[dtype], _DT[wd], _DT[_dtype(y, "y")]
+        y = torch.empty(shape, dtype=out_dtype or dtype, device=device)
+    if residual is not None and residual_out is None:
+        residual_out = torch.empty(shape, dtype=residual.dtype, device=device)
+    rd = F32 if residual is None else residual.dtype
+    a = _lib.LayerNormArgs(
+        ctypes.sizeof(_lib.LayerNormArgs), x.data_ptr(), _ptr(residual), _at(weight, "weight", (dim,), wd, device),
+        _at(bias, "bias", (dim,), wd, device), y.data_ptr(), _ptr(residual_out), _step(x, "x", shape, dtype, device),
+        _step(residual, "residual", shape, rd, device), _step(y, "y", shape, out_dtype or y.dtype, device),
+        _step(residual_out, "residual_out", shape, rd, device), x.numel() // dim if dim else 0, dim, eps, kind,
+        _kind(residual, "residual"), _kind(w, "weight"), _kind(y, "y"), _stream(device))
     _call("kda_layer_norm_fwd", a, device)
     return y if residual is None else (y, residual_out)
 
@@ -402,10 +437,11 @@ def layer_norm_fwd(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias:
 def layer_norm_bwd_workspace_bytes(x: torch.Tensor) -> int:
     """Bytes that ``layer_norm_bwd`` needs for x [..., D] with a weight or bias gradient."""
     a = _lib.LayerNormBwdArgs()
+    a.struct_size = ctypes.sizeof(a)
     a.dim = x.shape[-1]
     a.rows = x.numel() // a.dim if a.dim else 0
     a.grad_weight = 1
-    return _lib.layer_workspace("kda_layer_norm_bwd_workspace_bytes", a)
+    return _size("kda_layer_norm_bwd_workspace_bytes", a)
 
 
 def layer_norm_bwd(x: torch.Tensor, grad_y: torch.Tensor, weight: Optional[torch.Tensor] = None,
@@ -419,29 +455,24 @@ def layer_norm_bwd(x: torch.Tensor, grad_y: torch.Tensor, weight: Optional[torch
     dx in ``grad_dtype`` (``out`` may supply it; with a residual it is the
     gradient of both summands), dweight and dbias [D] fp32 (None where the
     parameter is None)."""
-    a = _lib.LayerNormBwdArgs()
-    dtype, device, dim = _dtype(x, "x"), x.device, x.shape[-1]
-    a.x_stride = _rows(x, "x", x.shape)
-    a.grad_y_stride = _rows(grad_y, "grad_y", x.shape, _dtype(grad_y, "grad_y"), device)
+    device = _first(x, "x", range(1, 9))
+    shape, dtype, dim = x.shape, x.dtype, x.shape[-1]
+    kind, grad_kind = _kind(x, "x"), _grad_dtype(grad_dtype)
     w = weight if weight is not None else bias
-    wd = F32 if w is None else _dtype(w, "weight")
-    _param(weight, "weight", (dim,), wd, device)
-    _param(bias, "bias", (dim,), wd, device)
-    if grad_residual is not None:
-        a.grad_residual_stride = _rows(grad_residual, "grad_residual", x.shape, _dtype(grad_residual, "grad_residual"), device)
-        a.grad_residual, a.res_dtype = _ptr(grad_residual), _DT[grad_residual.dtype]
-    if grad_dtype not in _DT:
-        raise ValueError(f"unsupported grad_dtype {grad_dtype}")
-    dx = out["dx"] if out is not None else torch.empty(x.shape, dtype=grad_dtype, device=device)
-    a.grad_x_stride = _rows(dx, "dx", x.shape, grad_dtype, device)
+    wd = F32 if w is None else w.dtype
+    gd = grad_y.dtype
+    rd = F32 if grad_residual is None else grad_residual.dtype
+    dx = out["dx"] if out is not None else torch.empty(shape, dtype=grad_dtype, device=device)
     got = dict(dx=dx, dweight=None if weight is None else torch.empty((dim,), dtype=F32, device=device),
                dbias=None if bias is None else torch.empty((dim,), dtype=F32, device=device))
-    a.x, a.grad_y, a.weight = _ptr(x), _ptr(grad_y), _ptr(weight)
-    a.grad_x, a.grad_weight, a.grad_bias = _ptr(dx), _ptr(got["dweight"]), _ptr(got["dbias"])
-    a.rows, a.dim, a.eps = x.numel() // dim if dim else 0, dim, eps
-    a.x_dtype, a.gy_dtype, a.w_dtype, a.grad_dtype = _DT[dtype], _DT[grad_y.dtype], _DT[wd], _DT[grad_dtype]
-    need = _lib.layer_workspace("kda_layer_norm_bwd_workspace_bytes", a)
-    workspace = _workspace(workspace, need, device)
-    a.workspace, a.workspace_bytes = (_ptr(workspace), need) if need else (None, 0)
+    _at(bias, "bias", (dim,), wd, device)
+    a = _lib.LayerNormBwdArgs(
+        ctypes.sizeof(_lib.LayerNormBwdArgs), x.data_ptr(), grad_y.data_ptr(), _at(weight, "weight", (dim,), wd, device),
+        _ptr(grad_residual), dx.data_ptr(), _ptr(got["dweight"]), _ptr(got["dbias"]), _step(x, "x", shape, dtype, device),
+        _step(grad_y, "grad_y", shape, gd, device), _step(grad_residual, "grad_residual", shape, rd, device),
+        _step(dx, "dx", shape, grad_dtype, device), x.numel() // dim if dim else 0, dim, eps, kind,
+        _kind(grad_y, "grad_y"), _kind(grad_residual, "grad_residual"), _kind(w, "weight"), grad_kind, None, 0,
+        _stream(device))
+    held = _give_workspace("kda_layer_norm_bwd_workspace_bytes", a, workspace, device)  # noqa: F841
     _call("kda_layer_norm_bwd", a, device)
     return got
