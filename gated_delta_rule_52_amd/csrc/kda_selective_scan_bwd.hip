@@ -231,6 +231,9 @@ __global__ void __launch_bounds__(256) scan_grad_kernel(ScanBwdLaunch P, BwdSpac
     static_assert(2 * kCkpt * NS % 256 == 0, "staging");
     __shared__ __attribute__((aligned(16))) float sBC[2][2][kCkpt][NS];
     __shared__ float sR[2][4][kCkpt][2 * NS];  // per wave: dB, dC of each token
+    // A block's decays wait in LDS, each lane's own, not in registers: with them there three waves fit a SIMD.
+    constexpr bool kStash = R <= 4;
+    __shared__ float4 sA[kStash ? kCkpt : 1][kStash ? 256 : 1];
     const int groups = (P.dim + 63) / 64;
     const int64_t slot = blockIdx.x / groups;
     const int group = static_cast<int>(blockIdx.x % groups);
@@ -346,7 +349,7 @@ __global__ void __launch_bounds__(256) scan_grad_kernel(ScanBwdLaunch P, BwdSpac
             }
             if (b > 0) fetch(b - 1);
             // forwards: decay a and carried state c = a h of every token of the block, and its output sum
-            float ha[kCkpt][R], hc[kCkpt][R], dA8[R], part[4];
+            float ha[kStash ? 1 : kCkpt][R], hc[kCkpt][R], dA8[R], part[4];
             auto ahead = [&](auto jc, auto ic) {
                 constexpr int j = decltype(jc)::value, i = decltype(ic)::value, t = 4 * j + i;
                 const float *bt = &sBC[buf][0][t][q * R], *ct = &sBC[buf][1][t][q * R];
@@ -356,10 +359,11 @@ __global__ void __launch_bounds__(256) scan_grad_kernel(ScanBwdLaunch P, BwdSpac
                 for (int r = 0; r < R; ++r) {
                     const float a = __builtin_amdgcn_exp2f(dl * A2[r]), c = a * h[r];
                     h[r] = fmaf(xl, bt[r], c);
-                    ha[t][r] = a;
+                    ha[kStash ? 0 : t][r] = a;
                     hc[t][r] = c;
                     if (GATED) acc = fmaf(ct[r], h[r], acc);
                 }
+                if constexpr (kStash) sA[t][threadIdx.x] = make_float4(ha[0][0], ha[0][1], ha[0][2], ha[0][3]);
                 part[i] = acc;
                 if (GATED && i == 3) yv[j] = transpose_sum(part, q);
             };
@@ -370,6 +374,8 @@ __global__ void __launch_bounds__(256) scan_grad_kernel(ScanBwdLaunch P, BwdSpac
                 const float *bt = &sBC[buf][0][t][q * R], *ct = &sBC[buf][1][t][q * R];
                 const float dl = lane_bcast<i>(de[j]), xl = lane_bcast<i>(xs[j]), g = lane_bcast<i>(gp[j]);
                 float dB[R], dC[R], pn = 0.f, sn = 0.f;
+                const float *a = kStash ? reinterpret_cast<const float *>(&sA[kStash ? t : 0][kStash ? threadIdx.x : 0])
+                                        : ha[kStash ? 0 : t];
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
                     const float gg = fmaf(ct[r], g, G[r]), c = hc[t][r], e = gg * c;
@@ -378,7 +384,7 @@ __global__ void __launch_bounds__(256) scan_grad_kernel(ScanBwdLaunch P, BwdSpac
                     pn = fmaf(gg, bt[r], pn);
                     sn = fmaf(e, A2[r], sn);
                     dA8[r] = fmaf(e, dl, dA8[r]);
-                    G[r] = ha[t][r] * gg;
+                    G[r] = a[r] * gg;
                 }
                 Pn[i] = pn;
                 Sn[i] = sn;
@@ -401,9 +407,13 @@ __global__ void __launch_bounds__(256) scan_grad_kernel(ScanBwdLaunch P, BwdSpac
 #pragma unroll
             for (int r = 0; r < R; ++r) dA8[r] = 0.f;
             ahead(KDA_I(0), KDA_I(0)); ahead(KDA_I(0), KDA_I(1)); ahead(KDA_I(0), KDA_I(2)); ahead(KDA_I(0), KDA_I(3));
+            // The second group where the tile reaches it.  The branch also ends the basic block, which keeps the
+            // scheduler from mixing the groups and paying in registers.
             if constexpr (J > 1) {
-                ahead(KDA_I(1), KDA_I(0)); ahead(KDA_I(1), KDA_I(1)); ahead(KDA_I(1), KDA_I(2)); ahead(KDA_I(1), KDA_I(3));
-                back(KDA_I(1), KDA_I(3)); back(KDA_I(1), KDA_I(2)); back(KDA_I(1), KDA_I(1)); back(KDA_I(1), KDA_I(0));
+                if (b * kCkpt + 4 < tl.len) {
+                    ahead(KDA_I(1), KDA_I(0)); ahead(KDA_I(1), KDA_I(1)); ahead(KDA_I(1), KDA_I(2)); ahead(KDA_I(1), KDA_I(3));
+                    back(KDA_I(1), KDA_I(3)); back(KDA_I(1), KDA_I(2)); back(KDA_I(1), KDA_I(1)); back(KDA_I(1), KDA_I(0));
+                }
             }
             back(KDA_I(0), KDA_I(3)); back(KDA_I(0), KDA_I(2)); back(KDA_I(0), KDA_I(1)); back(KDA_I(0), KDA_I(0));
 #undef KDA_I
