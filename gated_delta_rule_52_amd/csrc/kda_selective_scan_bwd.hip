@@ -490,7 +490,6 @@ BwdSpace space(float *ws, const SeqTiles &seq, int dim, int ds) {
 template <int R, bool InBf16, bool GATED>
 void launch_grad(const ScanBwdLaunch &P, const BwdSpace &w) {
     const int64_t slots = P.seq.slots();
-    if (slots == 0) return;
     const int groups = (P.dim + 63) / 64;
     const unsigned grid = static_cast<unsigned>(slots * groups);
     if (tiled(P.seq)) {
@@ -535,10 +534,12 @@ size_t scan_bwd_workspace_bytes(const SeqTiles &seq, int dim, int ds) { return s
 
 hipError_t launch_scan_bwd(const ScanBwdLaunch &P) {
     const BwdSpace w = space(P.ws, P.seq, P.dim, P.ds);
-    if (P.u.bf16) launch_any<true>(P, w);
-    else launch_any<false>(P, w);
+    if (P.seq.N > 0) {
+        if (P.u.bf16) launch_any<true>(P, w);
+        else launch_any<false>(P, w);
+    }
     const int64_t states = static_cast<int64_t>(P.dim) * P.ds;
-    launch_column_sum(w.par, states + 2 * P.dim, static_cast<int>(P.seq.slots()),
+    launch_column_sum(w.par, states + 2 * P.dim, P.seq.N > 0 ? static_cast<int>(P.seq.slots()) : 0,
                       {{P.dA, P.dD, P.ddt_bias}, {states, P.dim, P.dim}}, P.stream);
     return hipGetLastError();
 }

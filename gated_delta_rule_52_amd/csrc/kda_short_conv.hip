@@ -490,7 +490,7 @@ hipError_t launch_conv_bwd(const ConvBwdLaunch &P) {
     const int64_t ld = static_cast<int64_t>(P.width + 1) * P.dim;
     launch_column_sum(P.ws, ld, static_cast<int>(cut.parts), {{P.dw, P.db, nullptr}, {static_cast<int64_t>(P.width) * P.dim, P.dim, 0}},
                       P.stream);
-    if (P.dh0) {
+    if (P.dh0 && P.N > 0) {
         if (P.x.bf16) launch_state_grad<true>(P);
         else launch_state_grad<false>(P);
     }

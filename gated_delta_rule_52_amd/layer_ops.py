@@ -69,16 +69,16 @@ def _step(t, name, shape, dtype, device) -> int:
     strides = t.stride()
     if width != 1 and strides[-1] != 1:
         raise ValueError(f"{name} must be dense along its last dimension")
-    step, span = 0, 1  # of the innermost leading dimension with more than one entry, and the rows inside
+    step, span = None, 1  # of the innermost leading dimension with more than one entry, and the rows inside
     for size, stride in zip(reversed(shape[:-1]), reversed(strides[:-1])):
         if size == 1:
             continue
-        if step == 0:
+        if step is None:
             step = stride
         elif stride != span * step:
             raise ValueError(f"the rows of {name} must be equally spaced")
         span *= size
-    return step if span > 1 else width
+    return width if step is None else step
 
 
 def _at(t, name, shape, dtype, device):

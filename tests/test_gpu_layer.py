@@ -167,8 +167,11 @@ def test_scan_step(kda, N, dim, ds, dtype, gate):
     one = {k: None if v is None else v[:, None] for k, v in s.items()}
     y1, final = kda.selective_scan_fwd(one["u"], one["dt"], p["A"], one["B"], one["C"], p["D"], one["z"], p["dt_bias"],
                                        initial_state=dev(x["h0"]), dt_softplus=True, out_dtype=torch.float32)
+    y2, none = kda.selective_scan_fwd(one["u"], one["dt"], p["A"], one["B"], one["C"], p["D"], one["z"], p["dt_bias"],
+                                      initial_state=dev(x["h0"]), dt_softplus=True, out_dtype=torch.float32,
+                                      output_final_state=False)
     torch.cuda.synchronize()
-    assert torch.equal(y, y1[:, 0]) and torch.equal(state, final)
+    assert torch.equal(y, y1[:, 0]) and torch.equal(state, final) and torch.equal(y2, y1) and none is None
     want, size = ref.scan_forward(x, offsets), ref.scan_forward(x, offsets, absolute=True)
     n = ref.scan_roundings(x, offsets)
     ref.check("y", host(y), want["y"], size["y"], n)
@@ -404,6 +407,9 @@ NORM = [  # rows, dim, x, residual or None, weights or None, output
     (3, 1024, "fp32", None, "bf16", "fp32"), (6, 2048, "bf16", "fp32", "fp32", "bf16"), (3, 2049, "fp32", None, "fp32", "fp32"),
     (4, 4096, "bf16", "fp32", "fp32", "bf16"), (3, 5001, "fp32", "fp32", "fp32", "fp32"), (2, 8192, "bf16", None, "fp32", "fp32"),
     (3, 8193, "fp32", None, "fp32", "fp32"), (2, 16384, "bf16", "bf16", "bf16", "bf16"), (2500, 64, "bf16", None, "fp32", "fp32"),
+    # several rounds of rows for every workgroup, the last one partly filled
+    (40011, 24, "fp32", None, "fp32", "fp32"), (5003, 600, "bf16", "fp32", "fp32", "bf16"), (777, 5000, "bf16", None, "fp32", "fp32"),
+    (600, 9000, "fp32", None, "fp32", "fp32"),
 ]
 # roundings behind a sum over a row: a lane's 64 at most, the lanes' 6 steps and the waves' 16, and a dozen around them
 ROW = 100
@@ -457,6 +463,12 @@ def test_norm_of_heads_and_far_means(kda):
     far = rounded(1000 + r.normal(size=(6, 777)), "fp32")
     y = kda.layer_norm_fwd(dev(far))
     ref.check("far", host(y), ref.norm_forward(far, None, None, 1e-5)[0], ref.norm_scales(far, None, None, None, 1e-5)["y"], ROW)
+    far = rounded(1000 + r.normal(size=(6, 5001)), "fp32")  # a row over several waves
+    y = kda.layer_norm_fwd(dev(far))
+    ref.check("far, wide", host(y), ref.norm_forward(far, None, None, 1e-5)[0], ref.norm_scales(far, None, None, None, 1e-5)["y"], ROW)
+    far[:, 0] = 1e4  # one element far from its wave's others
+    y = kda.layer_norm_fwd(dev(far))
+    ref.check("outlier", host(y), ref.norm_forward(far, None, None, 1e-5)[0], ref.norm_scales(far, None, None, None, 1e-5)["y"], ROW)
     flat = np.full((3, 64), 7.0)
     assert bool((kda.layer_norm_fwd(dev(flat)) == 0).all())
     # the residual in place
@@ -489,8 +501,22 @@ def test_no_rows(kda):
     assert kda.layer_norm_fwd(e(0, 8), w).shape == (0, 8)
     g = kda.layer_norm_bwd(e(0, 8), e(0, 8), w, w)
     assert not g["dweight"].any() and not g["dbias"].any()
-    none = kda.selective_scan_bwd(e(0, 4, 6), e(0, 4, 6), A, e(0, 4, 16), e(0, 4, 16), e(0, 4, 6))
-    assert not none["dA"].any()
+    # no sequences: a batch of none, and packed rows that belong to no sequence (a single offset)
+    one = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for lead, c in (((0, 4), None), ((1, 5), one)):
+        y = torch.full((*lead, 6), 5.0, device="cuda")
+        args = e(*lead, 6), e(*lead, 6), A, e(*lead, 16), e(*lead, 16)
+        _, final = kda.selective_scan_fwd(*args, cu_seqlens=c, y=y)
+        assert final.shape == (0, 6, 16) and bool((y == 5).all())
+        out = {k: torch.full((*lead, 16 if k in ("dB", "dC") else 6), 5.0, device="cuda") for k in ("du", "ddt", "dB", "dC")}
+        none = kda.selective_scan_bwd(*args, y, cu_seqlens=c, out=out)
+        assert not none["dA"].any() and all(bool((v == 5).all()) for v in out.values())
+        x = e(*lead, 8)
+        y = torch.full((*lead, 8), 5.0, device="cuda")
+        kda.short_conv_fwd(x, torch.ones(8, 4, device="cuda"), cu_seqlens=c, y=y)
+        dx = torch.full((*lead, 8), 5.0, device="cuda")
+        none = kda.short_conv_bwd(x, torch.ones(8, 4, device="cuda"), x, cu_seqlens=c, out=dict(dx=dx))
+        assert not none["dweight"].any() and bool((y == 5).all()) and bool((dx == 5).all())
 
 
 def test_refusals(kda):
@@ -510,6 +536,8 @@ def test_refusals(kda):
            lambda: kda.short_conv_fwd(x, A, cu_seqlens=torch.zeros(3, dtype=torch.int64, device="cuda")),
            lambda: kda.layer_norm_fwd(x, A[:, 0].bfloat16(), A[:, 0].contiguous()),
            lambda: kda.layer_norm_fwd(x, eps=1e-5, residual=x[:1]),
+           # rows that repeat inside a batch whose sequences do not: no spacing fits, and none may be made up
+           lambda: kda.short_conv_fwd(x[:, :1].expand(2, 8, 16), A),
            lambda: kda.layer_norm_bwd(x, x, grad_dtype=torch.float16)]
     for i, f in enumerate(bad):
         with pytest.raises(ValueError):
@@ -520,9 +548,113 @@ def test_refusals(kda):
               lambda: kda.short_conv_fwd(x, torch.zeros(16, 5, device="cuda")),
               lambda: kda.short_conv_fwd(x[:1].expand(1, 8, 16), A, y=x[:1]),
               lambda: kda.short_conv_fwd(x[:, :1].expand(2, 8, 16)[:1], A),
+              lambda: kda.layer_norm_fwd(x[0, 0].expand(4, 16)),
               lambda: kda.layer_norm_fwd(torch.zeros(1, 16385, device="cuda"))):
         with pytest.raises(kda.KdaError):
             f()
+
+
+def test_rows_past_32_bits(kda):
+    """Rows whose offsets pass 2^32 elements, as slices of a very wide buffer: the same bits as a dense copy."""
+    import torch
+    rows, wide, dim, ds = 1100, 4_000_003, 24, 16
+    r = np.random.default_rng(12)
+    x = scan_inputs(13, [0, rows], rows, dim, ds, "bf16")
+    dense = scan_device(x, 1, rows, "bf16")
+    buffer = torch.empty(rows, wide, dtype=torch.bfloat16, device="cuda")
+    far, at = {}, 5
+    for k in ("u", "dt", "B", "C", "z"):
+        n = dense[k].shape[-1]
+        buffer[:, at:at + n] = dense[k][0]
+        far[k] = buffer[:, at:at + n][None]
+        at += n
+    p = {k: dense[k] for k in ("A", "D", "dt_bias")}
+    h0 = dev(x["h0"])
+    y, final = kda.selective_scan_fwd(**dense, initial_state=h0, dt_softplus=True)
+    y1, final1 = kda.selective_scan_fwd(**far, **p, initial_state=h0, dt_softplus=True, y=buffer[:, at:at + dim][None])
+    assert torch.equal(y, y1) and torch.equal(final, final1)
+    call = lambda s, out: kda.selective_scan_bwd(s["u"], s["dt"], p["A"], s["B"], s["C"], s["z"], p["D"], s["z"],  # noqa: E731
+                                                 p["dt_bias"], dt_softplus=True, grad_dtype=torch.bfloat16, out=out)
+    out = {k: buffer[:, at + i * 32:at + i * 32 + (ds if k in ("dB", "dC") else dim)][None]
+           for i, k in enumerate(("du", "ddt", "dB", "dC", "dz"))}
+    want, got = call(dense, None), call(far, out)
+    assert all(torch.equal(want[k], got[k]) for k in want if want[k] is not None)
+    w = dev(r.normal(size=(dim, 4)))
+    y, s = kda.short_conv_fwd(dense["u"], w, silu=True)
+    y1, s1 = kda.short_conv_fwd(far["u"], w, silu=True, y=buffer[:, at:at + dim][None])
+    assert torch.equal(y, y1) and torch.equal(s, s1)
+    want = kda.short_conv_bwd(dense["u"], w, dense["z"], silu=True, grad_dtype=torch.bfloat16)
+    got = kda.short_conv_bwd(far["u"], w, far["z"], silu=True, grad_dtype=torch.bfloat16, out=dict(dx=buffer[:, at:at + dim][None]))
+    assert all(torch.equal(want[k], got[k]) for k in want if want[k] is not None)
+    wt = w[:, 0].contiguous()
+    assert torch.equal(kda.layer_norm_fwd(dense["u"], wt), kda.layer_norm_fwd(far["u"], wt, y=buffer[:, at:at + dim][None]))
+    want = kda.layer_norm_bwd(dense["u"], dense["z"], wt, wt)
+    got = kda.layer_norm_bwd(far["u"], far["z"], wt, wt)
+    assert all(torch.equal(want[k], got[k]) for k in want)
+
+
+@pytest.mark.parametrize("B,T,dim,W,dtype", [(4, 4096, 4096, 4, "bf16"), (3, 5000, 2051, 3, "fp32")])
+def test_conv_full_size(kda, B, T, dim, W, dtype):
+    """Sizes at which each thread walks its longest tile, against the definition in 64 bits on the GPU."""
+    import torch
+    g = torch.Generator("cuda").manual_seed(3)
+    n = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    x, gy, w, b = n(B, T, dim).to(tdtype(dtype)), n(B, T, dim).to(tdtype(dtype)), n(dim, W) / W ** .5, .1 * n(dim)
+    y, _ = kda.short_conv_fwd(x, w, b, silu=True, out_dtype=torch.float32)
+    got = kda.short_conv_bwd(x, w, gy, b, silu=True)
+    worst = 0.0
+    for c in range(0, dim, 512):
+        xs = torch.nn.functional.pad(x[:, :, c:c + 512].double(), (0, 0, W - 1, 0))
+        ws, gs = w[c:c + 512].double(), gy[:, :, c:c + 512].double()
+        p = sum(xs[:, j:j + T] * ws[:, j] for j in range(W)) + b[c:c + 512].double()
+        size = sum((xs[:, j:j + T] * ws[:, j]).abs() for j in range(W)) + b[c:c + 512].double().abs()
+        sg = torch.sigmoid(p)
+        # 16 roundings of the absolute sum, as in the small cases
+        worst = max(worst, float(((y[:, :, c:c + 512].double() - p * sg).abs() / (16 * 2 ** -24 * size)).max()))
+        gp = gs * sg * (1 + p * (1 - sg))
+        pad = torch.nn.functional.pad(gp, (0, 0, 0, W - 1))
+        dx = sum(pad[:, W - 1 - j:W - 1 - j + T] * ws[:, j] for j in range(W))
+        dw = torch.stack([(gp * xs[:, j:j + T]).sum((0, 1)) for j in range(W)], 1)
+        near = lambda a, v: float((a.double() - v).norm() / v.norm())  # noqa: E731
+        # norms: some 40 independent roundings of terms that a sum of W (dx) or of B T (dweight) keeps up with
+        assert near(got["dx"][:, :, c:c + 512], dx) < 40 * 2 ** -24
+        assert near(got["dweight"][c:c + 512], dw) < 200 * 2 ** -24 and near(got["dbias"][c:c + 512], gp.sum((0, 1))) < 200 * 2 ** -24
+    assert worst <= 1, worst
+
+
+@pytest.mark.parametrize("B,T,dim,ds", [(16, 300, 2048, 16), (2, 2000, 1024, 16), (12, 130, 2900, 20)])
+def test_scan_full_size(kda, B, T, dim, ds):
+    """Sizes that take whole sequences and long tiles, against a walk over the tokens in 64 bits on the GPU; the
+    gradients against autograd through that walk, on a part of the channels."""
+    import torch
+    g = torch.Generator("cuda").manual_seed(4)
+    n = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    u, dt, z, gy = (n(B, T, dim).bfloat16() for _ in range(4))
+    Bm, Cm, A, D = n(B, T, ds).bfloat16(), n(B, T, ds).bfloat16(), -torch.exp(n(dim, ds)), n(dim)
+    bias, h0, gf = -3 + n(dim), n(B, dim, ds), n(B, dim, ds)
+    y, final = kda.selective_scan_fwd(u, dt, A, Bm, Cm, D, z, bias, initial_state=h0, dt_softplus=True, out_dtype=torch.float32)
+    got = kda.selective_scan_bwd(u, dt, A, Bm, Cm, gy, D, z, bias, initial_state=h0, grad_final_state=gf, dt_softplus=True)
+    some = torch.cat([torch.arange(40), torch.arange(dim - 40, dim)]).cuda()
+    leaf = lambda t: t.double().requires_grad_()  # noqa: E731
+    L = dict(u=leaf(u[..., some]), dt=leaf(dt[..., some]), z=leaf(z[..., some]), A=leaf(A[some]), D=leaf(D[some]),
+             b=leaf(bias[some]), h0=leaf(h0[:, some]))
+    Bd, Cd = Bm.double(), Cm.double()
+    delta = torch.logaddexp(L["dt"] + L["b"], torch.zeros((), dtype=torch.float64, device="cuda"))
+    h, ys = L["h0"], []
+    for t in range(T):
+        h = torch.exp(delta[:, t, :, None] * L["A"]) * h + (delta[:, t] * L["u"][:, t])[..., None] * Bd[:, t, None]
+        ys.append((h * Cd[:, t, None]).sum(-1))
+    want = (torch.stack(ys, 1) + L["D"] * L["u"]) * L["z"] * torch.sigmoid(L["z"])
+    ((want * gy[..., some].double()).sum() + (h * gf[:, some].double()).sum()).backward()
+    near = lambda a, v: float((a.double() - v).norm() / v.norm())  # noqa: E731
+    # roundings add up independently over a state's memory of at most T tokens: some sqrt(20 T) of them
+    bound = 2 * (20 * T) ** .5 * 2 ** -24
+    assert near(y[..., some], want.detach()) < bound and near(final[:, some], h.detach()) < bound
+    for k, v in (("du", "u"), ("ddt", "dt"), ("dz", "z"), ("dh0", "h0")):
+        a = got[k][..., some] if k != "dh0" else got[k][:, some]
+        assert near(a, L[v].grad) < 2 * bound, (k, near(a, L[v].grad), bound)
+    for k, v in (("dA", "A"), ("dD", "D"), ("ddt_bias", "b")):
+        assert near(got[k][some], L[v].grad) < 8 * bound, (k, near(got[k][some], L[v].grad), bound)
 
 
 def test_streams_graphs_and_repeats(kda):
