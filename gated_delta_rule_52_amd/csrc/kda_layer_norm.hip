@@ -14,24 +14,40 @@ namespace kda {
 
 namespace {
 
-// 8 elements of a row from `col` on, 16 bytes at a time wherever the row starts (the hardware takes these accesses
-// at any element's alignment); the row's last elements singly.
+// A tensor's rows as a workgroup walks them: the address of its first row, which is uniform and moves, and the
+// lane's byte offset from there (its row among the workgroup's and its column), which stays.
+struct Walk {
+    char *at;
+    int64_t step;   // bytes per row
+    uint32_t off;
+    int bf16;
+    __device__ __forceinline__ Walk(const Rows &r, int64_t row, int sub, int lane) {
+        const int e = r.bf16 ? 2 : 4;
+        at = static_cast<char *>(r.p) + row * r.stride * e;
+        step = r.stride * e;
+        off = static_cast<uint32_t>(sub) * static_cast<uint32_t>(step) + static_cast<uint32_t>(lane * 8 * e);
+        bf16 = r.bf16;
+    }
+    __device__ __forceinline__ char *unit(int more) const { return at + (off + static_cast<uint32_t>(more) * (bf16 ? 2 : 4)); }
+};
+// 8 elements, `more` elements behind the lane's first, 16 bytes at a time wherever the row starts (the hardware
+// takes these accesses at any element's alignment); of a row's last unit the `left` elements that it has, singly,
+// and zeros.
 typedef uint32_t any4 __attribute__((ext_vector_type(4), aligned(2)));
-__device__ __forceinline__ void load8(const Rows &r, int64_t row, int col, int dim, float (&x)[8]) {
-    const int64_t at = row * r.stride + col;
-    if (col + 8 > dim) {
+__device__ __forceinline__ void load8(const char *p, int bf16, int left, float (&x)[8]) {
+    if (left < 8) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = col + i < dim ? r.get(row, col + i) : 0.f;
-    } else if (r.bf16) {
-        const any4 v = *reinterpret_cast<const any4 *>(static_cast<const uint16_t *>(r.p) + at);
+        for (int i = 0; i < 8; ++i)
+            x[i] = i >= left ? 0.f : bf16 ? bf16_to_f32(reinterpret_cast<const uint16_t *>(p)[i]) : reinterpret_cast<const float *>(p)[i];
+    } else if (bf16) {
+        const any4 v = *reinterpret_cast<const any4 *>(p);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             x[2 * i] = __uint_as_float(v[i] << 16);
             x[2 * i + 1] = __uint_as_float(v[i] & 0xffff0000u);
         }
     } else {
-        const any4 *p = reinterpret_cast<const any4 *>(static_cast<const float *>(r.p) + at);
-        const any4 a = p[0], b = p[1];
+        const any4 a = reinterpret_cast<const any4 *>(p)[0], b = reinterpret_cast<const any4 *>(p)[1];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             x[i] = __uint_as_float(a[i]);
@@ -39,28 +55,32 @@ __device__ __forceinline__ void load8(const Rows &r, int64_t row, int col, int d
         }
     }
 }
-__device__ __forceinline__ void store8(const Rows &r, int64_t row, int col, int dim, const float (&x)[8]) {
-    const int64_t at = row * r.stride + col;
-    if (col + 8 > dim) {
+__device__ __forceinline__ void store8(char *p, int bf16, int left, const float (&x)[8]) {
+    if (left < 8) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (col + i < dim) r.put(row, col + i, x[i]);
-    } else if (r.bf16) {
+        for (int i = 0; i < 8; ++i) {
+            if (i >= left) break;
+            if (bf16) reinterpret_cast<uint16_t *>(p)[i] = to_bf16(x[i]);
+            else reinterpret_cast<float *>(p)[i] = x[i];
+        }
+    } else if (bf16) {
         any4 v;
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] = to_bf16(x[2 * i]) | static_cast<uint32_t>(to_bf16(x[2 * i + 1])) << 16;
-        *reinterpret_cast<any4 *>(static_cast<uint16_t *>(r.p) + at) = v;
+        *reinterpret_cast<any4 *>(p) = v;
     } else {
-        any4 *p = reinterpret_cast<any4 *>(static_cast<float *>(r.p) + at);
         any4 a, b;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             a[i] = __float_as_uint(x[i]);
             b[i] = __float_as_uint(x[4 + i]);
         }
-        p[0] = a;
-        p[1] = b;
+        reinterpret_cast<any4 *>(p)[0] = a;
+        reinterpret_cast<any4 *>(p)[1] = b;
     }
+}
+__device__ __forceinline__ void load_param(const void *p, int bf16, int col, int left, float (&x)[8]) {
+    load8(static_cast<const char *>(p) + static_cast<int64_t>(col) * (bf16 ? 2 : 4), bf16, left, x);
 }
 
 // First column of unit u of a lane among the SPAN that share a row.
@@ -89,33 +109,39 @@ struct RowSums {
     float mean, rstd, g, gx;  // g: sum of g, gx: sum of g times the normalised x (0 without g)
 };
 template <int LANES, int WAVES, int U, bool GRAD>
-__device__ __forceinline__ RowSums row_sums(const float (&x)[U][8], const float (&g)[U][8], int lane, int dim, float eps,
-                                            float (*shared)[4]) {
+__device__ __forceinline__ RowSums row_sums(const float (&x)[U][8], const float (&g)[U][8], const float (&w)[U][8], int lane,
+                                            int dim, float inv_n, float n, float inv_dim, float eps, float (*shared)[4]) {
     constexpr int SPAN = LANES * WAVES;
-    float s = 0.f, n = 0.f;
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const int in = dim - first_col<SPAN>(lane, u);  // elements of the unit that the row has
-        n += static_cast<float>(in < 0 ? 0 : in > 8 ? 8 : in);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) s += x[u][i];  // zeros past the row
-    }
-    s = lanes_sum<LANES>(s);
-    if constexpr (WAVES > 1) n = lanes_sum<LANES>(n);
-    else n = static_cast<float>(dim);
-    const float p = n > 0.f ? s / n : 0.f;
-    float m2 = 0.f, sg = 0.f, sx = 0.f;
+    float s = 0.f;
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float d = first_col<SPAN>(lane, u) + i < dim ? x[u][i] - p : 0.f;
-            m2 = fmaf(d, d, m2);
-            if (GRAD) {
-                sg += g[u][i];
-                sx = fmaf(g[u][i], d, sx);
+        for (int i = 0; i < 8; ++i) s += x[u][i];  // zeros past the row
+    const float p = lanes_sum<LANES>(s) * inv_n;
+    float m2 = 0.f, sg = 0.f, sx = 0.f;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int left = dim - first_col<SPAN>(lane, u);
+        if (left >= 8) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float d = x[u][i] - p;
+                m2 = fmaf(d, d, m2);
+                if (GRAD) sx = fmaf(g[u][i] * w[u][i], d, sx);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float d = i < left ? x[u][i] - p : 0.f;
+                m2 = fmaf(d, d, m2);
+                if (GRAD) sx = fmaf(g[u][i] * w[u][i], d, sx);
             }
         }
+        if (GRAD) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sg = fmaf(g[u][i], w[u][i], sg);
+        }
+    }
     m2 = lanes_sum<LANES>(m2);
     if (GRAD) {
         sg = lanes_sum<LANES>(sg);
@@ -135,7 +161,7 @@ __device__ __forceinline__ RowSums row_sums(const float (&x)[U][8], const float 
         float total = 0.f;
 #pragma unroll 4
         for (int w = 0; w < WAVES; ++w) total = fmaf(shared[2 * w][0], shared[2 * w][1], total);
-        r.mean = total / static_cast<float>(dim);
+        r.mean = total * inv_dim;
         m2 = sg = sx = 0.f;
 #pragma unroll 4
         for (int w = 0; w < WAVES; ++w) {
@@ -149,9 +175,22 @@ __device__ __forceinline__ RowSums row_sums(const float (&x)[U][8], const float 
         r.g = sg;
         r.gx = sx;
     }
-    r.rstd = 1.f / sqrtf(m2 / static_cast<float>(dim) + eps);
+    r.rstd = __builtin_amdgcn_rsqf(fmaf(m2, inv_dim, eps));
     r.gx *= r.rstd;
     return r;
+}
+
+// Elements of a row that a wave holds (all of them where a row is one wave's), and its inverse.
+template <int LANES, int WAVES, int U>
+__device__ __forceinline__ float wave_count(int lane, int dim) {
+    if constexpr (WAVES == 1) return static_cast<float>(dim);
+    float n = 0.f;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int left = dim - first_col<LANES * WAVES>(lane, u);
+        n += static_cast<float>(left < 0 ? 0 : left > 8 ? 8 : left);
+    }
+    return lanes_sum<LANES>(n);
 }
 
 template <int LANES, int WAVES>
@@ -161,45 +200,46 @@ constexpr int rows_per_group() { return WAVES == 1 ? 256 / LANES : 1; }
 
 template <int LANES, int WAVES, int U>
 __global__ void __launch_bounds__((norm_threads<LANES, WAVES>())) norm_fwd_kernel(NormFwdLaunch P) {
-    constexpr int SPAN = LANES * WAVES;
+    constexpr int SPAN = LANES * WAVES, ROWS = rows_per_group<LANES, WAVES>();
     __shared__ float shared[2 * WAVES][4];
     const int lane = threadIdx.x % SPAN;
-    int64_t row = static_cast<int64_t>(blockIdx.x) * rows_per_group<LANES, WAVES>() + threadIdx.x / SPAN;
-    const bool live = row < P.rows;
-    if (WAVES == 1 && !live) row = P.rows - 1;  // keeps the wave whole for the sums; stores nothing
+    int sub = threadIdx.x / SPAN;
+    const int64_t base = static_cast<int64_t>(blockIdx.x) * ROWS;
+    const bool live = base + sub < P.rows;
+    if (!live) sub = static_cast<int>(P.rows - 1 - base);  // keeps the wave whole for the sums; stores nothing
+    const Walk wx(P.x, base, sub, lane), wr(P.res, base, sub, lane), wo(P.res_out, base, sub, lane), wy(P.y, base, sub, lane);
+    const float n = wave_count<LANES, WAVES, U>(lane, P.dim), inv_dim = 1.f / static_cast<float>(P.dim);
     float x[U][8];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        const int col = first_col<SPAN>(lane, u);
-        if (col < P.dim) {
-            load8(P.x, row, col, P.dim, x[u]);
+        const int left = P.dim - first_col<SPAN>(lane, u), more = u * SPAN * 8;
+        if (left > 0) {
+            load8(wx.unit(more), P.x.bf16, left, x[u]);
             if (P.res.p) {
                 float r[8];
-                load8(P.res, row, col, P.dim, r);
+                load8(wr.unit(more), P.res.bf16, left, r);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) x[u][i] += r[i];
-                if (live) store8(P.res_out, row, col, P.dim, x[u]);
+                if (live) store8(wo.unit(more), P.res_out.bf16, left, x[u]);
             }
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i) x[u][i] = 0.f;
         }
     }
-    const RowSums s = row_sums<LANES, WAVES, U, false>(x, x, lane, P.dim, P.eps, shared);
+    const RowSums s = row_sums<LANES, WAVES, U, false>(x, x, x, lane, P.dim, n > 0.f ? 1.f / n : 0.f, n, inv_dim, P.eps, shared);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        const int col = first_col<SPAN>(lane, u);
-        if (col >= P.dim || !live) continue;
-        float w[8], b[8];
-        const Rows wr{const_cast<void *>(P.w), 0, P.w_bf16}, br{const_cast<void *>(P.b), 0, P.w_bf16};
-        if (P.w) load8(wr, 0, col, P.dim, w);
-        if (P.b) load8(br, 0, col, P.dim, b);
+        const int col = first_col<SPAN>(lane, u), left = P.dim - col;
+        if (left <= 0 || !live) continue;
+        float w[8], b[8] = {};
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float n = (x[u][i] - s.mean) * s.rstd;
-            x[u][i] = fmaf(n, P.w ? w[i] : 1.f, P.b ? b[i] : 0.f);
-        }
-        store8(P.y, row, col, P.dim, x[u]);
+        for (int i = 0; i < 8; ++i) w[i] = 1.f;
+        if (P.w) load_param(P.w, P.w_bf16, col, left, w);
+        if (P.b) load_param(P.b, P.w_bf16, col, left, b);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[u][i] = fmaf((x[u][i] - s.mean) * s.rstd, w[i], b[i]);
+        store8(wy.unit(u * SPAN * 8), P.y.bf16, left, x[u]);
     }
 }
 
@@ -213,52 +253,54 @@ __global__ void __launch_bounds__((norm_threads<LANES, WAVES>())) norm_bwd_kerne
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const int col = first_col<SPAN>(lane, u);
-        const Rows wr{const_cast<void *>(P.w), 0, P.w_bf16};
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             w[u][i] = 1.f;
             x[u][i] = g[u][i] = dw[u][i] = db[u][i] = 0.f;
         }
-        if (P.w && col < P.dim) load8(wr, 0, col, P.dim, w[u]);
+        if (P.w && col < P.dim) load_param(P.w, P.w_bf16, col, P.dim - col, w[u]);
     }
+    const float n = wave_count<LANES, WAVES, U>(lane, P.dim), inv_n = n > 0.f ? 1.f / n : 0.f;
+    const float inv_dim = 1.f / static_cast<float>(P.dim);
     const int64_t stride = static_cast<int64_t>(gridDim.x) * ROWS;
     int64_t base = static_cast<int64_t>(blockIdx.x) * ROWS;
-    // whole rounds for every lane of the workgroup: rows past the end are computed from the last and dropped
+    Walk wx(P.x, base, sub, lane), wg(P.gy, base, sub, lane), wr(P.gres, base, sub, lane), wd(P.dx, base, sub, lane);
+    // whole rounds for every lane of the workgroup: lanes past the last row hold what they had and are not counted
     for (int round = 0; base < P.rows; base += stride, round ^= 1) {
         const bool live = base + sub < P.rows;
-        const int64_t row = live ? base + sub : P.rows - 1;
-        float gy[U][8];
+        if (live) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int col = first_col<SPAN>(lane, u);
-            if (col < P.dim) {
-                load8(P.x, row, col, P.dim, x[u]);
-                load8(P.gy, row, col, P.dim, gy[u]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) gy[u][i] = 0.f;
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) g[u][i] = gy[u][i] * w[u][i];
-        }
-        const RowSums s = row_sums<LANES, WAVES, U, true>(x, g, lane, P.dim, P.eps, shared[round]);
-        const float m1 = s.g / static_cast<float>(P.dim), m2 = s.gx / static_cast<float>(P.dim);
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int col = first_col<SPAN>(lane, u);
-            float r[8] = {}, xh[8];
-            if (P.gres.p && live && col < P.dim) load8(P.gres, row, col, P.dim, r);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                xh[i] = (x[u][i] - s.mean) * s.rstd;  // past the row gy is 0
-                if (live) {
-                    dw[u][i] = fmaf(gy[u][i], xh[i], dw[u][i]);
-                    db[u][i] += gy[u][i];
+            for (int u = 0; u < U; ++u) {
+                const int left = P.dim - first_col<SPAN>(lane, u), more = u * SPAN * 8;
+                if (left > 0) {
+                    load8(wx.unit(more), P.x.bf16, left, x[u]);
+                    load8(wg.unit(more), P.gy.bf16, left, g[u]);
                 }
-                r[i] = fmaf(s.rstd, g[u][i] - fmaf(xh[i], m2, m1), r[i]);
             }
-            if (live && col < P.dim) store8(P.dx, row, col, P.dim, r);
         }
+        const RowSums s = row_sums<LANES, WAVES, U, true>(x, g, w, lane, P.dim, inv_n, n, inv_dim, P.eps, shared[round]);
+        const float m1 = s.g * inv_dim, m2 = s.gx * inv_dim;
+        if (live) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int left = P.dim - first_col<SPAN>(lane, u), more = u * SPAN * 8;
+                if (left <= 0) continue;
+                float r[8] = {};
+                if (P.gres.p) load8(wr.unit(more), P.gres.bf16, left, r);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float xh = (x[u][i] - s.mean) * s.rstd;  // past the row g is 0
+                    dw[u][i] = fmaf(g[u][i], xh, dw[u][i]);
+                    db[u][i] += g[u][i];
+                    r[i] = fmaf(s.rstd, fmaf(g[u][i], w[u][i], -fmaf(xh, m2, m1)), r[i]);
+                }
+                store8(wd.unit(more), P.dx.bf16, left, r);
+            }
+        }
+        wx.at += stride * wx.step;
+        wg.at += stride * wg.step;
+        wr.at += stride * wr.step;
+        wd.at += stride * wd.step;
     }
     if (!P.ws) return;
     // one partial row of dw and of db per workgroup
@@ -316,25 +358,25 @@ __global__ void __launch_bounds__(1024) column_sum_kernel(const float *in, int64
     }
 }
 
-// The smallest arrangement that holds a row with at most two units per lane, which is what leaves the backward
-// pass three waves per SIMD: 16 lanes (to 128 elements), 32, a wave (to 1,024), four, eight and sixteen waves.
-#define KDA_NORM_PICK(CALL)                        \
-    do {                                           \
-        if (P.dim <= 128) CALL(16, 1, 1);          \
-        else if (P.dim <= 256) CALL(32, 1, 1);     \
-        else if (P.dim <= 512) CALL(64, 1, 1);     \
-        else if (P.dim <= 1024) CALL(64, 1, 2);    \
-        else if (P.dim <= 2048) CALL(64, 4, 1);    \
-        else if (P.dim <= 4096) CALL(64, 4, 2);    \
-        else if (P.dim <= 8192) CALL(64, 8, 2);    \
-        else CALL(64, 16, 2);                      \
-    } while (0)
+// The smallest arrangement that holds a row: 16 lanes (to 128 elements), 32, a wave (to 1,024), then several.  The
+// backward pass, which keeps five values per element, spreads wide rows further, over 16-wave workgroups of one unit
+// per lane (8,192 x 4,096 bf16: 71 us with 8 waves, 84 with 4).
+#define KDA_NORM_NARROW(CALL)                      \
+    if (P.dim <= 128) CALL(16, 1, 1);              \
+    else if (P.dim <= 256) CALL(32, 1, 1);         \
+    else if (P.dim <= 512) CALL(64, 1, 1);         \
+    else if (P.dim <= 1024) CALL(64, 1, 2);        \
+    else if (P.dim <= 2048) CALL(64, 4, 1)
 
 int rows_of(int dim) {
     return dim <= 128 ? 16 : dim <= 256 ? 8 : dim <= 1024 ? 4 : 1;
 }
+// The backward pass's workgroups: as many as are resident at once, by its registers.  More leave a second, short
+// round and more partial rows to sum; fewer leave the chip (32,768 x 1,024 bf16: 56 us with 768, 74 with 1,024;
+// 16,384 x 2,048: 58 with 1,280, 77 with 512; 262,144 x 128: 47 with 1,024, 60 with 512).
 int64_t bwd_groups(int64_t rows, int dim) {
-    const int64_t whole = (rows + rows_of(dim) - 1) / rows_of(dim), most = dim <= 1024 ? 1024 : dim <= 4096 ? 512 : 256;
+    const int64_t whole = (rows + rows_of(dim) - 1) / rows_of(dim);
+    const int64_t most = dim <= 128 ? 1024 : dim <= 512 ? 1280 : dim <= 1024 ? 768 : dim <= 2048 ? 1280 : dim <= 4096 ? 512 : 256;
     return whole < most ? whole : most;
 }
 
@@ -349,7 +391,10 @@ hipError_t launch_norm_fwd(const NormFwdLaunch &P) {
 #define KDA_NORM_FWD(L, W, U)                                                                                    \
     norm_fwd_kernel<L, W, U><<<static_cast<unsigned>((P.rows + rows_per_group<L, W>() - 1) / rows_per_group<L, W>()), \
                                norm_threads<L, W>(), 0, P.stream>>>(P)
-    KDA_NORM_PICK(KDA_NORM_FWD);
+    KDA_NORM_NARROW(KDA_NORM_FWD);
+    else if (P.dim <= 4096) KDA_NORM_FWD(64, 4, 2);
+    else if (P.dim <= 8192) KDA_NORM_FWD(64, 8, 2);
+    else KDA_NORM_FWD(64, 16, 2);
 #undef KDA_NORM_FWD
     return hipGetLastError();
 }
@@ -362,7 +407,12 @@ hipError_t launch_norm_bwd(const NormBwdLaunch &P) {
     const int64_t groups = bwd_groups(P.rows, P.dim);
 #define KDA_NORM_BWD(L, W, U) \
     norm_bwd_kernel<L, W, U><<<static_cast<unsigned>(groups), norm_threads<L, W>(), 0, P.stream>>>(P)
-    if (groups > 0) KDA_NORM_PICK(KDA_NORM_BWD);
+    if (groups > 0) {
+        KDA_NORM_NARROW(KDA_NORM_BWD);
+        else if (P.dim <= 4096) KDA_NORM_BWD(64, 8, 1);
+        else if (P.dim <= 8192) KDA_NORM_BWD(64, 16, 1);
+        else KDA_NORM_BWD(64, 16, 2);
+    }
 #undef KDA_NORM_BWD
     if (P.dw || P.db)
         launch_column_sum(P.ws, 2 * P.dim, static_cast<int>(groups), {{P.dw, P.db, nullptr}, {P.dim, P.dim, 0}}, P.stream);
