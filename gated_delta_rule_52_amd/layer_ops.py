@@ -7,11 +7,10 @@ last dimension must be dense and the rows equally spaced.
 
 A decode step's kernels take a few microseconds, so the checks here look at a
 tensor once, in one condition, and work out what was wrong only where it fails;
-argument structs are filled by position, in the order of their fields.
+argument structs are packed by position, in the order of their fields.
 """
 from __future__ import annotations
 
-import ctypes
 from typing import Optional
 
 import torch
@@ -21,6 +20,9 @@ from .ops import _DT
 
 F32 = torch.float32
 _TOO_BIG = 2 ** 64 - 1
+_SCAN, _SCAN_BWD = _lib.packer(_lib.SelectiveScanArgs), _lib.packer(_lib.SelectiveScanBwdArgs)
+_CONV, _CONV_BWD = _lib.packer(_lib.ShortConvArgs), _lib.packer(_lib.ShortConvBwdArgs)
+_NORM, _NORM_BWD = _lib.packer(_lib.LayerNormArgs), _lib.packer(_lib.LayerNormBwdArgs)
 
 
 def _refuse(t, name, shape, dtype, device):
@@ -54,6 +56,8 @@ def _first(t, name: str, dims) -> torch.device:
         raise ValueError(f"{name} must be a device tensor")
     if t.dim() not in dims:
         raise ValueError(f"{name} has {t.dim()} dimensions, expected {' or '.join(map(str, dims))}")
+    if t.shape[-1] >> 31:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected sizes below 2^31")
     return t.device
 
 
@@ -84,49 +88,60 @@ def _step(t, name, shape, dtype, device) -> int:
 def _at(t, name, shape, dtype, device):
     """Checks a contiguous tensor (or None) and returns its address."""
     if t is None:
-        return None
+        return 0
     if t.dtype is not dtype or tuple(t.shape) != shape or t.device != device or not t.is_contiguous():
         _refuse(t, name, shape, dtype, device)
     return t.data_ptr()
 
 
 def _ptr(t):
-    return None if t is None else t.data_ptr()
+    return 0 if t is None else t.data_ptr()
 
 
-def _sequences(batch: int, cu_seqlens, device):
-    """(number of sequences, address of the offsets)"""
+def _new(like, shape, dtype):
+    """An output of `like`'s device, and its type where dtype is None."""
+    if dtype is None and like.is_contiguous():
+        return torch.empty_like(like)
+    return torch.empty(shape, dtype=dtype or like.dtype, device=like.device)
+
+
+def _sequences(x, cu_seqlens, device):
+    """(number of sequences, address of the offsets) of tokens [B,T,D] or [N,D]"""
+    if x.numel() >> 31 and max(x.shape) >> 31:  # the structs' sizes are int32
+        raise ValueError(f"the tokens have shape {tuple(x.shape)}, expected sizes below 2^31")
     if cu_seqlens is None:
-        return batch, None
+        return x.shape[0], 0
     return cu_seqlens.numel() - 1, _at(cu_seqlens, "cu_seqlens", (cu_seqlens.numel(),), torch.int32, device)
 
 
 def _stream(device) -> int:
-    # the address alone, without a Stream object around it (1.8 us of a decode step's 14)
+    # the address alone, without a Stream object around it (1.8 us less per call)
     return torch._C._cuda_getCurrentRawStream(device.index)
 
 
-def _call(name: str, args, device):
+def _call(name: str, args: bytes, device):
     if torch.cuda.current_device() == device.index:
-        status = _lib.layer_function(name)(ctypes.byref(args))
+        status = _lib.layer_function(name)(args)
     else:  # a launch goes to the current device
         with torch.cuda.device(device):
-            status = _lib.layer_function(name)(ctypes.byref(args))
+            status = _lib.layer_function(name)(args)
     if status:
         _lib.check(status)
 
 
-def _size(name: str, args) -> int:
+def _size(name: str, args: bytes) -> int:
     """A workspace query; invalid sizes raise."""
-    need = _lib.layer_function(name)(ctypes.byref(args))
+    need = _lib.layer_function(name)(args)
     if need == _TOO_BIG:
         raise _lib.KdaError(_lib.STATUS_CODE["KDA_ERR_BAD_SHAPE"], _lib.load().kda_last_error().decode())
     return need
 
 
-def _give_workspace(name: str, args, workspace, device):
-    """Puts a workspace of the size the call asks for into args; returns what holds it."""
-    need = _size(name, args)
+def _call_with_workspace(name: str, pack, front, back, workspace, device):
+    """Calls an entry point whose struct has workspace and workspace_bytes between `front` and `back`, with a
+    workspace of the size that it asks for."""
+    need = _size(name + "_workspace_bytes", pack(*front, 0, 0, *back))
+    at = 0
     if need:
         if workspace is None:
             workspace = torch.empty(need, dtype=torch.uint8, device=device)
@@ -134,8 +149,8 @@ def _give_workspace(name: str, args, workspace, device):
             raise ValueError("workspace must be a contiguous tensor on the call's device")
         elif workspace.numel() * workspace.element_size() < need:
             workspace = torch.empty(need, dtype=torch.uint8, device=device)
-        args.workspace, args.workspace_bytes = workspace.data_ptr(), need
-    return workspace
+        at = workspace.data_ptr()
+    _call(name, pack(*front, at, need, *back), device)
 
 
 def _grad_dtype(dtype) -> int:
@@ -147,29 +162,34 @@ def _grad_dtype(dtype) -> int:
 
 # ---- selective scan ------------------------------------------------------------------------------------
 
-def _scan_sizes(struct, u, ds, cu_seqlens):
-    device = _first(u, "u", (3,))
-    N, cu = _sequences(u.shape[0], cu_seqlens, device)
-    a = struct()
-    a.struct_size, a.cu_seqlens = ctypes.sizeof(struct), cu
-    a.batch, a.T, a.dim, a.ds, a.num_seqs = u.shape[0], u.shape[1], u.shape[2], ds, N
-    a.in_dtype = _kind(u, "u")
-    return a
+def _fields(struct, **values) -> bytes:
+    """A packed struct from its fields by name, the others zero."""
+    values["struct_size"] = _lib.packer(struct).size
+    return _lib.packer(struct).pack(*(values.get(name, 0) for name, _ in struct._fields_))
+
+
+def _batch(x, name, cu_seqlens):
+    device = _first(x, name, (3,))
+    N, cu = _sequences(x, cu_seqlens, device)
+    return dict(cu_seqlens=cu, batch=x.shape[0], T=x.shape[1], dim=x.shape[2], num_seqs=N, in_dtype=_kind(x, name))
 
 
 def selective_scan_fwd_workspace_bytes(u: torch.Tensor, ds: int, cu_seqlens: Optional[torch.Tensor] = None) -> int:
     """Bytes that ``selective_scan_fwd`` needs for u [B,T,D] and ds states per channel."""
-    return _size("kda_selective_scan_fwd_workspace_bytes", _scan_sizes(_lib.SelectiveScanArgs, u, ds, cu_seqlens))
+    return _size("kda_selective_scan_fwd_workspace_bytes",
+                 _fields(_lib.SelectiveScanArgs, ds=ds, **_batch(u, "u", cu_seqlens)))
 
 
 def selective_scan_bwd_workspace_bytes(u: torch.Tensor, ds: int, cu_seqlens: Optional[torch.Tensor] = None) -> int:
     """Bytes that ``selective_scan_bwd`` needs for u [B,T,D] and ds states per channel."""
-    return _size("kda_selective_scan_bwd_workspace_bytes", _scan_sizes(_lib.SelectiveScanBwdArgs, u, ds, cu_seqlens))
+    return _size("kda_selective_scan_bwd_workspace_bytes",
+                 _fields(_lib.SelectiveScanBwdArgs, ds=ds, **_batch(u, "u", cu_seqlens)))
 
 
 def _scan(u, dt, A, B, C, D, z, dt_bias, initial_state, cu_seqlens, dt_softplus, out_dtype, final_state,
           output_final_state, y):
-    """Checks and fills the arguments of the scan's forward and step; returns (args, y, final state, device)."""
+    """Checks the arguments of the scan's forward and step; returns (the struct's fields before the workspace, behind
+    it, y, final state, device)."""
     device = _first(u, "u", (2, 3))
     shape, dtype = u.shape, u.dtype
     kind = _kind(u, "u")
@@ -177,22 +197,21 @@ def _scan(u, dt, A, B, C, D, z, dt_bias, initial_state, cu_seqlens, dt_softplus,
         raise ValueError("A must be [D,ds]")
     dim, ds = shape[-1], A.shape[1]
     narrow = shape[:-1] + (ds,)
-    N, cu = _sequences(shape[0], cu_seqlens, device)
+    N, cu = _sequences(u, cu_seqlens, device)
     if final_state is None and output_final_state:
         final_state = torch.empty((N, dim, ds), dtype=F32, device=device)
     if y is None:
-        y = torch.empty(shape, dtype=out_dtype or dtype, device=device)
-    a = _lib.SelectiveScanArgs(
-        ctypes.sizeof(_lib.SelectiveScanArgs), u.data_ptr(), dt.data_ptr(), _at(A, "A", (dim, ds), F32, device),
+        y = _new(u, shape, out_dtype)
+    front = (
+        _SCAN.size, u.data_ptr(), dt.data_ptr(), _at(A, "A", (dim, ds), F32, device),
         B.data_ptr(), C.data_ptr(), _at(D, "D", (dim,), F32, device), _ptr(z),
         _at(dt_bias, "dt_bias", (dim,), F32, device), _at(initial_state, "initial_state", (N, dim, ds), F32, device),
         _at(final_state, "final_state", (N, dim, ds), F32, device), y.data_ptr(), cu,
         _step(u, "u", shape, dtype, device), _step(dt, "dt", shape, dtype, device),
         _step(B, "B", narrow, dtype, device), _step(C, "C", narrow, dtype, device),
         _step(z, "z", shape, dtype, device), _step(y, "y", shape, out_dtype or y.dtype, device),
-        shape[0], shape[1] if len(shape) == 3 else 1, dim, ds, N, kind, _kind(y, "y"), None, 0, _stream(device),
-        _lib.KDA_SCAN_DT_SOFTPLUS if dt_softplus else 0)
-    return a, y, final_state, device
+        shape[0], shape[1] if len(shape) == 3 else 1, dim, ds, N, kind, _kind(y, "y"))
+    return front, (_stream(device), _lib.KDA_SCAN_DT_SOFTPLUS if dt_softplus else 0), y, final_state, device
 
 
 def selective_scan_fwd(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.Tensor, C: torch.Tensor,
@@ -214,10 +233,9 @@ def selective_scan_fwd(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: to
     (y [B,T,D], final_state or None)."""
     if u.dim() != 3:
         raise ValueError("u must be [B,T,D]")
-    a, y, final_state, device = _scan(u, dt, A, B, C, D, z, dt_bias, initial_state, cu_seqlens, dt_softplus, out_dtype,
-                                      final_state, output_final_state, y)
-    held = _give_workspace("kda_selective_scan_fwd_workspace_bytes", a, workspace, device)  # noqa: F841
-    _call("kda_selective_scan_fwd", a, device)
+    front, back, y, final_state, device = _scan(u, dt, A, B, C, D, z, dt_bias, initial_state, cu_seqlens, dt_softplus,
+                                                out_dtype, final_state, output_final_state, y)
+    _call_with_workspace("kda_selective_scan_fwd", _SCAN.pack, front, back, workspace, device)
     return y, final_state
 
 
@@ -235,8 +253,9 @@ def selective_scan_step(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: t
         if state is None:
             raise ValueError("final_state is required when state is None")
         final_state = state
-    a, y, _, device = _scan(u, dt, A, B, C, D, z, dt_bias, state, None, dt_softplus, out_dtype, final_state, False, y)
-    _call("kda_selective_scan_step", a, device)
+    front, back, y, _, device = _scan(u, dt, A, B, C, D, z, dt_bias, state, None, dt_softplus, out_dtype, final_state,
+                                      False, y)
+    _call("kda_selective_scan_step", _SCAN.pack(*front, 0, 0, *back), device)
     return y
 
 
@@ -261,7 +280,7 @@ def selective_scan_bwd(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: to
         raise ValueError("A must be [D,ds]")
     dim, ds = shape[-1], A.shape[1]
     narrow = shape[:-1] + (ds,)
-    N, cu = _sequences(shape[0], cu_seqlens, device)
+    N, cu = _sequences(u, cu_seqlens, device)
     states = (N, dim, ds)
     if grad_initial_state is None and output_grad_initial_state:
         grad_initial_state = torch.empty(states, dtype=F32, device=device)
@@ -276,8 +295,8 @@ def selective_scan_bwd(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: to
     grads = (got["du"], got["ddt"], got["dB"], got["dC"], got["dz"])
     steps = [_step(t, n, s, grad_dtype, device) for t, n, s in
              zip(grads, ("du", "ddt", "dB", "dC", "dz"), (shape, shape, narrow, narrow, shape))]
-    a = _lib.SelectiveScanBwdArgs(
-        ctypes.sizeof(_lib.SelectiveScanBwdArgs), u.data_ptr(), dt.data_ptr(), _at(A, "A", (dim, ds), F32, device),
+    front = (
+        _SCAN_BWD.size, u.data_ptr(), dt.data_ptr(), _at(A, "A", (dim, ds), F32, device),
         B.data_ptr(), C.data_ptr(), _at(D, "D", (dim,), F32, device), _ptr(z),
         _at(dt_bias, "dt_bias", (dim,), F32, device), _at(initial_state, "initial_state", states, F32, device),
         grad_y.data_ptr(), _at(grad_final_state, "grad_final_state", states, F32, device),
@@ -287,31 +306,30 @@ def selective_scan_bwd(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: to
         _step(u, "u", shape, dtype, device), _step(dt, "dt", shape, dtype, device),
         _step(B, "B", narrow, dtype, device), _step(C, "C", narrow, dtype, device),
         _step(z, "z", shape, dtype, device), _step(grad_y, "grad_y", shape, dtype, device), *steps,
-        shape[0], shape[1], dim, ds, N, kind, grad_kind, None, 0, _stream(device),
-        _lib.KDA_SCAN_DT_SOFTPLUS if dt_softplus else 0)
-    held = _give_workspace("kda_selective_scan_bwd_workspace_bytes", a, workspace, device)  # noqa: F841
-    _call("kda_selective_scan_bwd", a, device)
+        shape[0], shape[1], dim, ds, N, kind, grad_kind)
+    back = _stream(device), _lib.KDA_SCAN_DT_SOFTPLUS if dt_softplus else 0
+    _call_with_workspace("kda_selective_scan_bwd", _SCAN_BWD.pack, front, back, workspace, device)
     return got
 
 
 # ---- short convolution ---------------------------------------------------------------------------------
 
 def _conv(x, weight, bias, initial_state, cu_seqlens, silu, out_dtype, final_state, output_final_state, y):
-    """Checks and fills the arguments of the convolution's forward and step; returns (args, y, final state, device)."""
+    """Checks and packs the arguments of the convolution's forward and step; returns (args, y, final state, device)."""
     device = _first(x, "x", (2, 3))
     shape, dtype = x.shape, x.dtype
     kind = _kind(x, "x")
     if weight.dim() != 2:
         raise ValueError("weight must be [D,W]")
     dim, width = shape[-1], weight.shape[1]
-    N, cu = _sequences(shape[0], cu_seqlens, device)
+    N, cu = _sequences(x, cu_seqlens, device)
     states = (N, width - 1, dim)
     if final_state is None and output_final_state:
         final_state = torch.empty(states, dtype=dtype, device=device)
     if y is None:
-        y = torch.empty(shape, dtype=out_dtype or dtype, device=device)
-    a = _lib.ShortConvArgs(
-        ctypes.sizeof(_lib.ShortConvArgs), x.data_ptr(), _at(weight, "weight", (dim, width), weight.dtype, device),
+        y = _new(x, shape, out_dtype)
+    a = _CONV.pack(
+        _CONV.size, x.data_ptr(), _at(weight, "weight", (dim, width), weight.dtype, device),
         _at(bias, "bias", (dim,), weight.dtype, device), _at(initial_state, "initial_state", states, dtype, device),
         _at(final_state, "final_state", states, dtype, device), y.data_ptr(), cu, _step(x, "x", shape, dtype, device),
         _step(y, "y", shape, out_dtype or y.dtype, device), shape[0], shape[1] if len(shape) == 3 else 1, dim, width, N,
@@ -358,13 +376,8 @@ def short_conv_step(x: torch.Tensor, weight: torch.Tensor, state: Optional[torch
 
 def short_conv_bwd_workspace_bytes(x: torch.Tensor, width: int, cu_seqlens: Optional[torch.Tensor] = None) -> int:
     """Bytes that ``short_conv_bwd`` needs for x [B,T,D] and `width` taps."""
-    device = _first(x, "x", (3,))
-    a = _lib.ShortConvBwdArgs()
-    a.struct_size = ctypes.sizeof(a)
-    a.num_seqs, a.cu_seqlens = _sequences(x.shape[0], cu_seqlens, device)
-    a.batch, a.T, a.dim, a.width = x.shape[0], x.shape[1], x.shape[2], width
-    a.in_dtype = _kind(x, "x")
-    return _size("kda_short_conv_bwd_workspace_bytes", a)
+    return _size("kda_short_conv_bwd_workspace_bytes",
+                 _fields(_lib.ShortConvBwdArgs, width=width, **_batch(x, "x", cu_seqlens)))
 
 
 def short_conv_bwd(x: torch.Tensor, weight: torch.Tensor, grad_y: torch.Tensor, bias: Optional[torch.Tensor] = None,
@@ -383,24 +396,23 @@ def short_conv_bwd(x: torch.Tensor, weight: torch.Tensor, grad_y: torch.Tensor, 
     if weight.dim() != 2:
         raise ValueError("weight must be [D,W]")
     dim, width = shape[-1], weight.shape[1]
-    N, cu = _sequences(shape[0], cu_seqlens, device)
+    N, cu = _sequences(x, cu_seqlens, device)
     states = (N, width - 1, dim)
     if grad_initial_state is None and output_grad_initial_state:
         grad_initial_state = torch.empty(states, dtype=F32, device=device)
     dx = out["dx"] if out is not None else torch.empty(shape, dtype=grad_dtype, device=device)
     got = dict(dx=dx, dweight=torch.empty((dim, width), dtype=F32, device=device),
                dbias=None if bias is None else torch.empty((dim,), dtype=F32, device=device), dh0=grad_initial_state)
-    a = _lib.ShortConvBwdArgs(
-        ctypes.sizeof(_lib.ShortConvBwdArgs), x.data_ptr(), _at(weight, "weight", (dim, width), weight.dtype, device),
+    front = (
+        _CONV_BWD.size, x.data_ptr(), _at(weight, "weight", (dim, width), weight.dtype, device),
         _at(bias, "bias", (dim,), weight.dtype, device), _at(initial_state, "initial_state", states, dtype, device),
         grad_y.data_ptr(), _at(grad_final_state, "grad_final_state", states, F32, device), dx.data_ptr(),
         got["dweight"].data_ptr(), _ptr(got["dbias"]),
         _at(grad_initial_state, "grad_initial_state", states, F32, device), cu, _step(x, "x", shape, dtype, device),
         _step(grad_y, "grad_y", shape, dtype, device), _step(dx, "dx", shape, grad_dtype, device), shape[0], shape[1],
-        dim, width, N, kind, grad_kind, _kind(weight, "weight"), None, 0, _stream(device),
-        _lib.KDA_CONV_SILU if silu else 0)
-    held = _give_workspace("kda_short_conv_bwd_workspace_bytes", a, workspace, device)  # noqa: F841
-    _call("kda_short_conv_bwd", a, device)
+        dim, width, N, kind, grad_kind, _kind(weight, "weight"))
+    back = _stream(device), _lib.KDA_CONV_SILU if silu else 0
+    _call_with_workspace("kda_short_conv_bwd", _CONV_BWD.pack, front, back, workspace, device)
     return got
 
 
@@ -420,12 +432,12 @@ def layer_norm_fwd(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias:
     w = weight if weight is not None else bias
     wd = F32 if w is None else w.dtype
     if y is None:
-        y = torch.empty(shape, dtype=out_dtype or dtype, device=device)
+        y = _new(x, shape, out_dtype)
     if residual is not None and residual_out is None:
-        residual_out = torch.empty(shape, dtype=residual.dtype, device=device)
+        residual_out = _new(residual, shape, None)
     rd = F32 if residual is None else residual.dtype
-    a = _lib.LayerNormArgs(
-        ctypes.sizeof(_lib.LayerNormArgs), x.data_ptr(), _ptr(residual), _at(weight, "weight", (dim,), wd, device),
+    a = _NORM.pack(
+        _NORM.size, x.data_ptr(), _ptr(residual), _at(weight, "weight", (dim,), wd, device),
         _at(bias, "bias", (dim,), wd, device), y.data_ptr(), _ptr(residual_out), _step(x, "x", shape, dtype, device),
         _step(residual, "residual", shape, rd, device), _step(y, "y", shape, out_dtype or y.dtype, device),
         _step(residual_out, "residual_out", shape, rd, device), x.numel() // dim if dim else 0, dim, eps, kind,
@@ -436,12 +448,9 @@ def layer_norm_fwd(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias:
 
 def layer_norm_bwd_workspace_bytes(x: torch.Tensor) -> int:
     """Bytes that ``layer_norm_bwd`` needs for x [..., D] with a weight or bias gradient."""
-    a = _lib.LayerNormBwdArgs()
-    a.struct_size = ctypes.sizeof(a)
-    a.dim = x.shape[-1]
-    a.rows = x.numel() // a.dim if a.dim else 0
-    a.grad_weight = 1
-    return _size("kda_layer_norm_bwd_workspace_bytes", a)
+    dim = x.shape[-1]
+    return _size("kda_layer_norm_bwd_workspace_bytes",
+                 _fields(_lib.LayerNormBwdArgs, dim=dim, rows=x.numel() // dim if dim else 0, grad_weight=1))
 
 
 def layer_norm_bwd(x: torch.Tensor, grad_y: torch.Tensor, weight: Optional[torch.Tensor] = None,
@@ -466,13 +475,11 @@ def layer_norm_bwd(x: torch.Tensor, grad_y: torch.Tensor, weight: Optional[torch
     got = dict(dx=dx, dweight=None if weight is None else torch.empty((dim,), dtype=F32, device=device),
                dbias=None if bias is None else torch.empty((dim,), dtype=F32, device=device))
     _at(bias, "bias", (dim,), wd, device)
-    a = _lib.LayerNormBwdArgs(
-        ctypes.sizeof(_lib.LayerNormBwdArgs), x.data_ptr(), grad_y.data_ptr(), _at(weight, "weight", (dim,), wd, device),
+    front = (
+        _NORM_BWD.size, x.data_ptr(), grad_y.data_ptr(), _at(weight, "weight", (dim,), wd, device),
         _ptr(grad_residual), dx.data_ptr(), _ptr(got["dweight"]), _ptr(got["dbias"]), _step(x, "x", shape, dtype, device),
         _step(grad_y, "grad_y", shape, gd, device), _step(grad_residual, "grad_residual", shape, rd, device),
         _step(dx, "dx", shape, grad_dtype, device), x.numel() // dim if dim else 0, dim, eps, kind,
-        _kind(grad_y, "grad_y"), _kind(grad_residual, "grad_residual"), _kind(w, "weight"), grad_kind, None, 0,
-        _stream(device))
-    held = _give_workspace("kda_layer_norm_bwd_workspace_bytes", a, workspace, device)  # noqa: F841
-    _call("kda_layer_norm_bwd", a, device)
+        _kind(grad_y, "grad_y"), _kind(grad_residual, "grad_residual"), _kind(w, "weight"), grad_kind)
+    _call_with_workspace("kda_layer_norm_bwd", _NORM_BWD.pack, front, (_stream(device),), workspace, device)
     return got

@@ -554,6 +554,22 @@ def test_refusals(kda):
             f()
 
 
+def test_sizes_past_32_bits_are_refused(kda):
+    """One element seen 2^31 times: the argument structs hold sizes in 32 bits."""
+    import torch
+    one, many = torch.zeros(1, 1, 1, device="cuda"), 2 ** 31
+    w, A = torch.ones(1, 4, device="cuda"), -torch.ones(1, 4, device="cuda")
+    for x in (one.expand(1, many, 1), one.expand(many, 1, 1), one.expand(1, 1, many)):
+        n = one.expand(*x.shape[:2], 4)
+        for call in (lambda: kda.selective_scan_fwd(x, x, A, n, n), lambda: kda.selective_scan_bwd(x, x, A, n, n, x),
+                     lambda: kda.short_conv_fwd(x, w), lambda: kda.short_conv_bwd(x, w, x),
+                     lambda: kda.selective_scan_fwd_workspace_bytes(x, 4), lambda: kda.short_conv_bwd_workspace_bytes(x, 4)):
+            with pytest.raises(ValueError):
+                call()
+    with pytest.raises(ValueError):
+        kda.layer_norm_fwd(one.expand(1, 1, many))
+
+
 def test_rows_past_32_bits(kda):
     """Rows whose offsets pass 2^32 elements, as slices of a very wide buffer: the same bits as a dense copy."""
     import torch

@@ -124,6 +124,16 @@ def test_struct_size_and_null(name, make):
     assert fn(None) == S[NULL]
 
 
+@pytest.mark.parametrize("struct", sorted({s for s, _ in _lib.LAYER_FUNCTIONS.values()}, key=lambda s: s.__name__))
+def test_packed_structs_have_the_layout_of_the_c_ones(struct):
+    """Every field packed with a value of its own comes back from the same bytes read as the C struct."""
+    pack = _lib.packer(struct)
+    assert pack.size == ctypes.sizeof(struct)
+    values = [float(i + 1) if kind is ctypes.c_float else i + 1 for i, (_, kind) in enumerate(struct._fields_)]
+    read = struct.from_buffer_copy(pack.pack(*values))
+    assert [getattr(read, name) for name, _ in struct._fields_] == values
+
+
 def test_empty_calls_are_no_ops():
     for name, make in (("kda_selective_scan_fwd", scan), ("kda_short_conv_fwd", conv)):
         assert _lib.layer_raw(name, make(batch=0, num_seqs=0)) == 0
