@@ -3,8 +3,8 @@
 //     y = (s - mean) rstd w + b, s = x + residual;      with g = dy w, xh = (s - mean) rstd:
 //     dx = rstd (g - mean(g) - xh mean(g xh)) + dres,   dw = sum dy xh,   db = sum dy
 //
-// Bound by HBM.  A row stays in registers between its one read and its one write, so mean and variance take
-// two exact passes over registers and cost no memory.  A row is held by LANES lanes of a wave (short rows:
+// Bound by HBM.  A row stays in registers between its one read and its one write, so the deviations are summed
+// around a mean already known and cost no memory.  A row is held by LANES lanes of a wave (short rows:
 // several per wave) or by a workgroup of WAVES waves; a lane holds U units of 8 elements.  The backward pass
 // gives each workgroup a share of the rows and keeps its part of dw and db in registers over all of them:
 // one partial row per workgroup, summed by the column sum in a fixed order.
@@ -175,7 +175,8 @@ __device__ __forceinline__ RowSums row_sums(const float (&x)[U][8], const float 
         r.g = sg;
         r.gx = sx;
     }
-    r.rstd = __builtin_amdgcn_rsqf(fmaf(m2, inv_dim, eps));
+    const float var = fmaf(m2, inv_dim, eps);  // the instruction takes a denormal (eps of 0, tiny values) as 0
+    r.rstd = var < 0x1p-120f ? __builtin_amdgcn_rsqf(var * 0x1p60f) * 0x1p30f : __builtin_amdgcn_rsqf(var);
     r.gx *= r.rstd;
     return r;
 }

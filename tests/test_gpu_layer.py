@@ -452,6 +452,21 @@ def test_norm_gradients(kda, rows, dim, dtype, rdtype, wdtype, out, sliced):
         assert got["dweight"] is None and got["dbias"] is None
 
 
+@pytest.mark.parametrize("dim", [64, 777, 5001])
+def test_norm_of_a_denormal_variance(kda, dim):
+    """eps = 0 and values of 2^-64: a variance near 2^-128.  Its summands and its own rounding are on the grid of
+    2^-149, off by 2^-150 each, which is 2^-22 of it: 4 roundings of 2^-24 twice over, of which the root takes half;
+    the gradient has the root three times."""
+    x = rounded(np.random.default_rng(dim).normal(size=(5, dim)), "fp32") * 2.0 ** -64
+    y = kda.layer_norm_fwd(dev(x), eps=0.0)
+    want = ref.norm_forward(x, None, None, 0.0)[0]
+    ref.check("y", host(y), want, ref.norm_scales(x, None, None, None, 0.0)["y"], ROW + 8)
+    gy = rounded(np.random.default_rng(1).normal(size=(5, dim)), "fp32") * 2.0 ** -64
+    got = kda.layer_norm_bwd(dev(x), dev(gy), eps=0.0)
+    ref.check("dx", host(got["dx"]), ref.norm_backward(x, None, gy, 0.0)["dx"],
+              ref.norm_scales(x, None, None, gy, 0.0)["dx"], ROW + 24)
+
+
 def test_norm_of_heads_and_far_means(kda):
     """The recurrence's output [B,T,H,dv] row by row, and rows whose mean is far above their spread."""
     import torch
