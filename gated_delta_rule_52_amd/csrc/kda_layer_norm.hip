@@ -108,15 +108,24 @@ __device__ __forceinline__ float lanes_sum(float x) {
 struct RowSums {
     float mean, rstd, g, gx;  // g: sum of g, gx: sum of g times the normalised x (0 without g)
 };
-template <int LANES, int WAVES, int U, bool GRAD>
+// BACK: a row's last unit was moved back inside the row, and its first elements are the neighbour's; otherwise the
+// values past the row are zeros.
+template <int LANES, int WAVES, int U, bool GRAD, bool BACK>
 __device__ __forceinline__ RowSums row_sums(const float (&x)[U][8], const float (&g)[U][8], const float (&w)[U][8], int lane,
                                             int dim, float inv_n, float n, float inv_dim, float eps, float (*shared)[4]) {
     constexpr int SPAN = LANES * WAVES;
     float s = 0.f;
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+    for (int u = 0; u < U; ++u) {
+        const int left = dim - first_col<SPAN>(lane, u);
+        if (!BACK || left >= 8) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s += x[u][i];  // zeros past the row
+            for (int i = 0; i < 8; ++i) s += x[u][i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s += i >= 8 - left ? x[u][i] : 0.f;
+        }
+    }
     const float p = lanes_sum<LANES>(s) * inv_n;
     float m2 = 0.f, sg = 0.f, sx = 0.f;
 #pragma unroll
@@ -128,16 +137,19 @@ __device__ __forceinline__ RowSums row_sums(const float (&x)[U][8], const float 
                 const float d = x[u][i] - p;
                 m2 = fmaf(d, d, m2);
                 if (GRAD) sx = fmaf(g[u][i] * w[u][i], d, sx);
+                if (GRAD && BACK) sg = fmaf(g[u][i], w[u][i], sg);
             }
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float d = i < left ? x[u][i] - p : 0.f;
+                const bool in = BACK ? i >= 8 - left : i < left;
+                const float d = in ? x[u][i] - p : 0.f;
                 m2 = fmaf(d, d, m2);
                 if (GRAD) sx = fmaf(g[u][i] * w[u][i], d, sx);
+                if (GRAD && BACK) sg = fmaf(in ? g[u][i] : 0.f, w[u][i], sg);
             }
         }
-        if (GRAD) {
+        if (GRAD && !BACK) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) sg = fmaf(g[u][i], w[u][i], sg);
         }
@@ -149,8 +161,8 @@ __device__ __forceinline__ RowSums row_sums(const float (&x)[U][8], const float 
     }
     RowSums r{p, 0.f, sg, sx};
     if constexpr (WAVES > 1) {
-        const int wave = threadIdx.x >> 6;
-        if ((threadIdx.x & 63) == 0) {
+        const int wave = lane >> 6;
+        if ((lane & 63) == 0) {
             shared[2 * wave][0] = n;
             shared[2 * wave][1] = p;
             shared[2 * wave][2] = m2;
@@ -195,9 +207,9 @@ __device__ __forceinline__ float wave_count(int lane, int dim) {
 }
 
 template <int LANES, int WAVES>
-constexpr int norm_threads() { return WAVES == 1 ? 256 : 64 * WAVES; }
+constexpr int norm_threads() { return WAVES <= 4 ? 256 : 64 * WAVES; }
 template <int LANES, int WAVES>
-constexpr int rows_per_group() { return WAVES == 1 ? 256 / LANES : 1; }
+constexpr int rows_per_group() { return norm_threads<LANES, WAVES>() / (LANES * WAVES); }
 
 template <int LANES, int WAVES, int U>
 __global__ void __launch_bounds__((norm_threads<LANES, WAVES>())) norm_fwd_kernel(NormFwdLaunch P) {
@@ -228,7 +240,7 @@ __global__ void __launch_bounds__((norm_threads<LANES, WAVES>())) norm_fwd_kerne
             for (int i = 0; i < 8; ++i) x[u][i] = 0.f;
         }
     }
-    const RowSums s = row_sums<LANES, WAVES, U, false>(x, x, x, lane, P.dim, n > 0.f ? 1.f / n : 0.f, n, inv_dim, P.eps, shared);
+    const RowSums s = row_sums<LANES, WAVES, U, false, false>(x, x, x, lane, P.dim, n > 0.f ? 1.f / n : 0.f, n, inv_dim, P.eps, shared);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const int col = first_col<SPAN>(lane, u), left = P.dim - col;
@@ -244,71 +256,110 @@ __global__ void __launch_bounds__((norm_threads<LANES, WAVES>())) norm_fwd_kerne
     }
 }
 
-template <int LANES, int WAVES, int U>
+// The next rows' loads are issued before a row's sums and wait in registers behind its stores, so that the exchange
+// and its barrier leave HBM busy.  Loads carry no branch: the unit that a row's end cuts is moved back inside,
+// computes some of its neighbour's elements again and stores the same values; only the sums leave them out.  That
+// takes rows of 8 elements; TINY ones are read singly, by one lane each.
+template <int U, bool Bf16, bool TINY>
+struct RawRow {
+    any4 v[U][Bf16 && !TINY ? 1 : 2];
+    // lanes with nothing to read (left <= 0) read what their neighbour does
+    __device__ __forceinline__ void load(const char *at, uint32_t off, const uint32_t (&col)[U], int left) {
+        if constexpr (TINY) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                v[0][i / 4][i % 4] = 0;
+                if (i >= left) continue;
+                if (Bf16) v[0][i / 4][i % 4] = static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(at + off)[i]) << 16;
+                else v[0][i / 4][i % 4] = reinterpret_cast<const uint32_t *>(at + off)[i];
+            }
+        } else {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int k = 0; k < (Bf16 ? 1 : 2); ++k)
+                    v[u][k] = reinterpret_cast<const any4 *>(at + (off + col[u] * (Bf16 ? 2 : 4)))[k];
+        }
+    }
+    __device__ __forceinline__ void widen(float (&x)[U][8]) const {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if constexpr (Bf16 && !TINY) x[u][i] = __uint_as_float(i & 1 ? v[u][0][i / 2] & 0xffff0000u : v[u][0][i / 2] << 16);
+                else x[u][i] = __uint_as_float(v[u][i / 4][i % 4]);
+    }
+};
+template <int LANES, int WAVES, int U, bool XBf16, bool GBf16, bool TINY>
 __global__ void __launch_bounds__((norm_threads<LANES, WAVES>())) norm_bwd_kernel(NormBwdLaunch P) {
     constexpr int SPAN = LANES * WAVES, ROWS = rows_per_group<LANES, WAVES>();
-    __shared__ float shared[2][2 * WAVES][4];  // two rows' exchanges: one barrier each
+    constexpr bool AHEAD = U == 1 || WAVES <= 8 || (XBf16 && GBf16);  // 16 waves leave the others no registers for it
+    __shared__ float shared[2][ROWS][2 * WAVES][4];     // two rows' exchanges: one barrier each
     __shared__ float fold[ROWS > 1 ? 256 * 8 : 1];
-    const int lane = threadIdx.x % SPAN, sub = threadIdx.x / SPAN;
+    const int lane = threadIdx.x % SPAN, sub = ROWS > 1 ? threadIdx.x / SPAN : 0;
     float w[U][8], dw[U][8], db[U][8], x[U][8], g[U][8];
+    uint32_t col[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        const int col = first_col<SPAN>(lane, u);
+        const int c = first_col<SPAN>(lane, u);
+        col[u] = TINY ? 0 : c + 8 > P.dim ? P.dim - 8 : c;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             w[u][i] = 1.f;
-            x[u][i] = g[u][i] = dw[u][i] = db[u][i] = 0.f;
+            dw[u][i] = db[u][i] = 0.f;
         }
-        if (P.w && col < P.dim) load_param(P.w, P.w_bf16, col, P.dim - col, w[u]);
+        if (P.w) load_param(P.w, P.w_bf16, col[u], TINY ? P.dim : 8, w[u]);
     }
+    const int tiny = lane == 0 ? P.dim : 0;  // elements of a TINY row
     const float n = wave_count<LANES, WAVES, U>(lane, P.dim), inv_n = n > 0.f ? 1.f / n : 0.f;
     const float inv_dim = 1.f / static_cast<float>(P.dim);
+    auto row_at = [](const Rows &r, int64_t row) { return static_cast<char *>(r.p) + row * r.stride * (r.bf16 ? 2 : 4); };
+    auto step = [](const Rows &r) { return static_cast<uint32_t>(r.stride) * (r.bf16 ? 2 : 4); };
+    RawRow<U, XBf16, TINY> nx;
+    RawRow<U, GBf16, TINY> ng;
+    // of the rows from `base` on this lane's, or the last one there is
+    auto load = [&](int64_t base) {
+        const int last = P.rows - 1 - base < ROWS ? static_cast<int>(P.rows - 1 - base) : ROWS - 1;
+        const uint32_t k = sub < last ? sub : last;
+        nx.load(row_at(P.x, base), k * step(P.x), col, tiny);
+        ng.load(row_at(P.gy, base), k * step(P.gy), col, tiny);
+    };
     const int64_t stride = static_cast<int64_t>(gridDim.x) * ROWS;
     int64_t base = static_cast<int64_t>(blockIdx.x) * ROWS;
-    Walk wx(P.x, base, sub, lane), wg(P.gy, base, sub, lane), wr(P.gres, base, sub, lane), wd(P.dx, base, sub, lane);
-    // whole rounds for every lane of the workgroup: lanes past the last row hold what they had and are not counted
+    if (AHEAD) load(base);
+    // whole rounds for every lane of the workgroup: lanes past the last row store and count nothing
     for (int round = 0; base < P.rows; base += stride, round ^= 1) {
-        const bool live = base + sub < P.rows;
-        if (live) {
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int left = P.dim - first_col<SPAN>(lane, u), more = u * SPAN * 8;
-                if (left > 0) {
-                    load8(wx.unit(more), P.x.bf16, left, x[u]);
-                    load8(wg.unit(more), P.gy.bf16, left, g[u]);
-                }
-            }
-        }
-        const RowSums s = row_sums<LANES, WAVES, U, true>(x, g, w, lane, P.dim, inv_n, n, inv_dim, P.eps, shared[round]);
+        if (!AHEAD) load(base);
+        nx.widen(x);
+        ng.widen(g);
+        if (AHEAD) load(base + stride < P.rows ? base + stride : base);
+        const bool live = ROWS == 1 || base + sub < P.rows;
+        const RowSums s = row_sums<LANES, WAVES, U, true, !TINY>(x, g, w, lane, P.dim, inv_n, n, inv_dim, P.eps, shared[round][sub]);
         const float m1 = s.g * inv_dim, m2 = s.gx * inv_dim;
         if (live) {
+            const char *res = row_at(P.gres, base) + sub * step(P.gres);
+            char *dx = row_at(P.dx, base) + sub * step(P.dx);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int left = P.dim - first_col<SPAN>(lane, u), more = u * SPAN * 8;
-                if (left <= 0) continue;
+                const int left = TINY ? tiny : first_col<SPAN>(lane, u) < P.dim ? 8 : 0;
                 float r[8] = {};
-                if (P.gres.p) load8(wr.unit(more), P.gres.bf16, left, r);
+                if (P.gres.p) load8(res + col[u] * (P.gres.bf16 ? 2 : 4), P.gres.bf16, TINY ? tiny : 8, r);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const float xh = (x[u][i] - s.mean) * s.rstd;  // past the row g is 0
+                    const float xh = (x[u][i] - s.mean) * s.rstd;  // past a TINY row g is 0
                     dw[u][i] = fmaf(g[u][i], xh, dw[u][i]);
                     db[u][i] += g[u][i];
                     r[i] = fmaf(s.rstd, fmaf(g[u][i], w[u][i], -fmaf(xh, m2, m1)), r[i]);
                 }
-                store8(wd.unit(more), P.dx.bf16, left, r);
+                if (left > 0) store8(dx + col[u] * (P.dx.bf16 ? 2 : 4), P.dx.bf16, TINY ? tiny : 8, r);
             }
         }
-        wx.at += stride * wx.step;
-        wg.at += stride * wg.step;
-        wr.at += stride * wr.step;
-        wd.at += stride * wd.step;
     }
     if (!P.ws) return;
     // one partial row of dw and of db per workgroup
     float *pw = P.ws + static_cast<int64_t>(blockIdx.x) * 2 * P.dim, *pb = pw + P.dim;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        const int col = first_col<SPAN>(lane, u);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             float (&v)[8] = half ? db[u] : dw[u];
@@ -326,11 +377,8 @@ __global__ void __launch_bounds__((norm_threads<LANES, WAVES>())) norm_bwd_kerne
                     }
                 }
             }
-            if (sub == 0) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (col + i < P.dim) (half ? pb : pw)[col + i] = v[i];
-            }
+            if (sub == 0 && first_col<SPAN>(lane, u) < P.dim)
+                store8(reinterpret_cast<char *>((half ? pb : pw) + col[u]), 0, TINY ? P.dim : 8, v);
         }
     }
 }
@@ -359,25 +407,16 @@ __global__ void __launch_bounds__(1024) column_sum_kernel(const float *in, int64
     }
 }
 
-// The smallest arrangement that holds a row: 16 lanes (to 128 elements), 32, a wave (to 1,024), then several.  The
-// backward pass, which keeps five values per element, spreads wide rows further, over 16-wave workgroups of one unit
-// per lane (8,192 x 4,096 bf16: 71 us with 8 waves, 84 with 4).
-#define KDA_NORM_NARROW(CALL)                      \
-    if (P.dim <= 128) CALL(16, 1, 1);              \
-    else if (P.dim <= 256) CALL(32, 1, 1);         \
-    else if (P.dim <= 512) CALL(64, 1, 1);         \
-    else if (P.dim <= 1024) CALL(64, 1, 2);        \
-    else if (P.dim <= 2048) CALL(64, 4, 1)
-
+// Rows per workgroup of the backward pass, as its launch arranges them.
 int rows_of(int dim) {
-    return dim <= 128 ? 16 : dim <= 256 ? 8 : dim <= 1024 ? 4 : 1;
+    return dim <= 128 ? 16 : dim <= 256 ? 8 : dim <= 1024 ? 4 : dim <= 2048 ? 2 : 1;
 }
-// The backward pass's workgroups: as many as are resident at once, by its registers.  More leave a second, short
-// round and more partial rows to sum; fewer leave the chip (32,768 x 1,024 bf16: 56 us with 768, 74 with 1,024;
-// 16,384 x 2,048: 58 with 1,280, 77 with 512; 262,144 x 128: 47 with 1,024, 60 with 512).
+// The backward pass's workgroups: no more than are resident at once, and of these as few as keep HBM busy, as each
+// adds a partial row to sum (32,768 x 1,024 bf16: 45 us with 768, 47 with 512, 52 with 1,024; 262,144 x 128: 45
+// with 1,024, 46 with 768, 54 with 512; 8,192 x 4,096: 53 with 512, 61 with 256).
 int64_t bwd_groups(int64_t rows, int dim) {
     const int64_t whole = (rows + rows_of(dim) - 1) / rows_of(dim);
-    const int64_t most = dim <= 128 ? 1024 : dim <= 512 ? 1280 : dim <= 1024 ? 768 : dim <= 2048 ? 1280 : dim <= 4096 ? 512 : 256;
+    const int64_t most = dim <= 512 ? 1024 : dim <= 2048 ? 768 : dim <= 4096 ? 512 : 256;
     return whole < most ? whole : most;
 }
 
@@ -388,11 +427,16 @@ void launch_column_sum(const float *in, int64_t ld, int parts, const ColumnSums 
     if (cols > 0) column_sum_kernel<<<static_cast<unsigned>((cols + 15) / 16), 1024, 0, stream>>>(in, ld, parts, to);
 }
 
+// The smallest arrangement that holds a row: 16 lanes (to 128 elements), 32, a wave (to 1,024), then several.
 hipError_t launch_norm_fwd(const NormFwdLaunch &P) {
 #define KDA_NORM_FWD(L, W, U)                                                                                    \
     norm_fwd_kernel<L, W, U><<<static_cast<unsigned>((P.rows + rows_per_group<L, W>() - 1) / rows_per_group<L, W>()), \
                                norm_threads<L, W>(), 0, P.stream>>>(P)
-    KDA_NORM_NARROW(KDA_NORM_FWD);
+    if (P.dim <= 128) KDA_NORM_FWD(16, 1, 1);
+    else if (P.dim <= 256) KDA_NORM_FWD(32, 1, 1);
+    else if (P.dim <= 512) KDA_NORM_FWD(64, 1, 1);
+    else if (P.dim <= 1024) KDA_NORM_FWD(64, 1, 2);
+    else if (P.dim <= 2048) KDA_NORM_FWD(64, 4, 1);
     else if (P.dim <= 4096) KDA_NORM_FWD(64, 4, 2);
     else if (P.dim <= 8192) KDA_NORM_FWD(64, 8, 2);
     else KDA_NORM_FWD(64, 16, 2);
@@ -404,17 +448,31 @@ size_t norm_bwd_workspace_bytes(int64_t rows, int dim) {
     return static_cast<size_t>(bwd_groups(rows, dim)) * 2 * dim * 4;
 }
 
+template <int LANES, int WAVES, int U, bool TINY = false>
+static void launch_bwd(const NormBwdLaunch &P, int64_t groups) {
+    const unsigned grid = static_cast<unsigned>(groups);
+    constexpr int threads = norm_threads<LANES, WAVES>();
+    if (P.x.bf16 && P.gy.bf16) norm_bwd_kernel<LANES, WAVES, U, true, true, TINY><<<grid, threads, 0, P.stream>>>(P);
+    else if (P.x.bf16) norm_bwd_kernel<LANES, WAVES, U, true, false, TINY><<<grid, threads, 0, P.stream>>>(P);
+    else if (P.gy.bf16) norm_bwd_kernel<LANES, WAVES, U, false, true, TINY><<<grid, threads, 0, P.stream>>>(P);
+    else norm_bwd_kernel<LANES, WAVES, U, false, false, TINY><<<grid, threads, 0, P.stream>>>(P);
+}
+
 hipError_t launch_norm_bwd(const NormBwdLaunch &P) {
     const int64_t groups = bwd_groups(P.rows, P.dim);
-#define KDA_NORM_BWD(L, W, U) \
-    norm_bwd_kernel<L, W, U><<<static_cast<unsigned>(groups), norm_threads<L, W>(), 0, P.stream>>>(P)
+    // As many units per lane as registers hold the next row's loads beside: rows in fewer waves spend less on the
+    // exchange (8,192 x 8,192 bf16: 94 us with 8 waves of two units, 124 with 16 of one).
     if (groups > 0) {
-        KDA_NORM_NARROW(KDA_NORM_BWD);
-        else if (P.dim <= 4096) KDA_NORM_BWD(64, 8, 1);
-        else if (P.dim <= 8192) KDA_NORM_BWD(64, 16, 1);
-        else KDA_NORM_BWD(64, 16, 2);
+        if (P.dim < 8) launch_bwd<16, 1, 1, true>(P, groups);
+        else if (P.dim <= 128) launch_bwd<16, 1, 1>(P, groups);
+        else if (P.dim <= 256) launch_bwd<32, 1, 1>(P, groups);
+        else if (P.dim <= 512) launch_bwd<64, 1, 1>(P, groups);
+        else if (P.dim <= 1024) launch_bwd<64, 1, 2>(P, groups);
+        else if (P.dim <= 2048) launch_bwd<64, 2, 2>(P, groups);
+        else if (P.dim <= 4096) launch_bwd<64, 4, 2>(P, groups);
+        else if (P.dim <= 8192) launch_bwd<64, 8, 2>(P, groups);
+        else launch_bwd<64, 16, 2>(P, groups);
     }
-#undef KDA_NORM_BWD
     if (P.dw || P.db)
         launch_column_sum(P.ws, 2 * P.dim, static_cast<int>(groups), {{P.dw, P.db, nullptr}, {P.dim, P.dim, 0}}, P.stream);
     return hipGetLastError();

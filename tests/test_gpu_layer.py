@@ -409,7 +409,10 @@ NORM = [  # rows, dim, x, residual or None, weights or None, output
     (3, 8193, "fp32", None, "fp32", "fp32"), (2, 16384, "bf16", "bf16", "bf16", "bf16"), (2500, 64, "bf16", None, "fp32", "fp32"),
     # several rounds of rows for every workgroup, the last one partly filled
     (40011, 24, "fp32", None, "fp32", "fp32"), (5003, 600, "bf16", "fp32", "fp32", "bf16"), (777, 5000, "bf16", None, "fp32", "fp32"),
-    (600, 9000, "fp32", None, "fp32", "fp32"),
+    (600, 9000, "fp32", None, "fp32", "fp32"), (9001, 200, "bf16", "fp32", "bf16", "bf16"), (4501, 509, "fp32", "bf16", "fp32", "fp32"),
+    (2503, 1500, "bf16", None, "fp32", "fp32"), (1101, 4001, "fp32", "bf16", "fp32", "bf16"),
+    # around the smallest row that is read in whole units
+    (37, 8, "bf16", "fp32", "fp32", "fp32"), (37, 9, "fp32", "bf16", "bf16", "fp32"), (20000, 6, "bf16", "fp32", "fp32", "bf16"),
 ]
 # roundings behind a sum over a row: a lane's 64 at most, the lanes' 6 steps and the waves' 16, and a dozen around them
 ROW = 100
