@@ -14,25 +14,21 @@ namespace kda {
 
 namespace {
 
-// A tensor's rows as a workgroup walks them: the address of its first row, which is uniform and moves, and the
-// lane's byte offset from there (its row among the workgroup's and its column), which stays.
+// A lane's row of a tensor: the address of the workgroup's first one, which is uniform, and the byte offset from there.
 struct Walk {
     char *at;
-    int64_t step;   // bytes per row
     uint32_t off;
     int bf16;
-    __device__ __forceinline__ Walk(const Rows &r, int64_t row, int sub, int lane) {
+    __device__ __forceinline__ Walk(const Rows &r, int64_t row, int sub) {
         const int e = r.bf16 ? 2 : 4;
         at = static_cast<char *>(r.p) + row * r.stride * e;
-        step = r.stride * e;
-        off = static_cast<uint32_t>(sub) * static_cast<uint32_t>(step) + static_cast<uint32_t>(lane * 8 * e);
+        off = static_cast<uint32_t>(sub) * static_cast<uint32_t>(r.stride * e);
         bf16 = r.bf16;
     }
-    __device__ __forceinline__ char *unit(int more) const { return at + (off + static_cast<uint32_t>(more) * (bf16 ? 2 : 4)); }
+    __device__ __forceinline__ char *unit(int col) const { return at + (off + static_cast<uint32_t>(col) * (bf16 ? 2 : 4)); }
 };
-// 8 elements, `more` elements behind the lane's first, 16 bytes at a time wherever the row starts (the hardware
-// takes these accesses at any element's alignment); of a row's last unit the `left` elements that it has, singly,
-// and zeros.
+// 8 elements, 16 bytes at a time wherever the row starts (the hardware takes these accesses at any element's
+// alignment); of a row that has only `left` elements these, singly, and zeros.
 typedef uint32_t any4 __attribute__((ext_vector_type(4), aligned(2)));
 __device__ __forceinline__ void load8(const char *p, int bf16, int left, float (&x)[8]) {
     if (left < 8) {
@@ -211,7 +207,9 @@ constexpr int norm_threads() { return WAVES <= 4 ? 256 : 64 * WAVES; }
 template <int LANES, int WAVES>
 constexpr int rows_per_group() { return norm_threads<LANES, WAVES>() / (LANES * WAVES); }
 
-template <int LANES, int WAVES, int U>
+// As the gradients below, a row's last unit is moved back inside the row; TINY rows, of fewer than 8 elements, are read
+// singly.  residual_out is written behind the sums, when every lane of the row has read what it may replace.
+template <int LANES, int WAVES, int U, bool TINY>
 __global__ void __launch_bounds__((norm_threads<LANES, WAVES>())) norm_fwd_kernel(NormFwdLaunch P) {
     constexpr int SPAN = LANES * WAVES, ROWS = rows_per_group<LANES, WAVES>();
     __shared__ float shared[2 * WAVES][4];
@@ -220,39 +218,38 @@ __global__ void __launch_bounds__((norm_threads<LANES, WAVES>())) norm_fwd_kerne
     const int64_t base = static_cast<int64_t>(blockIdx.x) * ROWS;
     const bool live = base + sub < P.rows;
     if (!live) sub = static_cast<int>(P.rows - 1 - base);  // keeps the wave whole for the sums; stores nothing
-    const Walk wx(P.x, base, sub, lane), wr(P.res, base, sub, lane), wo(P.res_out, base, sub, lane), wy(P.y, base, sub, lane);
+    const Walk wx(P.x, base, sub), wr(P.res, base, sub), wo(P.res_out, base, sub), wy(P.y, base, sub);
     const float n = wave_count<LANES, WAVES, U>(lane, P.dim), inv_dim = 1.f / static_cast<float>(P.dim);
     float x[U][8];
+    int col[U], left[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        const int left = P.dim - first_col<SPAN>(lane, u), more = u * SPAN * 8;
-        if (left > 0) {
-            load8(wx.unit(more), P.x.bf16, left, x[u]);
-            if (P.res.p) {
-                float r[8];
-                load8(wr.unit(more), P.res.bf16, left, r);
+        const int c = first_col<SPAN>(lane, u);
+        col[u] = TINY ? 0 : c + 8 > P.dim ? P.dim - 8 : c;
+        left[u] = c >= P.dim ? 0 : TINY ? P.dim : 8;
+        const int all = TINY ? left[u] : 8;
+        load8(wx.unit(col[u]), P.x.bf16, all, x[u]);
+        if (P.res.p) {
+            float r[8];
+            load8(wr.unit(col[u]), P.res.bf16, all, r);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) x[u][i] += r[i];
-                if (live) store8(wo.unit(more), P.res_out.bf16, left, x[u]);
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[u][i] = 0.f;
+            for (int i = 0; i < 8; ++i) x[u][i] += r[i];
         }
     }
-    const RowSums s = row_sums<LANES, WAVES, U, false, false>(x, x, x, lane, P.dim, n > 0.f ? 1.f / n : 0.f, n, inv_dim, P.eps, shared);
+    const RowSums s = row_sums<LANES, WAVES, U, false, !TINY>(x, x, x, lane, P.dim, n > 0.f ? 1.f / n : 0.f, n, inv_dim, P.eps, shared);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        const int col = first_col<SPAN>(lane, u), left = P.dim - col;
-        if (left <= 0 || !live) continue;
+        if (left[u] == 0 || !live) continue;
+        const int all = TINY ? left[u] : 8;
+        if (P.res_out.p) store8(wo.unit(col[u]), P.res_out.bf16, all, x[u]);
         float w[8], b[8] = {};
 #pragma unroll
         for (int i = 0; i < 8; ++i) w[i] = 1.f;
-        if (P.w) load_param(P.w, P.w_bf16, col, left, w);
-        if (P.b) load_param(P.b, P.w_bf16, col, left, b);
+        if (P.w) load_param(P.w, P.w_bf16, col[u], all, w);
+        if (P.b) load_param(P.b, P.w_bf16, col[u], all, b);
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[u][i] = fmaf((x[u][i] - s.mean) * s.rstd, w[i], b[i]);
-        store8(wy.unit(u * SPAN * 8), P.y.bf16, left, x[u]);
+        store8(wy.unit(col[u]), P.y.bf16, all, x[u]);
     }
 }
 
@@ -447,20 +444,24 @@ void launch_column_sum(const float *in, int64_t ld, int parts, const ColumnSums 
     if (cols > 0) column_sum_kernel<<<static_cast<unsigned>((cols + 15) / 16), 1024, 0, stream>>>(in, ld, parts, to);
 }
 
+template <int LANES, int WAVES, int U, bool TINY = false>
+static void launch_fwd(const NormFwdLaunch &P) {
+    constexpr int ROWS = rows_per_group<LANES, WAVES>();
+    norm_fwd_kernel<LANES, WAVES, U, TINY>
+        <<<static_cast<unsigned>((P.rows + ROWS - 1) / ROWS), norm_threads<LANES, WAVES>(), 0, P.stream>>>(P);
+}
+
 // The smallest arrangement that holds a row: 16 lanes (to 128 elements), 32, a wave (to 1,024), then several.
 hipError_t launch_norm_fwd(const NormFwdLaunch &P) {
-#define KDA_NORM_FWD(L, W, U)                                                                                    \
-    norm_fwd_kernel<L, W, U><<<static_cast<unsigned>((P.rows + rows_per_group<L, W>() - 1) / rows_per_group<L, W>()), \
-                               norm_threads<L, W>(), 0, P.stream>>>(P)
-    if (P.dim <= 128) KDA_NORM_FWD(16, 1, 1);
-    else if (P.dim <= 256) KDA_NORM_FWD(32, 1, 1);
-    else if (P.dim <= 512) KDA_NORM_FWD(64, 1, 1);
-    else if (P.dim <= 1024) KDA_NORM_FWD(64, 1, 2);
-    else if (P.dim <= 2048) KDA_NORM_FWD(64, 4, 1);
-    else if (P.dim <= 4096) KDA_NORM_FWD(64, 4, 2);
-    else if (P.dim <= 8192) KDA_NORM_FWD(64, 8, 2);
-    else KDA_NORM_FWD(64, 16, 2);
-#undef KDA_NORM_FWD
+    if (P.dim < 8) launch_fwd<16, 1, 1, true>(P);
+    else if (P.dim <= 128) launch_fwd<16, 1, 1>(P);
+    else if (P.dim <= 256) launch_fwd<32, 1, 1>(P);
+    else if (P.dim <= 512) launch_fwd<64, 1, 1>(P);
+    else if (P.dim <= 1024) launch_fwd<64, 1, 2>(P);
+    else if (P.dim <= 2048) launch_fwd<64, 4, 1>(P);
+    else if (P.dim <= 4096) launch_fwd<64, 4, 2>(P);
+    else if (P.dim <= 8192) launch_fwd<64, 8, 2>(P);
+    else launch_fwd<64, 16, 2>(P);
     return hipGetLastError();
 }
 

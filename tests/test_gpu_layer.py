@@ -497,6 +497,20 @@ def test_norm_of_heads_and_far_means(kda):
     assert s1 is c and torch.equal(y, y1) and torch.equal(s, c)
 
 
+@pytest.mark.parametrize("rows,dim", [(33, 5), (33, 13), (7, 700), (5, 5001), (3, 9003)])
+def test_norm_residual_in_place(kda, rows, dim):
+    """The sums take every lane's inputs before one of them is replaced, also where units of a row overlap."""
+    import torch
+    g = torch.Generator("cuda").manual_seed(dim)
+    x, res = (torch.randn(rows, dim, generator=g, device="cuda") for _ in range(2))
+    y, s = kda.layer_norm_fwd(x, residual=res)
+    assert torch.equal(s, x + res)
+    for _ in range(3):
+        held = res.clone()
+        z, out = kda.layer_norm_fwd(x, residual=held, residual_out=held)
+        assert out is held and torch.equal(held, s) and torch.equal(z, y)
+
+
 def test_no_rows(kda):
     """No tokens: states pass through, parameter gradients are zero, nothing else is written."""
     import torch
