@@ -29,10 +29,6 @@ struct Rows {
         else static_cast<float *>(p)[i] = x;
     }
 };
-// A parameter vector in bf16 or fp32.
-__device__ __forceinline__ float param(const void *p, int bf16, int64_t i) {
-    return bf16 ? bf16_to_f32(static_cast<const uint16_t *>(p)[i]) : static_cast<const float *>(p)[i];
-}
 
 // Sequences cut into tiles of L tokens.  A launch has one slot per possible tile: sequence n's tiles take
 // the slots from (start_n / L + n) on.  As ceil(len / L) <= (start + len) / L - start / L + 1 these ranges

@@ -36,25 +36,27 @@ __device__ __forceinline__ void bounds_of(const int32_t *cu, int N, int T, int n
 // some of its neighbour's again and stores the same values.
 typedef uint32_t any4 __attribute__((ext_vector_type(4), aligned(2)));
 template <int V, bool InBf16>
-__device__ __forceinline__ void load_v(const void *p, int64_t at, float *x) {
-    using E = typename Elem<InBf16>::T;
-    const E *e = static_cast<const E *>(p) + at;
-    if constexpr (V == 1) {
-        x[0] = Elem<InBf16>::load(e, 0);
-    } else {
-        constexpr int words = V * static_cast<int>(sizeof(E)) / 4;
-        typedef uint32_t some __attribute__((ext_vector_type(words), aligned(2)));
-        const some v = *reinterpret_cast<const some *>(e);
-#pragma unroll
-        for (int i = 0; i < words; ++i) {
-            if constexpr (InBf16) {
-                x[2 * i] = __uint_as_float(v[i] << 16);
-                x[2 * i + 1] = __uint_as_float(v[i] & 0xffff0000u);
-            } else {
-                x[i] = __uint_as_float(v[i]);
-            }
-        }
+struct Raw {
+    static constexpr int kWords = V == 1 ? 1 : V * (InBf16 ? 2 : 4) / 4;
+    typedef uint32_t some __attribute__((ext_vector_type(kWords), aligned(2)));
+    some v;
+    __device__ __forceinline__ void load(const void *p, int64_t at) {
+        const typename Elem<InBf16>::T *e = static_cast<const typename Elem<InBf16>::T *>(p) + at;
+        if constexpr (V == 1) v[0] = InBf16 ? *reinterpret_cast<const uint16_t *>(e) : *reinterpret_cast<const uint32_t *>(e);
+        else v = *reinterpret_cast<const some *>(e);
     }
+    __device__ __forceinline__ void widen(float *x) const {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if constexpr (!InBf16) x[i] = __uint_as_float(v[i]);
+            else x[i] = __uint_as_float(V > 1 && (i & 1) ? v[i / 2] & 0xffff0000u : v[i / 2] << 16);
+    }
+};
+template <int V, bool InBf16>
+__device__ __forceinline__ void load_v(const void *p, int64_t at, float *x) {
+    Raw<V, InBf16> r;
+    r.load(p, at);
+    r.widen(x);
 }
 template <int V>
 __device__ __forceinline__ void store_v(const Rows &r, int64_t row, int col, const float *x) {
@@ -317,9 +319,24 @@ __global__ void __launch_bounds__(256) conv_grad_kernel(ConvBwdLaunch P, int64_t
             gradient(x[0], g[0], true);
             shift<W, V>(gp, g[0]);
         }
-        for (; i + kGradAhead <= stop; i += kGradAhead) {  // nothing to ask here
+        // nothing to ask here; the next rows' loads are in flight behind a pair's work
+        Raw<V, InBf16> nx[kGradAhead], ng[kGradAhead];
+        auto ahead = [&](int64_t i) {
 #pragma unroll
-            for (int a = 0; a < kGradAhead; ++a) load(i + a, x[a], g[a]);
+            for (int a = 0; a < kGradAhead; ++a) {
+                const int64_t row = i + a < stop ? i + a : stop - 1;
+                nx[a].load(P.x.p, row * P.x.stride + c0);
+                ng[a].load(P.gy.p, row * P.gy.stride + c0);
+            }
+        };
+        ahead(i);
+        for (; i + kGradAhead <= stop; i += kGradAhead) {
+#pragma unroll
+            for (int a = 0; a < kGradAhead; ++a) {
+                nx[a].widen(x[a]);
+                ng[a].widen(g[a]);
+            }
+            ahead(i + kGradAhead);
 #pragma unroll
             for (int a = 0; a < kGradAhead; ++a) {
                 gradient(x[a], g[a], true);
