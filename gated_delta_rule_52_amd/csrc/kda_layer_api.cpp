@@ -98,7 +98,7 @@ kda_status check_batch(const A *a) {
 }
 // Threads of one launch stay below 2^32.
 kda_status check_grid(int64_t threads) {
-    if (threads >= (int64_t{1} << 32)) return fail(KDA_ERR_UNSUPPORTED, "problem too large for one launch");
+    if (threads < 0 || threads >= (int64_t{1} << 32)) return fail(KDA_ERR_UNSUPPORTED, "problem too large for one launch");
     return KDA_OK;
 }
 

@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(256) scan_combine_kernel(ScanFwdLaunch P) {
     int64_t start;
     int len;
     P.seq.sequence(n, start, len);
-    const int count = (len + P.seq.L - 1) / P.seq.L;
+    const int count = P.seq.tiles(len);
     if (e >= states || count <= 1) return;
     const FwdSpace W = fwd_space(P.ws, P.seq, P.dim, P.ds);
     const int64_t first = P.seq.first_slot(n, start);

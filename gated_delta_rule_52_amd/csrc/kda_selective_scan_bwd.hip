@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(256) scan_bwd_combine_kernel(ScanBwdLaunch P, 
     int64_t start;
     int len;
     P.seq.sequence(n, start, len);
-    const int count = (len + P.seq.L - 1) / P.seq.L;
+    const int count = P.seq.tiles(len);
     if (e >= states || count <= 1) return;
     const int64_t first = P.seq.first_slot(n, start);
     const float A2 = kLog2e * P.A[e];
