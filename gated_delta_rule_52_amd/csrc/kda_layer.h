@@ -164,6 +164,7 @@ struct ScanBwdLaunch {
 SeqTiles scan_bwd_tiles(const int32_t *cu, int N, int T, int dim, int ds);
 size_t scan_bwd_workspace_bytes(const SeqTiles &seq, int dim, int ds);
 hipError_t launch_scan_bwd(const ScanBwdLaunch &P);
+int64_t scan_bwd_threads(const SeqTiles &seq, int dim, int ds);
 
 struct ConvLaunch {
     Rows x, y;
@@ -177,6 +178,7 @@ struct ConvLaunch {
     hipStream_t stream;
 };
 hipError_t launch_conv_fwd(const ConvLaunch &P);
+int64_t conv_fwd_threads(int64_t rows, int dim);  // of its largest launch over the rows
 hipError_t launch_conv_step(const ConvLaunch &P);
 
 struct ConvBwdLaunch {
@@ -194,6 +196,7 @@ struct ConvBwdLaunch {
 };
 size_t conv_bwd_workspace_bytes(int64_t rows, int dim, int width, bool bf16);
 hipError_t launch_conv_bwd(const ConvBwdLaunch &P);
+int64_t conv_bwd_threads(int64_t rows, int dim, bool bf16);
 
 struct NormFwdLaunch {
     Rows x, res, y, res_out;
@@ -205,6 +208,7 @@ struct NormFwdLaunch {
     hipStream_t stream;
 };
 hipError_t launch_norm_fwd(const NormFwdLaunch &P);
+int64_t norm_fwd_threads(int64_t rows, int dim);
 
 struct NormBwdLaunch {
     Rows x, gy, gres, dx;
@@ -226,6 +230,7 @@ struct ColumnSums {
     float *out[3];
     int64_t cols[3];
 };
+int64_t column_sum_threads(int64_t cols);
 void launch_column_sum(const float *in, int64_t ld, int parts, const ColumnSums &to, hipStream_t stream);
 
 }  // namespace kda

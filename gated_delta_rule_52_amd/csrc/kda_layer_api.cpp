@@ -177,8 +177,7 @@ kda_status check_scan_bwd_sizes(const kda_selective_scan_bwd_args *a) {
         return fail(KDA_ERR_UNSUPPORTED, "in_dtype=%d grad_dtype=%d", a->in_dtype, a->grad_dtype);
     if (a->flags & ~KDA_SCAN_DT_SOFTPLUS) return fail(KDA_ERR_UNSUPPORTED, "unknown flags 0x%x", a->flags);
     const kda::SeqTiles s = kda::scan_bwd_tiles(a->cu_seqlens, a->num_seqs, a->T, a->dim, a->ds);
-    KDA_TRY(check_grid(s.slots() * ((a->dim + 63) / 64) * 256));
-    return check_grid(s.rows() * 2 * a->ds);
+    return check_grid(kda::scan_bwd_threads(s, a->dim, a->ds));
 }
 
 // ---- short convolution ---------------------------------------------------------------------------------
@@ -191,15 +190,14 @@ kda_status check_conv_sizes(const A *a) {
     if (!valid_dtype(a->in_dtype) || !valid_dtype(a->w_dtype))
         return fail(KDA_ERR_UNSUPPORTED, "in_dtype=%d w_dtype=%d", a->in_dtype, a->w_dtype);
     if (a->flags & ~KDA_CONV_SILU) return fail(KDA_ERR_UNSUPPORTED, "unknown flags 0x%x", a->flags);
-    const int64_t rows = static_cast<int64_t>(a->batch) * a->T, cb = (a->dim + 255) / 256;  // at least any launch's
-    KDA_TRY(check_grid((rows + 7) / 8 * cb * 256));
-    return check_grid(static_cast<int64_t>(a->num_seqs) * cb * 256);
+    return check_grid(static_cast<int64_t>(a->num_seqs) * ((a->dim + 255) / 256) * 256);  // the states', at least the step's
 }
 
 kda_status check_conv(const kda_short_conv_args *a) {
     KDA_TRY(check_conv_sizes(a));
     if (!valid_dtype(a->out_dtype)) return fail(KDA_ERR_UNSUPPORTED, "out_dtype=%d", a->out_dtype);
     const int64_t rows = static_cast<int64_t>(a->batch) * a->T;
+    KDA_TRY(check_grid(kda::conv_fwd_threads(rows, a->dim)));
     if (rows > 0 && (!a->x || !a->y)) return fail(KDA_ERR_NULL_POINTER, "x and y are required");
     if (!a->weight) return fail(KDA_ERR_NULL_POINTER, "weight is required");
     KDA_TRY(check_stride("x", a->x, a->x_stride, a->dim, rows));
@@ -214,6 +212,11 @@ kda_status check_conv(const kda_short_conv_args *a) {
     const Span outs[] = {strided("y", a->y, rows, a->dim, a->y_stride, a->out_dtype),
                          flat("final_state", a->final_state, state)};
     return check_overlaps(ins, outs);
+}
+
+kda_status check_conv_bwd_sizes(const kda_short_conv_bwd_args *a) {
+    KDA_TRY(check_conv_sizes(a));
+    return check_grid(kda::conv_bwd_threads(static_cast<int64_t>(a->batch) * a->T, a->dim, a->in_dtype == KDA_DTYPE_BF16));
 }
 
 kda::ConvLaunch conv_launch(const kda_short_conv_args *a) {
@@ -365,13 +368,13 @@ kda_status kda_short_conv_step(const kda_short_conv_args *a) {
 }
 
 size_t kda_short_conv_bwd_workspace_bytes(const kda_short_conv_bwd_args *a) {
-    if (check_conv_sizes(a) != KDA_OK) return static_cast<size_t>(-1);
+    if (check_conv_bwd_sizes(a) != KDA_OK) return static_cast<size_t>(-1);
     return kda::conv_bwd_workspace_bytes(static_cast<int64_t>(a->batch) * a->T, a->dim, a->width, a->in_dtype == KDA_DTYPE_BF16);
 }
 
 kda_status kda_short_conv_bwd(const kda_short_conv_bwd_args *a) {
     kda::set_last_error("");
-    KDA_TRY(check_conv_sizes(a));
+    KDA_TRY(check_conv_bwd_sizes(a));
     if (!valid_dtype(a->grad_dtype)) return fail(KDA_ERR_UNSUPPORTED, "grad_dtype=%d", a->grad_dtype);
     const int64_t rows = static_cast<int64_t>(a->batch) * a->T;
     if (rows > 0 && (!a->x || !a->grad_y || !a->grad_x)) return fail(KDA_ERR_NULL_POINTER, "x, grad_y and grad_x are required");
@@ -427,7 +430,7 @@ kda_status kda_layer_norm_fwd(const kda_layer_norm_args *a) {
     KDA_TRY(check_stride("y", a->y, a->y_stride, a->dim, a->rows));
     KDA_TRY(check_stride("residual", a->residual, a->residual_stride, a->dim, a->rows));
     KDA_TRY(check_stride("residual_out", a->residual_out, a->residual_out_stride, a->dim, a->rows));
-    KDA_TRY(check_grid(a->rows * (a->dim <= 1024 ? 64 : a->dim <= 4096 ? 256 : 1024)));
+    KDA_TRY(check_grid(kda::norm_fwd_threads(a->rows, a->dim)));
     const int64_t param = a->dim * dsize(a->w_dtype);
     const bool in_place = a->residual == a->residual_out && a->residual_stride == a->residual_out_stride;
     const Span ins[] = {strided("x", a->x, a->rows, a->dim, a->x_stride, a->x_dtype),

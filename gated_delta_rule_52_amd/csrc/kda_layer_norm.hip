@@ -459,6 +459,7 @@ void launch_column_sum(const float *in, int64_t ld, int parts, const ColumnSums 
     const int64_t cols = to.cols[0] + to.cols[1] + to.cols[2];
     if (cols > 0) column_sum_kernel<<<static_cast<unsigned>((cols + 15) / 16), 1024, 0, stream>>>(in, ld, parts, to);
 }
+int64_t column_sum_threads(int64_t cols) { return (cols + 15) / 16 * 1024; }
 
 template <int LANES, int WAVES, int U, bool TINY = false>
 static void launch_fwd(const NormFwdLaunch &P) {
@@ -479,6 +480,11 @@ hipError_t launch_norm_fwd(const NormFwdLaunch &P) {
     else if (P.dim <= 8192) launch_fwd<64, 8, 2>(P);
     else launch_fwd<64, 16, 2>(P);
     return hipGetLastError();
+}
+int64_t norm_fwd_threads(int64_t rows, int dim) {
+    const int lanes = dim <= 128 ? 16 : dim <= 256 ? 32 : dim <= 1024 ? 64 : dim <= 4096 ? 256 : dim <= 8192 ? 512 : 1024;
+    const int group = lanes < 256 ? 256 : lanes;
+    return (rows + group / lanes - 1) / (group / lanes) * group;
 }
 
 size_t norm_bwd_workspace_bytes(int64_t rows, int dim) {

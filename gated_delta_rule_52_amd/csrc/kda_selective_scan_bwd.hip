@@ -531,6 +531,12 @@ SeqTiles scan_bwd_tiles(const int32_t *cu, int N, int T, int dim, int ds) {
     return s;
 }
 
+int64_t scan_bwd_threads(const SeqTiles &seq, int dim, int ds) {
+    const int64_t walks = seq.slots() * ((dim + 63) / 64) * 256, sums = (seq.rows() * 2 * ds + 255) / 256 * 256;
+    const int64_t params = column_sum_threads(static_cast<int64_t>(dim) * (ds + 2));
+    return walks > sums ? walks > params ? walks : params : sums > params ? sums : params;
+}
+
 size_t scan_bwd_workspace_bytes(const SeqTiles &seq, int dim, int ds) { return space(nullptr, seq, dim, ds).bytes; }
 
 hipError_t launch_scan_bwd(const ScanBwdLaunch &P) {

@@ -467,12 +467,22 @@ int64_t conv_rows(const int32_t *cu, int N, int T) { return cu ? T : static_cast
 
 }  // namespace
 
+// How the forward kernel cuts its rows.
+struct ConvFwdCut {
+    int V, tile, cb;
+    int64_t grid;
+};
+static ConvFwdCut conv_fwd_cut(int64_t rows, int dim) {
+    const int V = vector_of(dim, 4), cb = (dim + 64 * V - 1) / (64 * V), tile = tile_of(rows, dim, V, 64, 16);
+    return {V, tile, cb, (rows + tile * kWaves - 1) / (tile * kWaves) * cb};
+}
+int64_t conv_fwd_threads(int64_t rows, int dim) { return conv_fwd_cut(rows, dim).grid * 256; }
+
 hipError_t launch_conv_fwd(const ConvLaunch &P) {
     const int64_t rows = conv_rows(P.cu, P.N, P.T);
-    const int V = vector_of(P.dim, 4), cb = (P.dim + 64 * V - 1) / (64 * V);
-    const int tile = tile_of(rows, P.dim, V, 64, 16);
-    const unsigned grid = static_cast<unsigned>((rows + tile * kWaves - 1) / (tile * kWaves) * cb);
-    if (rows > 0) KDA_CONV_PICK(conv_kernel, 4, 4, grid, P, rows, cb, tile);
+    const ConvFwdCut cut = conv_fwd_cut(rows, P.dim);
+    const int V = cut.V;
+    if (rows > 0) KDA_CONV_PICK(conv_kernel, 4, 4, static_cast<unsigned>(cut.grid), P, rows, cut.cb, cut.tile);
     if (P.hT) {
         if (P.x.bf16) launch_state<uint16_t>(P);
         else launch_state<float>(P);
@@ -491,12 +501,17 @@ hipError_t launch_conv_step(const ConvLaunch &P) {
 
 // How the gradient kernel cuts its rows: 64 to a thread for bf16, 8 channels wide, 16,384 x 4,096 112 us (32: 131).
 struct ConvCut {
-    int V, tile;
-    int64_t parts;  // workgroups along the rows
+    int V, tile, cb;  // cb: workgroups across the channels
+    int64_t parts;    // and along the rows
 };
 static ConvCut conv_cut(int64_t rows, int dim, bool bf16) {
     const int V = vector_of(dim, bf16 ? 8 : 4), tile = tile_of(rows, dim, V, 256 / kGradSubs, 64);
-    return {V, tile, (rows + tile * kGradSubs - 1) / (tile * kGradSubs)};
+    const int cb = (dim + 256 / kGradSubs * V - 1) / (256 / kGradSubs * V);
+    return {V, tile, cb, (rows + tile * kGradSubs - 1) / (tile * kGradSubs)};
+}
+int64_t conv_bwd_threads(int64_t rows, int dim, bool bf16) {
+    const ConvCut cut = conv_cut(rows, dim, bf16);
+    return cut.parts * cut.cb * 256;
 }
 
 size_t conv_bwd_workspace_bytes(int64_t rows, int dim, int width, bool bf16) {
@@ -506,9 +521,9 @@ size_t conv_bwd_workspace_bytes(int64_t rows, int dim, int width, bool bf16) {
 hipError_t launch_conv_bwd(const ConvBwdLaunch &P) {
     const int64_t rows = conv_rows(P.cu, P.N, P.T);
     const ConvCut cut = conv_cut(rows, P.dim, P.x.bf16);
-    const int V = cut.V, cb = (P.dim + 256 / kGradSubs * V - 1) / (256 / kGradSubs * V);
+    const int V = cut.V;
     if (rows > 0)
-        KDA_CONV_PICK(conv_grad_kernel, 8, 4, static_cast<unsigned>(cut.parts * cb), P, rows, cb, cut.tile);
+        KDA_CONV_PICK(conv_grad_kernel, 8, 4, static_cast<unsigned>(cut.parts * cut.cb), P, rows, cut.cb, cut.tile);
     const int64_t ld = static_cast<int64_t>(P.width + 1) * P.dim;
     launch_column_sum(P.ws, ld, static_cast<int>(cut.parts), {{P.dw, P.db, nullptr}, {static_cast<int64_t>(P.width) * P.dim, P.dim, 0}},
                       P.stream);
