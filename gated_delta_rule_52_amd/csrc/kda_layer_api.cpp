@@ -64,8 +64,13 @@ kda_status check_overlaps(const Span (&ins)[NI], const Span (&outs)[NO]) {
     return KDA_OK;
 }
 
-kda_status check_stride(const char *name, const void *p, int64_t stride, int64_t width, int64_t rows) {
-    if (p && (stride < width || stride >= (int64_t{1} << 22) || stride > (int64_t{1} << 40) / (rows > 0 ? rows : 1)))
+// Row strides below which an operator's address arithmetic holds; the others form every row's address in 64 bits.
+constexpr int64_t kAnyStride = int64_t{1} << 40;
+constexpr int64_t kScanStride = int64_t{1} << 22;  // the walk over tokens: a row's bytes in a 24-bit multiply
+constexpr int64_t kNormStride = int64_t{1} << 26;  // rows that share a workgroup, up to 16: 32-bit distances within it
+
+kda_status check_stride(const char *name, const void *p, int64_t stride, int64_t width, int64_t rows, int64_t below) {
+    if (p && (stride < width || stride >= below || stride > (int64_t{1} << 40) / (rows > 0 ? rows : 1)))
         return fail(KDA_ERR_BAD_SHAPE, "%s: stride %lld for rows of %lld", name, static_cast<long long>(stride),
                     static_cast<long long>(width));
     return KDA_OK;
@@ -123,18 +128,25 @@ kda_status check_scan_sizes(const kda_selective_scan_args *a) {
     return check_grid(s.slots() * ((a->dim + 63) / 64) * 256);
 }
 
+// One token per sequence is the first row of a tile of its own, at no distance from it.
+template <class A>
+int64_t scan_stride(const A *a) {
+    return a->cu_seqlens || a->T > 1 ? kScanStride : kAnyStride;
+}
+
 kda_status check_scan(const kda_selective_scan_args *a) {
     KDA_TRY(check_scan_sizes(a));
     const int64_t rows = static_cast<int64_t>(a->batch) * a->T;
     if (rows > 0 && (!a->u || !a->dt || !a->B || !a->C || !a->y))
         return fail(KDA_ERR_NULL_POINTER, "u, dt, B, C and y are required");
     if (!a->A) return fail(KDA_ERR_NULL_POINTER, "A is required");
-    KDA_TRY(check_stride("u", a->u, a->u_stride, a->dim, rows));
-    KDA_TRY(check_stride("dt", a->dt, a->dt_stride, a->dim, rows));
-    KDA_TRY(check_stride("B", a->B, a->B_stride, a->ds, rows));
-    KDA_TRY(check_stride("C", a->C, a->C_stride, a->ds, rows));
-    KDA_TRY(check_stride("z", a->z, a->z_stride, a->dim, rows));
-    KDA_TRY(check_stride("y", a->y, a->y_stride, a->dim, rows));
+    const int64_t below = scan_stride(a);
+    KDA_TRY(check_stride("u", a->u, a->u_stride, a->dim, rows, below));
+    KDA_TRY(check_stride("dt", a->dt, a->dt_stride, a->dim, rows, below));
+    KDA_TRY(check_stride("B", a->B, a->B_stride, a->ds, rows, below));
+    KDA_TRY(check_stride("C", a->C, a->C_stride, a->ds, rows, below));
+    KDA_TRY(check_stride("z", a->z, a->z_stride, a->dim, rows, below));
+    KDA_TRY(check_stride("y", a->y, a->y_stride, a->dim, rows, below));
     const int64_t state = static_cast<int64_t>(a->num_seqs) * a->dim * a->ds * 4, param = static_cast<int64_t>(a->dim) * 4;
     const bool in_place = a->initial_state == a->final_state;
     const Span ins[] = {strided("u", a->u, rows, a->dim, a->u_stride, a->in_dtype),
@@ -200,8 +212,8 @@ kda_status check_conv(const kda_short_conv_args *a) {
     KDA_TRY(check_grid(kda::conv_fwd_threads(rows, a->dim)));
     if (rows > 0 && (!a->x || !a->y)) return fail(KDA_ERR_NULL_POINTER, "x and y are required");
     if (!a->weight) return fail(KDA_ERR_NULL_POINTER, "weight is required");
-    KDA_TRY(check_stride("x", a->x, a->x_stride, a->dim, rows));
-    KDA_TRY(check_stride("y", a->y, a->y_stride, a->dim, rows));
+    KDA_TRY(check_stride("x", a->x, a->x_stride, a->dim, rows, kAnyStride));
+    KDA_TRY(check_stride("y", a->y, a->y_stride, a->dim, rows, kAnyStride));
     const int64_t state = static_cast<int64_t>(a->num_seqs) * (a->width - 1) * a->dim * dsize(a->in_dtype);
     const int64_t param = a->dim * dsize(a->w_dtype);
     const bool in_place = a->initial_state == a->final_state;
@@ -233,6 +245,9 @@ kda::ConvLaunch conv_launch(const kda_short_conv_args *a) {
 }
 
 // ---- layer norm ----------------------------------------------------------------------------------------
+
+// Up to 2048 elements several rows share a workgroup.
+int64_t norm_stride(int32_t dim) { return dim > 2048 ? kAnyStride : kNormStride; }
 
 kda_status check_norm_sizes(int64_t rows, int32_t dim, float eps) {
     if (rows < 0 || dim < 1) return fail(KDA_ERR_BAD_SHAPE, "rows=%lld dim=%d", static_cast<long long>(rows), dim);
@@ -288,17 +303,18 @@ kda_status kda_selective_scan_bwd(const kda_selective_scan_bwd_args *a) {
         return fail(KDA_ERR_NULL_POINTER, "grad_z is given exactly where z is");
     if (a->grad_dt_bias && !a->dt_bias) return fail(KDA_ERR_NULL_POINTER, "grad_dt_bias without dt_bias");
     if (a->grad_D && !a->D) return fail(KDA_ERR_NULL_POINTER, "grad_D without D");
-    KDA_TRY(check_stride("u", a->u, a->u_stride, a->dim, rows));
-    KDA_TRY(check_stride("dt", a->dt, a->dt_stride, a->dim, rows));
-    KDA_TRY(check_stride("B", a->B, a->B_stride, a->ds, rows));
-    KDA_TRY(check_stride("C", a->C, a->C_stride, a->ds, rows));
-    KDA_TRY(check_stride("z", a->z, a->z_stride, a->dim, rows));
-    KDA_TRY(check_stride("grad_y", a->grad_y, a->grad_y_stride, a->dim, rows));
-    KDA_TRY(check_stride("grad_u", a->grad_u, a->grad_u_stride, a->dim, rows));
-    KDA_TRY(check_stride("grad_dt", a->grad_dt, a->grad_dt_stride, a->dim, rows));
-    KDA_TRY(check_stride("grad_B", a->grad_B, a->grad_B_stride, a->ds, rows));
-    KDA_TRY(check_stride("grad_C", a->grad_C, a->grad_C_stride, a->ds, rows));
-    KDA_TRY(check_stride("grad_z", a->grad_z, a->grad_z_stride, a->dim, rows));
+    const int64_t below = scan_stride(a);
+    KDA_TRY(check_stride("u", a->u, a->u_stride, a->dim, rows, below));
+    KDA_TRY(check_stride("dt", a->dt, a->dt_stride, a->dim, rows, below));
+    KDA_TRY(check_stride("B", a->B, a->B_stride, a->ds, rows, below));
+    KDA_TRY(check_stride("C", a->C, a->C_stride, a->ds, rows, below));
+    KDA_TRY(check_stride("z", a->z, a->z_stride, a->dim, rows, below));
+    KDA_TRY(check_stride("grad_y", a->grad_y, a->grad_y_stride, a->dim, rows, below));
+    KDA_TRY(check_stride("grad_u", a->grad_u, a->grad_u_stride, a->dim, rows, below));
+    KDA_TRY(check_stride("grad_dt", a->grad_dt, a->grad_dt_stride, a->dim, rows, below));
+    KDA_TRY(check_stride("grad_B", a->grad_B, a->grad_B_stride, a->ds, rows, below));
+    KDA_TRY(check_stride("grad_C", a->grad_C, a->grad_C_stride, a->ds, rows, below));
+    KDA_TRY(check_stride("grad_z", a->grad_z, a->grad_z_stride, a->dim, rows, below));
     const kda::SeqTiles seq = kda::scan_bwd_tiles(a->cu_seqlens, a->num_seqs, a->T, a->dim, a->ds);
     const size_t need = kda::scan_bwd_workspace_bytes(seq, a->dim, a->ds);
     if (a->workspace_bytes < need || (need > 0 && !a->workspace))
@@ -379,9 +395,9 @@ kda_status kda_short_conv_bwd(const kda_short_conv_bwd_args *a) {
     const int64_t rows = static_cast<int64_t>(a->batch) * a->T;
     if (rows > 0 && (!a->x || !a->grad_y || !a->grad_x)) return fail(KDA_ERR_NULL_POINTER, "x, grad_y and grad_x are required");
     if (!a->weight || !a->grad_weight) return fail(KDA_ERR_NULL_POINTER, "weight and grad_weight are required");
-    KDA_TRY(check_stride("x", a->x, a->x_stride, a->dim, rows));
-    KDA_TRY(check_stride("grad_y", a->grad_y, a->grad_y_stride, a->dim, rows));
-    KDA_TRY(check_stride("grad_x", a->grad_x, a->grad_x_stride, a->dim, rows));
+    KDA_TRY(check_stride("x", a->x, a->x_stride, a->dim, rows, kAnyStride));
+    KDA_TRY(check_stride("grad_y", a->grad_y, a->grad_y_stride, a->dim, rows, kAnyStride));
+    KDA_TRY(check_stride("grad_x", a->grad_x, a->grad_x_stride, a->dim, rows, kAnyStride));
     const size_t need = kda::conv_bwd_workspace_bytes(rows, a->dim, a->width, a->in_dtype == KDA_DTYPE_BF16);
     if (a->workspace_bytes < need || (need > 0 && !a->workspace))
         return fail(KDA_ERR_WORKSPACE_TOO_SMALL, "workspace %zu < %zu bytes", a->workspace_bytes, need);
@@ -426,10 +442,11 @@ kda_status kda_layer_norm_fwd(const kda_layer_norm_args *a) {
     if (!a->x || !a->y) return fail(KDA_ERR_NULL_POINTER, "x and y are required");
     if ((a->residual == nullptr) != (a->residual_out == nullptr))
         return fail(KDA_ERR_NULL_POINTER, "residual and residual_out come together");
-    KDA_TRY(check_stride("x", a->x, a->x_stride, a->dim, a->rows));
-    KDA_TRY(check_stride("y", a->y, a->y_stride, a->dim, a->rows));
-    KDA_TRY(check_stride("residual", a->residual, a->residual_stride, a->dim, a->rows));
-    KDA_TRY(check_stride("residual_out", a->residual_out, a->residual_out_stride, a->dim, a->rows));
+    const int64_t below = norm_stride(a->dim);
+    KDA_TRY(check_stride("x", a->x, a->x_stride, a->dim, a->rows, below));
+    KDA_TRY(check_stride("y", a->y, a->y_stride, a->dim, a->rows, below));
+    KDA_TRY(check_stride("residual", a->residual, a->residual_stride, a->dim, a->rows, below));
+    KDA_TRY(check_stride("residual_out", a->residual_out, a->residual_out_stride, a->dim, a->rows, below));
     KDA_TRY(check_grid(kda::norm_fwd_threads(a->rows, a->dim)));
     const int64_t param = a->dim * dsize(a->w_dtype);
     const bool in_place = a->residual == a->residual_out && a->residual_stride == a->residual_out_stride;
@@ -466,10 +483,11 @@ kda_status kda_layer_norm_bwd(const kda_layer_norm_bwd_args *a) {
                     a->gy_dtype, a->res_dtype, a->w_dtype, a->grad_dtype);
     if (a->rows > 0 && (!a->x || !a->grad_y || !a->grad_x))
         return fail(KDA_ERR_NULL_POINTER, "x, grad_y and grad_x are required");
-    KDA_TRY(check_stride("x", a->x, a->x_stride, a->dim, a->rows));
-    KDA_TRY(check_stride("grad_y", a->grad_y, a->grad_y_stride, a->dim, a->rows));
-    KDA_TRY(check_stride("grad_residual", a->grad_residual, a->grad_residual_stride, a->dim, a->rows));
-    KDA_TRY(check_stride("grad_x", a->grad_x, a->grad_x_stride, a->dim, a->rows));
+    const int64_t below = norm_stride(a->dim);
+    KDA_TRY(check_stride("x", a->x, a->x_stride, a->dim, a->rows, below));
+    KDA_TRY(check_stride("grad_y", a->grad_y, a->grad_y_stride, a->dim, a->rows, below));
+    KDA_TRY(check_stride("grad_residual", a->grad_residual, a->grad_residual_stride, a->dim, a->rows, below));
+    KDA_TRY(check_stride("grad_x", a->grad_x, a->grad_x_stride, a->dim, a->rows, below));
     const size_t need = kda_layer_norm_bwd_workspace_bytes(a);
     if (a->workspace_bytes < need || (need > 0 && !a->workspace))
         return fail(KDA_ERR_WORKSPACE_TOO_SMALL, "workspace %zu < %zu bytes", a->workspace_bytes, need);

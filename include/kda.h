@@ -463,10 +463,13 @@ size_t kda_chunk_fwd_noalloc_max_workspace_bytes(void);
  * additions:
  *  - Token tensors have a row stride: `x_stride` is the distance in elements
  *    between consecutive tokens (rows) of `x`, at least its width, so that
- *    slices of a wider projection need no copy, and below 2^22.  Token t of sequence b of a
- *    fixed-length batch is row b * T + t.  Token tensors need only their
- *    elements' alignment; 16-byte aligned bases and strides run faster.
- *    Parameters and states are contiguous.
+ *    slices of a wider projection, or one position of every sequence, need no
+ *    copy.  Strides stay below 2^22 in a scan of several tokens per sequence
+ *    and below 2^26 in layer norm of up to 2048 elements; rows times stride
+ *    stay within 2^40 everywhere.  Token t of sequence b of a fixed-length
+ *    batch is row b * T + t.  Token tensors need only their elements'
+ *    alignment; 16-byte aligned bases and strides run faster.  Parameters and
+ *    states are contiguous.
  *  - At most 65535 sequences.
  *  - Packed input (cu_seqlens, N + 1 device offsets) may end before the last
  *    row: output rows at and behind cu_seqlens[N] are left as they were.
