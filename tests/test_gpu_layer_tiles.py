@@ -1,10 +1,11 @@
-"""The selective scan where it cuts sequences into tiles, against references in 64 bits: sequences as long as 32-bit
-sizes hold."""
+"""The selective scan where it cuts sequences into tiles, against references in 64 bits: every tile
+length, every size of state, sequences as long as 32-bit sizes hold."""
 import numpy as np
 import pytest
 
 import layer_testlib as ref
-from test_gpu_layer import host, kda  # noqa: F401  (kda is the fixture)
+import test_gpu_layer as base
+from test_gpu_layer import dev, host, kda, layout, scan_inputs  # noqa: F401  (kda is the fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -67,3 +68,86 @@ def test_scan_of_the_longest_sequences(kda):
             ref.check(f"{k} at {w}", host(out[k][0, w:w + size]), want[k][part], scale[k][part], n, "bf16")
         if a == 0:
             ref.check("dh0", host(got["dh0"]), want["dh0"], scale["dh0"], n)
+
+
+# (sequences, ds, input, output): a state of every arrangement of lanes, some of them padded, in tiles of 64 tokens
+STATES = [((1, 300), 12, "bf16", "fp32"), ((1, 300), 20, "fp32", "fp32"), ((1, 300), 32, "bf16", "bf16"),
+          ((1, 300), 40, "fp32", "fp32"), ((1, 300), 64, "bf16", "fp32"), ((2, 129), 3, "fp32", "fp32"),
+          ([200, 0, 1, 131], 8, "bf16", "fp32"), ([200, 0, 1, 131], 20, "bf16", "fp32"), ([200, 0, 1, 131], 64, "fp32", "fp32"),
+          ([65, 0, 64, 1, 63, 190], 33, "bf16", "fp32")]
+
+
+@pytest.mark.parametrize("seqs,ds,dtype,out", STATES)
+@pytest.mark.parametrize("gate", [True, False])
+def test_tiles_of_every_state_size(kda, seqs, ds, dtype, out, gate):
+    base.test_scan_forward(kda, seqs, 70, ds, dtype, out, dict(gate=gate))
+    base.test_scan_gradients(kda, seqs, 70, ds, dtype, out, dict(gate=gate))
+
+
+def walk(offsets, u, dt, A, B, C, D, z, bias, h0, gy, gf):
+    """The definition in 64 bits on the GPU, token by token: outputs, final states and gradients."""
+    import torch
+    d = lambda t: t.double().reshape(-1, t.shape[-1])  # noqa: E731
+    u, B, C, z, gy, A, D, h0, gf = d(u), d(B), d(C), d(z), d(gy), A.double(), D.double(), h0.double(), gf.double()
+    raw = d(dt) + bias.double()
+    delta, sg = torch.logaddexp(raw, torch.zeros_like(raw)), 1 / (1 + torch.exp(-z))
+    gate = z * sg
+    gp, xl = gy * gate, delta * u
+    rows, dim, ds = len(u), *A.shape
+    h, carried = (torch.empty(rows, dim, ds, dtype=torch.float64, device="cuda") for _ in range(2))
+    final, dh0, dA = h0.clone(), gf.clone(), torch.zeros_like(A)
+    dB, dC, P, S = torch.empty_like(B), torch.empty_like(C), torch.empty_like(u), torch.empty_like(u)
+    for n, (s, e) in ref.spans(offsets):
+        state = h0[n]
+        for t in range(s, e):
+            torch.mul(torch.exp(delta[t, :, None] * A), state, out=carried[t])
+            state = torch.addcmul(carried[t], xl[t, :, None], B[t], out=h[t])
+        if e > s:
+            final[n] = state
+        g = gf[n]
+        for t in range(e - 1, s - 1, -1):
+            G = torch.addcmul(g, gp[t, :, None], C[t])
+            c = G * carried[t]
+            dC[t], dB[t], P[t], S[t] = gp[t] @ h[t], xl[t] @ G, G @ B[t], (c * A).sum(-1)
+            dA.addcmul_(c, delta[t, :, None])
+            g = torch.exp(delta[t, :, None] * A) * G
+        dh0[n] = g
+    yp = (h * C[:, None]).sum(-1) + D * u
+    ddt = (u * P + S) / (1 + torch.exp(-raw))
+    return dict(y=yp * gate, final=final, du=D * gp + delta * P, ddt=ddt, dz=gy * yp * sg * (1 + z * (1 - sg)), dB=dB, dC=dC,
+                dA=dA, dD=(gp * u).sum(0), ddt_bias=ddt.sum(0), dh0=dh0)
+
+
+@pytest.mark.parametrize("seqs,ds,dtype,tile", [
+    ((1, 4499), 16, "bf16", 144), ((1, 8200), 16, "bf16", 256), ((3, 1500), 16, "fp32", 144),
+    ([700, 0, 1, 1500, 144, 0, 998], 16, "fp32", 112), ((1, 2400), 24, "bf16", 80), ((1, 2400), 40, "fp32", 80),
+    ([3000, 1, 0, 2000], 8, "bf16", 160)])
+def test_long_tiles(kda, seqs, ds, dtype, tile):
+    """Tiles above the shortest, of lengths that are no powers of two, the last of a sequence shorter.  Every token's row
+    is held by itself: a state's roundings, some 20 a token, add up independently over the tokens that it remembers, at
+    most the longest sequence; the gradients have them on both ways, and sums over channels or tokens some more."""
+    import torch
+    dim = 2048
+    offsets, B, T, cu = layout(seqs)
+    N, rows = len(offsets) - 1, offsets[-1]
+    g = torch.Generator("cuda").manual_seed(ds + rows)
+    n = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    tokens = lambda d: n(B, T, d).to(base.tdtype(dtype))  # noqa: E731
+    u, dt, z, gy, Bm, Cm = tokens(dim), tokens(dim), tokens(dim), tokens(dim), tokens(ds), tokens(ds)
+    A, D, bias, h0, gf = -torch.exp(n(dim, ds)), n(dim), n(dim) - 3, n(N, dim, ds), n(N, dim, ds)
+    slots = N * -(-T // tile) if cu is None else T // tile + N
+    assert kda.selective_scan_fwd_workspace_bytes(u, ds, cu) == slots * dim * (ds + 1) * 4, "another tile length"
+    kw = dict(initial_state=h0, cu_seqlens=cu, dt_softplus=True)
+    y, final = kda.selective_scan_fwd(u, dt, A, Bm, Cm, D, z, bias, out_dtype=torch.float32, **kw)
+    got = kda.selective_scan_bwd(u, dt, A, Bm, Cm, gy, D, z, bias, grad_final_state=gf, **kw)
+    got.update(y=y, final=final)
+    want = walk(offsets, u, dt, A, Bm, Cm, D, z, bias, h0, gy, gf)
+    longest = max(b - a for a, b in zip(offsets, offsets[1:]))
+    bound = 2 * (20 * longest) ** .5 * 2 ** -24
+    for k, v in want.items():
+        v = v.reshape(-1, v.shape[-1]) if k not in ("final", "dh0") else v.reshape(N, -1)
+        v = v if k not in ("dD", "ddt_bias") else v.reshape(1, -1)
+        err = (got[k].double().reshape(v.shape) - v).norm(dim=1) / v.norm(dim=1)
+        most = bound if k in ("y", "final") else 2 * bound if k in ("du", "ddt", "dz", "dB", "dC", "dh0") else 8 * bound
+        print(f"    {k}: worst row {float(err.max() / most):.3f} of its bound", flush=True)
+        assert float(err.max()) < most, k
