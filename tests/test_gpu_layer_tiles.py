@@ -1,5 +1,5 @@
-"""The selective scan where it cuts sequences into tiles, against references in 64 bits: every tile
-length, every size of state, sequences as long as 32-bit sizes hold."""
+"""The selective scan where it cuts sequences into tiles, and its step where a workgroup takes two sequences, against
+references in 64 bits: every tile length, every size of state, sequences as long as 32-bit sizes hold."""
 import numpy as np
 import pytest
 
@@ -151,3 +151,38 @@ def test_long_tiles(kda, seqs, ds, dtype, tile):
         most = bound if k in ("y", "final") else 2 * bound if k in ("du", "ddt", "dz", "dB", "dC", "dh0") else 8 * bound
         print(f"    {k}: worst row {float(err.max() / most):.3f} of its bound", flush=True)
         assert float(err.max()) < most, k
+
+
+@pytest.mark.parametrize("N,dim,ds,dtype", [(65, 4096, 16, "bf16"), (129, 2050, 13, "fp32"), (67, 4096, 40, "fp32"),
+                                            (131, 2100, 32, "bf16")])
+@pytest.mark.parametrize("gate", [True, False])
+def test_steps_of_a_full_batch(kda, N, dim, ds, dtype, gate):
+    """Batches from which on a workgroup takes two sequences, odd ones: in place, against the definition and bit for bit
+    against smaller batches, of which it takes one each."""
+    import torch
+    assert N * -(-dim // 64) >= 4096 and (N - N // 2) * -(-dim // 64) < 4096
+    offsets = list(range(N + 1))
+    x = scan_inputs(4, offsets, N, dim, ds, dtype, gate=gate)
+    s = {k: None if x[k] is None else dev(x[k], dtype, sliced=k == "B") for k in ("u", "dt", "B", "C", "z")}
+    p = {k: dev(x[k]) for k in ("A", "D", "dt_bias")}
+
+    def step(a, b, state):
+        t = {k: None if v is None else v[a:b] for k, v in s.items()}
+        return kda.selective_scan_step(t["u"], t["dt"], p["A"], t["B"], t["C"], state, p["D"], t["z"], p["dt_bias"],
+                                       dt_softplus=True, out_dtype=torch.float32)
+
+    state, half = dev(x["h0"]), N // 2
+    parts = dev(x["h0"][:half]), dev(x["h0"][half:])
+    y = step(0, N, state)
+    y0, y1 = step(0, half, parts[0]), step(half, N, parts[1])
+    assert torch.equal(y, torch.cat([y0, y1])) and torch.equal(state, torch.cat(parts))
+    want, size = ref.scan_forward(x, offsets), ref.scan_forward(x, offsets, absolute=True)
+    n = ref.scan_roundings(x, offsets)
+    ref.check("y", host(y), want["y"], size["y"], n)
+    ref.check("state", host(state), want["final"], size["final"], n)
+    other = torch.full_like(state, 7.0)  # to memory of its own, the old state kept
+    old = dev(x["h0"])
+    t = {k: v for k, v in s.items() if v is not None}
+    y2 = kda.selective_scan_step(t["u"], t["dt"], p["A"], t["B"], t["C"], old, p["D"], t.get("z"), p["dt_bias"], dt_softplus=True,
+                                 out_dtype=torch.float32, final_state=other)
+    assert torch.equal(y2, y) and torch.equal(other, state) and torch.equal(old, dev(x["h0"]))
