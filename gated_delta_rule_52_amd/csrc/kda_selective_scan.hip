@@ -45,8 +45,8 @@ __host__ __device__ inline FwdSpace fwd_space(float *ws, const SeqTiles &seq, in
 
 enum { kOutputs, kLocal };
 
-// LPC lanes per channel with R states each; tokens in groups of LPC, one per lane.  Two lanes and one were slower
-// at every size (16,384 x 4,096: 536 and 695 us against 497), four give the most waves.
+// LPC lanes per channel with R states each; tokens in groups of LPC, one per lane.  Four give the most waves: two and
+// one were slower at every size when they were compared (16,384 x 4,096: 536 and 695 us against 497, which are 465 by now).
 template <int MODE, int R, bool InBf16, bool GATED>
 __global__ void __launch_bounds__(256) scan_kernel(ScanFwdLaunch P) {
     using E = typename Raw<InBf16>::T;
@@ -302,8 +302,10 @@ __global__ void __launch_bounds__(256) scan_step_kernel(ScanFwdLaunch P) {
 }  // namespace
 
 // Whole sequences where they fill the chip by themselves, one pass; else tiles, and a second pass over the inputs.
-// On MI355X, bf16: 8 x 1,024 x 4,096 (512 workgroups) 185 us whole and 240 tiled, 12 x 1,024 x 2,048 (384) 181
-// and 184, 8 x 2,048 x 2,048 (256) 275 and 252, 2 x 4,096 x 4,096 (128) 544 and 246.
+// On MI355X, bf16: 8 x 1,024 x 4,096 (512 workgroups) 187 us whole and 241 tiled, 12 x 1,024 x 2,048 (384) 184
+// and 186, 8 x 2,048 x 2,048 (256) 274 and 249, 2 x 4,096 x 4,096 (128) 539 and 248.  Packed sequences go in tiles:
+// their lengths are on the device, and one long one would be what the call waits for (8,000 tokens beside 80 of 100, at
+// 4,096 channels: 380 us in tiles of 256, 1,074 whole).  Equal ones pay for it (16 x 2,048 x 4,096: 863 against 600).
 SeqTiles scan_fwd_tiles(const int32_t *cu, int N, int T, int dim, int ds) {
     SeqTiles s{cu, N, T, T > 0 ? T : 1};
     const int64_t groups = (dim + kScanChannels - 1) / kScanChannels;

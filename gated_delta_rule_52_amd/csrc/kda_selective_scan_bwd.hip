@@ -521,9 +521,10 @@ void launch_any(const ScanBwdLaunch &P, const BwdSpace &w) {
 
 }  // namespace
 
-// Whole sequences where they give two waves per SIMD, which is what the gradient kernel's registers allow, by
-// themselves; else tiles.  On MI355X, bf16: 16 x 1,024 x 4,096 (1,024 workgroups) 1,257 us whole and 1,410
-// tiled, 8 x 1,024 x 4,096 (512) 783 and 904, 12 x 1,024 x 2,048 (384) 757 and 672.
+// Whole sequences where they give two waves per SIMD by themselves, else tiles.  On MI355X, bf16: 16 x 1,024 x 4,096
+// (1,024 workgroups) 1,207 us whole and 1,285 tiled, 8 x 1,024 x 4,096 (512) 696 and 693, 12 x 1,024 x 2,048 (384) 670
+// and 520.  Packed ones go in tiles, as in the forward pass (8,000 tokens beside 80 of 100, 4,096 channels: 1,283 us
+// against 3,781 whole; 16 x 1,024 x 4,096 1,285 against 1,213).
 SeqTiles scan_bwd_tiles(const int32_t *cu, int N, int T, int dim, int ds) {
     SeqTiles s{cu, N, T, T > 0 ? T : 1};
     const int64_t groups = (dim + 63) / 64;

@@ -42,8 +42,11 @@ struct SeqTiles {
 };
 
 // Tiles of 256 tokens where the rows allow about 1,024 workgroups of `groups` to a tile, down to 64: longer ones
-// leave the chip idle, shorter ones spend on the chain what they gain (1 x 8,192 x 1,024: 86 us at 128, 92 at 64
-// and 256; 16,384 x 4,096: 470 at 256, 481 at 128, 552 at 64).
+// leave the chip idle, shorter ones spend on the chain what they gain.  Forward, bf16: 16,384 x 4,096 465 us at 256,
+// 471 at 128, 495 at 64, 476 at 512; 8,192 x 1,024 82 at 128, 87 at 64 and 256.  At the lower end, in us with tiles of
+// 64, 48 and 32 tokens: 8,192 x 512 57, 65, 71 (gradients 133, 148, 158), 4,096 x 512 37, 41, 44 (82, 89, 93), 3,001 x
+// 777 fp32 40, 40, 40 (87, 90, 89).  Below about 500 workgroups shorter ones win, which the rule does not follow:
+// 2,500 x 515 fp32 32, 29, 30 (70, 62, 63), 2,048 x 256 26, 24, 24 (59, 53, 49), 1,000 x 128 25, 21, 20 (54, 47, 42).
 inline void tile_for(SeqTiles &s, int64_t groups) {
     int64_t L = (s.rows() * groups / 1024 + 15) / 16 * 16;
     L = L < 64 ? 64 : L > 256 ? 256 : L;
