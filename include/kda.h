@@ -470,7 +470,8 @@ size_t kda_chunk_fwd_noalloc_max_workspace_bytes(void);
  *    batch is row b * T + t.  Token tensors need only their elements'
  *    alignment; 16-byte aligned bases and strides run faster.  Parameters and
  *    states are contiguous.
- *  - At most 65535 sequences.
+ *  - At most 65535 sequences and 2^31 - 1 tokens; sizes of which one launch
+ *    would take 2^32 threads or more are refused (KDA_ERR_UNSUPPORTED).
  *  - Packed input (cu_seqlens, N + 1 device offsets) may end before the last
  *    row: output rows at and behind cu_seqlens[N] are left as they were.
  * Outputs overlap neither inputs nor each other, except where an entry point
