@@ -12,7 +12,11 @@ __all__ = ["chunk_fwd", "recurrent_fwd", "recurrent_step", "recurrent_bwd", "Kda
 _LAYER = ["selective_scan_fwd", "selective_scan_step", "selective_scan_bwd", "short_conv_fwd", "short_conv_step",
           "short_conv_bwd", "layer_norm_fwd", "layer_norm_bwd", "selective_scan_fwd_workspace_bytes",
           "selective_scan_bwd_workspace_bytes", "short_conv_bwd_workspace_bytes", "layer_norm_bwd_workspace_bytes"]
-__all__ += _LAYER
+# latent attention between the recurrence's layers
+_LATENT = ["rotary_frequencies", "rotary_fwd", "rotary_bwd", "latent_cache_append", "latent_attention_step",
+           "latent_attention_fwd", "latent_attention_bwd", "latent_attention_step_workspace_bytes",
+           "latent_attention_bwd_workspace_bytes"]
+__all__ += _LAYER + _LATENT
 
 
 def __getattr__(name):
@@ -20,6 +24,8 @@ def __getattr__(name):
         raise AttributeError(name)
     if name in _LAYER:
         from . import layer_ops as module
+    elif name in _LATENT:
+        from . import latent_ops as module
     else:
         from . import ops as module
     value = globals()[name] = getattr(module, name)  # found here from now on

@@ -19,6 +19,8 @@ KDA_FLAG_GATE_SOFTPLUS = 2
 KDA_FLAG_SCALAR_GATE = 4
 KDA_SCAN_DT_SOFTPLUS = 1
 KDA_CONV_SILU = 1
+KDA_ROTARY_INTERLEAVED = 1
+KDA_ATTENTION_CAUSAL = 1
 
 STATUS = {
     0: "KDA_OK", 1: "KDA_ERR_NULL_POINTER", 2: "KDA_ERR_BAD_SHAPE", 3: "KDA_ERR_UNSUPPORTED",
@@ -36,7 +38,10 @@ EXPORTS = ("kda_chunk_fwd_workspace_bytes", "kda_chunk_fwd", "kda_recurrent_fwd"
            "kda_selective_scan_fwd_workspace_bytes", "kda_selective_scan_fwd", "kda_selective_scan_step",
            "kda_selective_scan_bwd_workspace_bytes", "kda_selective_scan_bwd", "kda_short_conv_fwd",
            "kda_short_conv_step", "kda_short_conv_bwd_workspace_bytes", "kda_short_conv_bwd",
-           "kda_layer_norm_fwd", "kda_layer_norm_bwd_workspace_bytes", "kda_layer_norm_bwd")
+           "kda_layer_norm_fwd", "kda_layer_norm_bwd_workspace_bytes", "kda_layer_norm_bwd",
+           "kda_rotary_fwd", "kda_rotary_bwd", "kda_latent_cache_append",
+           "kda_latent_attention_step_workspace_bytes", "kda_latent_attention_step", "kda_latent_attention_fwd",
+           "kda_latent_attention_bwd_workspace_bytes", "kda_latent_attention_bwd")
 
 vp = ctypes.c_void_p
 
@@ -199,6 +204,72 @@ class LayerNormBwdArgs(ctypes.Structure):
         p: stream""")
 
 
+class RotaryArgs(ctypes.Structure):
+    _fields_ = _fields("""
+        u: struct_size
+        p: x y positions inv_freq
+        l: x_stride x_head_stride y_stride y_head_stride rows
+        i: heads dim rot offset
+        f: scale
+        d: dtype
+        p: stream
+        u: flags""")
+
+
+class LatentAppendArgs(ctypes.Structure):
+    _fields_ = _fields("""
+        u: struct_size
+        p: latent rope cache slots positions inv_freq
+        l: latent_stride rope_stride rows
+        i: num_blocks page dl dr
+        f: scale
+        d: dtype
+        p: stream
+        u: flags""")
+
+
+class LatentStepArgs(ctypes.Structure):
+    _fields_ = _fields("""
+        u: struct_size
+        p: q_latent q_rope cache block_table lengths o lse
+        l: q_latent_stride q_latent_head_stride q_rope_stride q_rope_head_stride o_stride o_head_stride
+        l: block_table_stride
+        i: N H dl dr page num_blocks max_blocks
+        f: scale
+        d: in_dtype out_dtype
+        p: workspace
+        z: workspace_bytes
+        p: stream""")
+
+
+class LatentAttentionArgs(ctypes.Structure):
+    _fields_ = _fields("""
+        u: struct_size
+        p: q k k_rope v o lse cu_seqlens_q cu_seqlens_k
+        l: q_stride q_head_stride k_stride k_head_stride k_rope_stride v_stride v_head_stride o_stride o_head_stride
+        i: batch Tq Tk H dn dr dv num_seqs
+        f: scale
+        d: in_dtype out_dtype
+        p: stream
+        u: flags""")
+
+
+class LatentAttentionBwdArgs(ctypes.Structure):
+    _fields_ = _fields("""
+        u: struct_size
+        p: q k k_rope v o lse grad_o grad_q grad_k grad_k_rope grad_v cu_seqlens_q cu_seqlens_k
+        l: q_stride q_head_stride k_stride k_head_stride k_rope_stride v_stride v_head_stride o_stride o_head_stride
+        l: grad_o_stride grad_o_head_stride grad_q_stride grad_q_head_stride grad_k_stride grad_k_head_stride
+        l: grad_k_rope_stride grad_v_stride grad_v_head_stride
+        i: batch Tq Tk H dn dr dv num_seqs
+        f: scale
+        d: in_dtype grad_dtype
+        p: workspace
+        z: workspace_bytes
+        p: stream
+        u: flags""")
+
+
 # The layer operators' functions: their argument struct, and whether they return a size.
 LAYER_FUNCTIONS = {
     "kda_selective_scan_fwd_workspace_bytes": (SelectiveScanArgs, True),
@@ -213,6 +284,14 @@ LAYER_FUNCTIONS = {
     "kda_layer_norm_fwd": (LayerNormArgs, False),
     "kda_layer_norm_bwd_workspace_bytes": (LayerNormBwdArgs, True),
     "kda_layer_norm_bwd": (LayerNormBwdArgs, False),
+    "kda_rotary_fwd": (RotaryArgs, False),
+    "kda_rotary_bwd": (RotaryArgs, False),
+    "kda_latent_cache_append": (LatentAppendArgs, False),
+    "kda_latent_attention_step_workspace_bytes": (LatentStepArgs, True),
+    "kda_latent_attention_step": (LatentStepArgs, False),
+    "kda_latent_attention_fwd": (LatentAttentionArgs, False),
+    "kda_latent_attention_bwd_workspace_bytes": (LatentAttentionBwdArgs, True),
+    "kda_latent_attention_bwd": (LatentAttentionBwdArgs, False),
 }
 
 

@@ -1,0 +1,151 @@
+// kda_attend.hip - latent attention over expanded keys and values, forward.
+//
+// Per head, o_i = sum_j p_ij v_j with p_ij = exp(s_ij - lse_i), s_ij = scale (q_i[:dn] . k_j + q_i[dn:] . k_rope_j),
+// lse_i = log sum_j exp(s_ij) over the keys that query i sees.
+#include "kda_latent.h"
+
+namespace kda {
+namespace {
+
+using namespace la;
+
+template <class E, int NP, int RP, int VP>
+__global__ __launch_bounds__(256, 2) void attend_fwd_kernel(const AttendLaunch P) {
+    constexpr int BN = sizeof(E) == 2 ? 64 : 32;  // keys per tile
+    constexpr int SN = NP / (2 * Mx<E>::PER), SR = RP / (2 * Mx<E>::PER), ST = kSteps32<E>;
+    using KT = LdsTile<NP, E>;
+    using RT = LdsTile<RP, E>;
+    using VT = LdsTile<VP, E>;
+    constexpr int OR = BN * KT::ROW, OV = OR + BN * RT::ROW, BUF = OV + BN * VT::ROW;
+    __shared__ __attribute__((aligned(1024))) char lds[2 * BUF];
+
+    const Place w = place_of(P, P.q_seq);
+    if (!w.valid || w.at >= w.nq) return;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int shift = w.nk - w.nq;              // query i sees keys up to i + shift
+    const int q0 = w.at + 32 * wave, q = q0 + (lane & 31);
+    const bool live = q < w.nq;
+    const int tile_end = min(w.at + 128, w.nq);  // behind the workgroup's last query
+    const int keys = P.causal ? max(0, min(w.nk, tile_end + shift)) : w.nk;
+    const int wave_keys = P.causal ? min(w.nk, min(q0 + 32, w.nq) + shift) : w.nk;
+    const int limit = P.causal ? min(w.nk, q + shift + 1) : w.nk;  // the lane's query sees keys below it
+
+    typename Mx<E>::frag qf[SN + SR];
+    {
+        const E *row = head_row<E>(P.q, w.q_row + (live ? q : 0), w.h);
+#pragma unroll
+        for (int s = 0; s < SN; ++s) qf[s] = row_operand<E>(row, s, P.dn, live, lane);
+#pragma unroll
+        for (int s = 0; s < SR; ++s) qf[SN + s] = row_operand<E>(row + P.dn, s, P.dr, live, lane);
+    }
+    const E *kp = head_row<E>(P.k, w.k_row, w.h), *rp = head_row<E>(P.kr, w.k_row, 0), *vp = head_row<E>(P.v, w.k_row, w.h);
+    auto fetch = [&](int key0, char *to) {
+        const int rows = min(BN, w.nk - key0);
+        KT::template fill<BN, 4>(to, rows_buffer(kp + key0 * P.k.stride, P.k.stride, rows, P.dn), P.k.stride * sizeof(E), P.dn * sizeof(E), wave, lane);
+        RT::template fill<BN, 4>(to + OR, rows_buffer(rp + key0 * P.kr.stride, P.kr.stride, rows, P.dr), P.kr.stride * sizeof(E), P.dr * sizeof(E), wave, lane);
+        VT::template fill<BN, 4>(to + OV, rows_buffer(vp + key0 * P.v.stride, P.v.stride, rows, P.dv), P.v.stride * sizeof(E), P.dv * sizeof(E), wave, lane);
+    };
+
+    f16 acc[VP / 32];
+#pragma unroll
+    for (int c = 0; c < VP / 32; ++c)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[c][i] = 0.f;
+    float m = neg_inf(), l = 0.f;  // in powers of two; l: this lane's half of the row
+    const float c2 = P.scale * kLog2e;
+
+    if (keys > 0) fetch(0, lds);
+    int buf = 0;
+    for (int key0 = 0; key0 < keys; key0 += BN, buf ^= 1) {
+        loads_landed();
+        const char *t = lds + buf * BUF;
+        if (key0 + BN < keys) fetch(key0 + BN, lds + (buf ^ 1) * BUF);
+        if (key0 >= wave_keys) continue;
+        f16 s[BN / 32];
+#pragma unroll
+        for (int b = 0; b < BN / 32; ++b) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[b][i] = 0.f;
+#pragma unroll
+            for (int k = 0; k < SN; ++k) s[b] = Mx<E>::mma32(KT::rows32(t, 32 * b, k, lane), qf[k], s[b]);
+#pragma unroll
+            for (int k = 0; k < SR; ++k) s[b] = Mx<E>::mma32(RT::rows32(t + OR, 32 * b, k, lane), qf[SN + k], s[b]);
+        }
+        // a tile that some query of the wave sees only in part
+        if (key0 + BN > w.nk || (P.causal && key0 + BN > q0 + shift + 1)) {
+#pragma unroll
+            for (int b = 0; b < BN / 32; ++b)
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (key0 + 32 * b + 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3) >= limit) s[b][i] = neg_inf();
+        }
+        float top = s[0][0];
+#pragma unroll
+        for (int b = 0; b < BN / 32; ++b)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) top = fmaxf(top, s[b][i]);
+        top = fmaxf(top, other_half(top)) * c2;
+        // The reference point follows the maximum only when it lags by 2^8: weights up to 2^8 lose nothing in fp32 or
+        // bf16, and most tiles leave the sums as they are.
+        const bool move = top > m + 8.f;
+        if (__any(move)) {
+            const float to = move ? top : m, by = move ? exp2_f(m - to) : 1.f;
+            m = to;
+            l *= by;
+#pragma unroll
+            for (int c = 0; c < VP / 32; ++c)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) acc[c][i] *= by;
+        }
+        const float at = m == neg_inf() ? 0.f : m;
+#pragma unroll
+        for (int b = 0; b < BN / 32; ++b) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                s[b][i] = exp2_f(fmaf(s[b][i], c2, -at));
+                l += s[b][i];
+            }
+#pragma unroll
+            for (int k = 0; k < ST; ++k) {
+                const typename Mx<E>::frag p = result_operand<E>(s[b], k);
+#pragma unroll
+                for (int c = 0; c < VP / 32; ++c)
+                    acc[c] = Mx<E>::mma32(VT::cols32(t + OV, 32 * b, k, 32 * c, lane), p, acc[c]);
+            }
+        }
+    }
+    if (!live) return;
+    l += other_half(l);
+    const float by = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;  // NaN stays
+    const int64_t row = w.q_row + q;
+    if (P.lse && lane < 32) P.lse[row * P.H + w.h] = l == 0.f ? neg_inf() : (m + __log2f(l)) * kLn2;
+    const int64_t out = row * P.o.stride + w.h * P.o.head_stride;
+#pragma unroll
+    for (int c = 0; c < VP / 32; ++c)
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            const int col = 32 * c + 8 * b + 4 * (lane >> 5);
+            if (col < P.dv)
+                store4(P.o.p, out + col, P.out_bf16, acc[c][4 * b] * by, acc[c][4 * b + 1] * by, acc[c][4 * b + 2] * by, acc[c][4 * b + 3] * by);
+        }
+}
+
+template <class E, int NP, int RP, int VP>
+void launch(const AttendLaunch &P, unsigned grid) {
+    attend_fwd_kernel<E, NP, RP, VP><<<grid, 256, 0, P.stream>>>(P);
+}
+
+}  // namespace
+
+hipError_t launch_attend_fwd(const AttendLaunch &P) {
+    AttendLaunch L = P;
+    L.q_seq.L = 128;
+    const int64_t grid = (L.q_seq.cu ? L.q_seq.slots() : L.q_seq.N * static_cast<int64_t>(L.q_seq.per_seq())) * P.H;
+    const bool small = P.dn <= 64 && P.dr <= 32 && P.dv <= 64;
+    const unsigned n = static_cast<unsigned>(grid);
+    if (P.bf16) small ? launch<uint16_t, 64, 32, 64>(L, n) : launch<uint16_t, 128, 64, 128>(L, n);
+    else small ? launch<float, 64, 32, 64>(L, n) : launch<float, 128, 64, 128>(L, n);
+    return hipGetLastError();
+}
+
+}  // namespace kda

@@ -1,0 +1,313 @@
+// kda_latent.h - what the latent attention kernels share: launch structs, matrix products of 32 x 32 and 16 x 16 tiles
+// in bf16 or fp32, and tiles of rows in LDS that are filled by loads past the registers.
+#pragma once
+
+#include <type_traits>
+
+#include "kda_device.h"
+#include "kda_latent_pages.h"
+#include "kda_seq_tiles.h"
+
+namespace kda {
+
+// [rows, heads, width] elements, rows and heads any distance apart.
+struct Heads {
+    void *p;
+    int64_t stride, head_stride;  // elements
+};
+
+struct RotaryLaunch {
+    Heads x, y;
+    const int32_t *positions;
+    const float *inv_freq;
+    int64_t rows;
+    int heads, dim, rot, offset;
+    float scale;
+    int interleaved, inverse, bf16;
+    hipStream_t stream;
+};
+hipError_t launch_rotary(const RotaryLaunch &P);
+int64_t rotary_threads(int64_t rows, int heads, int dim);
+
+struct AppendLaunch {
+    Heads latent, rope;  // head_stride unused
+    void *cache;
+    const int32_t *slots, *positions;
+    const float *inv_freq;  // null: no rotation
+    int64_t rows, cache_rows;
+    int dl, dr;
+    float scale;
+    int interleaved, bf16;
+    hipStream_t stream;
+};
+hipError_t launch_append(const AppendLaunch &P);
+
+struct LatentStepLaunch {
+    Heads ql, qr, o;
+    const void *cache;
+    CachePages pages;
+    const int32_t *lengths;
+    float *lse;  // may be null
+    int N, H, dl, dr;
+    float scale;
+    int bf16, out_bf16;
+    int splits;
+    float *ws;
+    hipStream_t stream;
+};
+int latent_step_splits(int N, int H, int dl, int64_t longest, bool bf16);
+size_t latent_step_workspace_bytes(int N, int H, int dl, int splits);
+hipError_t launch_latent_step(const LatentStepLaunch &P);
+int64_t latent_step_threads(int N, int H, bool bf16, int splits);
+
+struct AttendLaunch {
+    Heads q, k, v, o;
+    Heads kr;    // head_stride unused
+    float *lse;  // [rows_q, H]
+    SeqTiles q_seq, k_seq;  // L set by the kernel that walks them
+    int H, dn, dr, dv;
+    float scale;
+    int causal, bf16, out_bf16;
+    hipStream_t stream;
+    // gradients
+    Heads go, dq, dk, dkr, dvg;
+    int grad_bf16;
+    float *delta;     // [rows_q, H]
+    float *dkr_part;  // [rows_k, H, dr]
+};
+hipError_t launch_attend_fwd(const AttendLaunch &P);
+hipError_t launch_attend_bwd(const AttendLaunch &P);
+int64_t attend_threads(const SeqTiles &q, const SeqTiles &k, int H, int dr, bool backward);
+
+// ---- device side ---------------------------------------------------------------------------------------
+
+namespace la {
+
+typedef __bf16 b8 __attribute__((ext_vector_type(8)));
+typedef __bf16 b4 __attribute__((ext_vector_type(4)));
+typedef short s4 __attribute__((ext_vector_type(4)));
+typedef float f4 __attribute__((ext_vector_type(4)));
+typedef float f16 __attribute__((ext_vector_type(16)));
+typedef unsigned u4 __attribute__((ext_vector_type(4)));
+typedef unsigned u2 __attribute__((ext_vector_type(2)));
+typedef __amdgpu_buffer_rsrc_t rsrc_t;
+typedef __attribute__((address_space(3))) void *lds_ptr;
+typedef __attribute__((address_space(3))) s4 *lds_s4;
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ float neg_inf() { return -__builtin_inff(); }
+__device__ __forceinline__ float exp2_f(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// Bytes [base, base + bytes) as a buffer: loads at or past its end give zeros, so rows behind a sequence and columns
+// behind a head need no branch.
+__device__ __forceinline__ rsrc_t buffer(const void *base, uint32_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), 0, static_cast<int>(bytes), 0x00020000);
+}
+constexpr uint32_t kOutside = 0x7ffffff0u;  // an offset past the end of every buffer here (all are below 2^30 bytes)
+
+// Four consecutive elements stored from fp32.
+__device__ __forceinline__ void store4(void *p, int64_t i, bool bf16, float a, float b, float c, float d) {
+    if (bf16) {
+        b4 v = {static_cast<__bf16>(a), static_cast<__bf16>(b), static_cast<__bf16>(c), static_cast<__bf16>(d)};
+        *reinterpret_cast<u2 *>(static_cast<uint16_t *>(p) + i) = __builtin_bit_cast(u2, v);
+    } else {
+        *reinterpret_cast<f4 *>(static_cast<float *>(p) + i) = f4{a, b, c, d};
+    }
+}
+
+// Matrix products.  A `step` multiplies what one 16-byte operand per lane holds: for a 32 x 32 tile lane l has row
+// (or column) l % 32 and half h = l / 32 of the step's elements along the contraction, for 16 x 16 row l % 16 and
+// quarter l / 16.  fp32 spends four instructions on it, each with the operand's next element; which element of the
+// contraction a lane's element is does not matter as long as both operands agree.
+template <class E>
+struct Mx;
+template <>
+struct Mx<uint16_t> {
+    typedef b8 frag;
+    static constexpr int PER = 8;  // elements of an operand
+    __device__ __forceinline__ static f16 mma32(frag a, frag b, f16 c) {
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+    }
+    __device__ __forceinline__ static f4 mma16(frag a, frag b, f4 c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+    }
+    __device__ __forceinline__ static frag zero() { return __builtin_bit_cast(frag, (u4{0, 0, 0, 0})); }
+};
+template <>
+struct Mx<float> {
+    typedef f4 frag;
+    static constexpr int PER = 4;
+    __device__ __forceinline__ static f16 mma32(frag a, frag b, f16 c) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[j], b[j], c, 0, 0, 0);
+        return c;
+    }
+    __device__ __forceinline__ static f4 mma16(frag a, frag b, f4 c) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[j], b[j], c, 0, 0, 0);
+        return c;
+    }
+    __device__ __forceinline__ static frag zero() { return f4{0, 0, 0, 0}; }
+};
+
+// Rows of W elements in LDS, in 16-byte units.  Unit u of row r lies at place u ^ swz(r): the four rows that a
+// transposing read takes 32 bytes of each, and the rows that an operand read takes 16 bytes of each, then lie in
+// different banks.  swz repeats after 8 rows.
+template <int W, class E>
+struct LdsTile {
+    static constexpr int ROW = W * static_cast<int>(sizeof(E)), UNITS = ROW / 16;
+    static_assert(UNITS >= 4 && (UNITS & (UNITS - 1)) == 0, "rows of 64 bytes or a power of two more");
+    __device__ __forceinline__ static int swz(int row) {
+        return UNITS >= 16 ? (row & 7) << 1 : UNITS == 8 ? ((row >> 1) & 3) << 1 : ((row >> 2) & 1) << 1;
+    }
+    __device__ __forceinline__ static int at(int row, int unit) { return row * ROW + ((unit ^ swz(row)) << 4); }
+
+    // Fills ROWS rows from rows `stride` bytes apart of a buffer, `width` bytes of each (a multiple of 16), zeros
+    // behind them and behind the buffer, past the registers: the data has arrived after a wait for the wave's loads.
+    template <int ROWS, int WAVES>
+    __device__ __forceinline__ static void fill(char *lds, rsrc_t from, uint32_t stride, uint32_t width, int wave, int lane) {
+        constexpr int LOADS = ROWS * UNITS / 64;
+        static_assert(LOADS > 0, "");
+#pragma unroll
+        for (int i = 0; i < (LOADS + WAVES - 1) / WAVES; ++i) {
+            const int u = wave + WAVES * i;
+            if (LOADS % WAVES != 0 && u >= LOADS) break;
+            const int c = u * 64 + lane, row = c / UNITS, unit = (c % UNITS) ^ swz(row);
+            const uint32_t off = static_cast<uint32_t>(unit) * 16 < width ? row * stride + unit * 16 : kOutside;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (lds_ptr)(lds + u * 1024), 16, static_cast<int>(off), 0, 0, 0);
+        }
+    }
+    // A step's operand whose rows are the tile's.
+    __device__ __forceinline__ static typename Mx<E>::frag rows32(const char *lds, int row0, int step, int lane) {
+        return *reinterpret_cast<const typename Mx<E>::frag *>(lds + at(row0 + (lane & 31), 2 * step + (lane >> 5)));
+    }
+    __device__ __forceinline__ static typename Mx<E>::frag rows16(const char *lds, int row0, int step, int lane) {
+        return *reinterpret_cast<const typename Mx<E>::frag *>(lds + at(row0 + (lane & 15), 4 * step + (lane >> 4)));
+    }
+    // A step's operand whose rows are the tile's columns col0 .. + 31, contracted over the tile's rows, in the order
+    // in which a lane holds the rows of a 32 x 32 result (lane half h: rows 8 b + 4 h + i): bf16 steps take 16 rows,
+    // fp32 steps 8.
+    __device__ __forceinline__ static typename Mx<E>::frag cols32(const char *lds, int row0, int step, int col0, int lane) {
+        const int h = lane >> 5;
+        if constexpr (sizeof(E) == 2) {
+            const int i = lane & 15, row = row0 + 16 * step + 4 * h + (i >> 2);
+            const int unit = (col0 >> 3) + ((lane >> 3) & 2) + ((i >> 1) & 1);
+            const char *p = lds + (i & 1) * 8;
+            const s4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4)(p + at(row, unit)));
+            const s4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4)(p + at(row, unit) + 8 * ROW));
+            return __builtin_bit_cast(b8, (__attribute__((ext_vector_type(8))) short){lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]});
+        } else {
+            const int col = col0 + (lane & 31);
+            f4 v;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                v[j] = *reinterpret_cast<const float *>(lds + at(row0 + 8 * step + 4 * h + j, col >> 2) + (col & 3) * 4);
+            return v;
+        }
+    }
+    // The same for 16 columns and the row order of a quarter's consecutive rows (bf16: 8 g .. + 7 of 32, fp32: 4 g .. + 3
+    // of 16).
+    __device__ __forceinline__ static typename Mx<E>::frag cols16(const char *lds, int row0, int col0, int lane) {
+        const int g = lane >> 4, i = lane & 15;
+        if constexpr (sizeof(E) == 2) {
+            const int row = row0 + 8 * g + (i >> 2), unit = (col0 >> 3) + ((i >> 1) & 1);
+            const char *p = lds + (i & 1) * 8;
+            const s4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4)(p + at(row, unit)));
+            const s4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4)(p + at(row + 4, unit)));
+            return __builtin_bit_cast(b8, (__attribute__((ext_vector_type(8))) short){lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]});
+        } else {
+            const int col = col0 + i;
+            f4 v;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                v[j] = *reinterpret_cast<const float *>(lds + at(row0 + 4 * g + j, col >> 2) + (col & 3) * 4);
+            return v;
+        }
+    }
+};
+
+// Rows of a 32 x 32 result as a step's operand (the order that cols32 reads in).
+template <class E>
+__device__ __forceinline__ typename Mx<E>::frag result_operand(const f16 &s, int step) {
+    if constexpr (sizeof(E) == 2) {
+        b8 v;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = static_cast<__bf16>(s[8 * step + j]);
+        return v;
+    } else {
+        return f4{s[4 * step], s[4 * step + 1], s[4 * step + 2], s[4 * step + 3]};
+    }
+}
+template <class E>
+constexpr int kSteps32 = 32 / (2 * Mx<E>::PER);  // steps that contract 32 rows
+
+// A row's operands straight from memory: element 2 PER step + PER h on; zeros from `width` on or where !live.
+template <class E>
+__device__ __forceinline__ typename Mx<E>::frag row_operand(const E *row, int step, int width, bool live, int lane) {
+    const int c = (2 * step + (lane >> 5)) * Mx<E>::PER;
+    return live && c < width ? *reinterpret_cast<const typename Mx<E>::frag *>(row + c) : Mx<E>::zero();
+}
+
+// A value and that of the lane in the other half.
+__device__ __forceinline__ float other_half(float x) {
+    const u2 r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return __uint_as_float((threadIdx.x & 32) ? r[0] : r[1]);
+}
+
+// All of the wave's loads into LDS have arrived, and every wave is here.
+__device__ __forceinline__ void loads_landed() {
+    __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
+    __syncthreads();
+}
+
+// ---- attention over expanded keys and values -------------------------------------------------------------
+
+// Where a workgroup's tile lies: the sequence's rows of queries and keys.
+struct Place {
+    int h;
+    int64_t q_row, k_row;  // the sequences' first rows
+    int nq, nk;            // their lengths
+    int at;                // first row of the tile in its sequence
+    bool valid;
+};
+// Workgroups go round-robin over the 8 XCDs: heads (of sequences, where they have equal lengths) are dealt to the XCDs
+// whole where their number allows, so that an L2 fetches a head's keys once.  A head's last tiles, which see the most keys,
+// start first.
+__device__ __forceinline__ Place place_of(const AttendLaunch &P, const SeqTiles &tiled) {
+    const int64_t per = tiled.cu ? tiled.slots() : tiled.per_seq();
+    const int64_t groups = static_cast<int64_t>(P.H) * (tiled.cu ? 1 : tiled.N);
+    const int64_t id = blockIdx.x;
+    int64_t group, k;
+    if (groups % 8 == 0) {
+        const int64_t r = id >> 3;
+        group = (id & 7) + 8 * (r / per);
+        k = r % per;
+    } else {
+        group = id / per;
+        k = id % per;
+    }
+    k = per - 1 - k;
+    Place w;
+    w.h = static_cast<int>(group % P.H);
+    const Tile t = tile_at(tiled, (tiled.cu ? 0 : group / P.H * per) + k);
+    const int n = __builtin_amdgcn_readfirstlane(t.n);
+    w.valid = t.valid;
+    P.q_seq.sequence(n, w.q_row, w.nq);
+    P.k_seq.sequence(n, w.k_row, w.nk);
+    w.at = __builtin_amdgcn_readfirstlane(t.k) * tiled.L;
+    return w;
+}
+
+template <class E>
+__device__ __forceinline__ const E *head_row(const Heads &t, int64_t row, int h) {
+    return static_cast<const E *>(t.p) + row * t.stride + h * t.head_stride;
+}
+// A buffer over `rows` rows of `width` elements from there.
+template <class E>
+__device__ __forceinline__ rsrc_t rows_buffer(const E *p, int64_t stride, int rows, int width) {
+    return buffer(p, rows > 0 ? static_cast<uint32_t>(((rows - 1) * stride + width) * static_cast<int64_t>(sizeof(E))) : 0);
+}
+
+}  // namespace la
+}  // namespace kda

@@ -1,85 +1,15 @@
 // kda_layer_api.cpp - host entry points of the layer operators in include/kda.h: selective scan, short
 // convolution, layer norm.  As in kda_api.cpp every argument is validated before anything is enqueued.
 #include <cmath>
-#include <cstdarg>
-#include <cstddef>
-#include <cstdio>
 
-#include "kda.h"
-#include "kda_internal.h"
+#include "kda_checks.h"
 #include "kda_layer.h"
 
 namespace {
 
-kda_status fail(kda_status s, const char *fmt, ...) __attribute__((format(printf, 2, 3)));
-kda_status fail(kda_status s, const char *fmt, ...) {
-    char buf[256];
-    va_list ap;
-    va_start(ap, fmt);
-    vsnprintf(buf, sizeof buf, fmt, ap);
-    va_end(ap);
-    kda::set_last_error(buf);
-    return s;
-}
-
-kda_status hip_status(hipError_t e, const char *what) {
-    if (e == hipSuccess) return KDA_OK;
-    return fail(KDA_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
-}
-
-bool valid_dtype(kda_dtype d) { return d == KDA_DTYPE_BF16 || d == KDA_DTYPE_FP32; }
-int64_t dsize(kda_dtype d) { return d == KDA_DTYPE_BF16 ? 2 : 4; }
-
-// The memory of a tensor: `rows` rows of `width` bytes, `stride` bytes apart.
-struct Span {
-    const char *name;
-    uintptr_t at;
-    int64_t rows, width, stride;
-    bool empty() const { return !at || rows <= 0 || width <= 0; }
-    uintptr_t end() const { return at + static_cast<uintptr_t>((rows - 1) * stride + width); }
-};
-Span flat(const char *name, const void *p, int64_t bytes) {
-    return {name, reinterpret_cast<uintptr_t>(p), 1, bytes, bytes};
-}
-Span strided(const char *name, const void *p, int64_t rows, int64_t width, int64_t stride, kda_dtype d) {
-    return {name, reinterpret_cast<uintptr_t>(p), rows, width * dsize(d), stride * dsize(d)};
-}
-bool overlap(const Span &a, const Span &b) {
-    if (a.empty() || b.empty() || a.at >= b.end() || b.at >= a.end()) return false;
-    if (a.stride == b.stride && a.rows > 1 && b.rows > 1) {  // column slices of one buffer may interleave
-        const int64_t m = a.stride, d = ((static_cast<int64_t>(b.at - a.at) % m) + m) % m;
-        if (d >= a.width && d + b.width <= m) return false;
-    }
-    return true;
-}
-// Every output against every input and the other outputs.
-template <size_t NI, size_t NO>
-kda_status check_overlaps(const Span (&ins)[NI], const Span (&outs)[NO]) {
-    for (size_t i = 0; i < NO; ++i) {
-        for (const Span &s : ins)
-            if (overlap(outs[i], s)) return fail(KDA_ERR_ALIAS, "%s overlaps %s", outs[i].name, s.name);
-        for (size_t j = i + 1; j < NO; ++j)
-            if (overlap(outs[i], outs[j])) return fail(KDA_ERR_ALIAS, "%s overlaps %s", outs[i].name, outs[j].name);
-    }
-    return KDA_OK;
-}
-
 // Row strides below which an operator's address arithmetic holds; the others form every row's address in 64 bits.
-constexpr int64_t kAnyStride = int64_t{1} << 40;
 constexpr int64_t kScanStride = int64_t{1} << 22;  // the walk over tokens: a row's bytes in a 24-bit multiply
 constexpr int64_t kNormStride = int64_t{1} << 26;  // rows that share a workgroup, up to 16: 32-bit distances within it
-
-kda_status check_stride(const char *name, const void *p, int64_t stride, int64_t width, int64_t rows, int64_t below) {
-    if (p && (stride < width || stride >= below || stride > (int64_t{1} << 40) / (rows > 0 ? rows : 1)))
-        return fail(KDA_ERR_BAD_SHAPE, "%s: stride %lld for rows of %lld", name, static_cast<long long>(stride),
-                    static_cast<long long>(width));
-    return KDA_OK;
-}
-#define KDA_TRY(x)                          \
-    do {                                    \
-        const kda_status st_ = (x);         \
-        if (st_ != KDA_OK) return st_;      \
-    } while (0)
 
 kda::Rows rows_of(const void *p, int64_t stride, kda_dtype d) {
     return {const_cast<void *>(p), stride, d == KDA_DTYPE_BF16 ? 1 : 0};
@@ -99,19 +29,6 @@ kda_status check_batch(const A *a) {
         return fail(KDA_ERR_BAD_SHAPE, "problem too large");
     if (a->dim >= 1 << 22) return fail(KDA_ERR_UNSUPPORTED, "dim=%d (below 2^22)", a->dim);
     if (a->num_seqs > 65535) return fail(KDA_ERR_UNSUPPORTED, "num_seqs=%d (at most 65535)", a->num_seqs);
-    return KDA_OK;
-}
-// Threads of one launch stay below 2^32.
-kda_status check_grid(int64_t threads) {
-    if (threads < 0 || threads >= (int64_t{1} << 32)) return fail(KDA_ERR_UNSUPPORTED, "problem too large for one launch");
-    return KDA_OK;
-}
-
-template <class A>
-kda_status check_struct(const A *a) {
-    if (!a) return fail(KDA_ERR_NULL_POINTER, "args is NULL");
-    if (a->struct_size != sizeof(A))
-        return fail(KDA_ERR_BAD_STRUCT, "struct_size %u (expected %zu)", a->struct_size, sizeof(A));
     return KDA_OK;
 }
 

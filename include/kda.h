@@ -724,6 +724,209 @@ typedef struct {
 size_t kda_layer_norm_bwd_workspace_bytes(const kda_layer_norm_bwd_args *args);
 kda_status kda_layer_norm_bwd(const kda_layer_norm_bwd_args *args);
 
+/*
+ * ---- Latent attention ------------------------------------------------------
+ *
+ * The attention layer that the Kimi Linear review notes put between every
+ * three layers of the recurrence ("Hybrid model"; its keys and values come
+ * from one latent vector per token): rotary positions, the paged cache of
+ * latent vectors, attention over expanded keys and values for prompts and
+ * gradients, and its absorbed form for single tokens over the cache.
+ *
+ * The conventions of the top of this file hold, with these additions:
+ *  - A tensor [rows, heads, width] has two strides in elements: `x_stride`
+ *    between rows and `x_head_stride` between heads (not looked at where there
+ *    is one row, or one head).  Heads may lie inside a row or rows inside a
+ *    head; elements of a head are consecutive.  Row t of batch entry b is
+ *    row b * T + t.
+ *  - Attention takes sizes that are multiples of 8, and bases and strides that
+ *    are multiples of 16 bytes; others are refused (KDA_ERR_UNSUPPORTED).
+ *    Rotation and the cache's rows need only their elements' alignment.
+ *  - Scores, softmax statistics and sums are fp32; in bf16 the weights exp(s -
+ *    max) and the scores' gradients are rounded to bf16 where a matrix product
+ *    takes them.
+ *  - A query that sees no key gets o = 0 and lse = -inf, and no gradient.
+ *  - Rows outside the sequences of a packed batch are left as they were.
+ */
+
+/* Pairs are adjacent elements (2 j, 2 j + 1) instead of (j, j + rot / 2). */
+#define KDA_ROTARY_INTERLEAVED 1u
+/* Query i of nq sees keys 0 .. i + nk - nq of nk, instead of all. */
+#define KDA_ATTENTION_CAUSAL 1u
+
+/*
+ * Rotary positions.  Of each head's `dim` elements, the `rot` from `offset` on
+ * are turned in pairs (a, b), pair j by the angle positions[row] inv_freq[j],
+ *     (a, b) -> scale (a cos - b sin, b cos + a sin);
+ * the others are copied.  Angles are formed in 64 bits, so far positions lose
+ * nothing.  Long contexts are a matter of inv_freq and scale.
+ *   x, y : [rows, heads, dim] dtype; y may be x (same strides): only the
+ *          turned part is touched then.  positions : [rows] int32, inv_freq :
+ *          [rot / 2] fp32.  rot is even, at most 4096; dim at most 2^20.
+ * kda_rotary_bwd: the gradient (x: of y, y: of x), which turns the other way.
+ */
+typedef struct {
+    uint32_t struct_size; /* = sizeof(kda_rotary_args) */
+    const void *x;
+    void *y;
+    const int32_t *positions;
+    const float *inv_freq;
+    int64_t x_stride, x_head_stride, y_stride, y_head_stride;
+    int64_t rows;
+    int32_t heads, dim, rot, offset;
+    float scale;
+    kda_dtype dtype;
+    void *stream;
+    uint32_t flags; /* KDA_ROTARY_* */
+} kda_rotary_args;
+
+kda_status kda_rotary_fwd(const kda_rotary_args *args);
+kda_status kda_rotary_bwd(const kda_rotary_args *args);
+
+/*
+ * Rows into the paged cache: cache row slots[i] becomes [latent_i | rope_i],
+ * rope_i turned as in kda_rotary_fwd (all dr elements) where inv_freq is given.
+ *   latent : [rows, dl], rope : [rows, dr], cache : [num_blocks, page, dl + dr]
+ *   dtype;  slots : [rows] int32, a block times `page` plus the place in it.
+ *   Rows whose slot is negative or behind the cache are skipped.  Slots of
+ *   one call differ: a slot given twice holds elements of either row.
+ *   positions : [rows] int32, inv_freq : [dr / 2] fp32, both or neither.
+ */
+typedef struct {
+    uint32_t struct_size; /* = sizeof(kda_latent_append_args) */
+    const void *latent;
+    const void *rope;
+    void *cache;
+    const int32_t *slots;
+    const int32_t *positions;
+    const float *inv_freq;
+    int64_t latent_stride, rope_stride;
+    int64_t rows;
+    int32_t num_blocks, page, dl, dr;
+    float scale;
+    kda_dtype dtype;
+    void *stream;
+    uint32_t flags; /* KDA_ROTARY_INTERLEAVED */
+} kda_latent_append_args;
+
+kda_status kda_latent_cache_append(const kda_latent_append_args *args);
+
+/*
+ * One token per sequence over the cache, in the absorbed form (the cached row
+ * [c | r] is every head's key and its first part the value):
+ *     s_hj = scale (q_latent_h . c_j + q_rope_h . r_j),
+ *     lse_h = log sum_j exp(s_hj),   o_h = sum_j exp(s_hj - lse_h) c_j
+ * over the first lengths[n] rows of sequence n, row j at place j % page of
+ * block block_table[n, j / page].
+ *   q_latent, o : [N, H, dl], q_rope : [N, H, dr] (in_dtype; o: out_dtype)
+ *   cache : [num_blocks, page, dl + dr] in_dtype;  lse : [N, H] fp32 or NULL
+ *   block_table : [N, max_blocks] int32, block_table_stride apart;  lengths :
+ *   [N] int32.  Lengths are held to 0 .. max_blocks * page; rows on blocks
+ *   that do not exist are left out, and entries behind a sequence's last row
+ *   are not read.
+ *   dl : at most 512, dr : at most 64.  scale > 0.
+ *   workspace : kda_latent_attention_step_workspace_bytes() bytes.
+ */
+typedef struct {
+    uint32_t struct_size; /* = sizeof(kda_latent_step_args) */
+    const void *q_latent;
+    const void *q_rope;
+    const void *cache;
+    const int32_t *block_table;
+    const int32_t *lengths;
+    void *o;
+    float *lse;
+    int64_t q_latent_stride, q_latent_head_stride, q_rope_stride, q_rope_head_stride;
+    int64_t o_stride, o_head_stride, block_table_stride;
+    int32_t N, H, dl, dr, page, num_blocks, max_blocks;
+    float scale;
+    kda_dtype in_dtype;
+    kda_dtype out_dtype;
+    void *workspace;
+    size_t workspace_bytes;
+    void *stream;
+} kda_latent_step_args;
+
+size_t kda_latent_attention_step_workspace_bytes(const kda_latent_step_args *args);
+kda_status kda_latent_attention_step(const kda_latent_step_args *args);
+
+/*
+ * Attention over expanded keys and values, per sequence and head:
+ *     s_ij = scale (q_i[:dn] . k_j + q_i[dn:] . k_rope_j),
+ *     lse_i = log sum_j exp(s_ij),   o_i = sum_j exp(s_ij - lse_i) v_j,
+ * k_rope shared by the heads.
+ *   q : [rows_q, H, dn + dr], k : [rows_k, H, dn], k_rope : [rows_k, dr],
+ *   v : [rows_k, H, dv] in_dtype;  o : [rows_q, H, dv] out_dtype;
+ *   lse : [rows_q, H] fp32 or NULL.  Slices of a projection's [rows, H, dn +
+ *   dv] output serve as k and v.
+ *   cu_seqlens_q, cu_seqlens_k : NULL, or int32 [num_seqs + 1] offsets of the
+ *   queries and of the keys (both; then batch is 1).
+ *   dn, dv : at most 128, dr : at most 64.  scale > 0.  Row strides are below
+ *   2^22 elements; at most 2^30 rows.
+ */
+typedef struct {
+    uint32_t struct_size; /* = sizeof(kda_latent_attention_args) */
+    const void *q;
+    const void *k;
+    const void *k_rope;
+    const void *v;
+    void *o;
+    float *lse;
+    const int32_t *cu_seqlens_q;
+    const int32_t *cu_seqlens_k;
+    int64_t q_stride, q_head_stride, k_stride, k_head_stride, k_rope_stride, v_stride, v_head_stride;
+    int64_t o_stride, o_head_stride;
+    int32_t batch, Tq, Tk, H, dn, dr, dv, num_seqs;
+    float scale;
+    kda_dtype in_dtype;
+    kda_dtype out_dtype;
+    void *stream;
+    uint32_t flags; /* KDA_ATTENTION_* */
+} kda_latent_attention_args;
+
+kda_status kda_latent_attention_fwd(const kda_latent_attention_args *args);
+
+/*
+ * Its gradients for grad_o [rows_q, H, dv] (in_dtype), from the inputs and
+ * what the forward pass left: o (in_dtype) and lse.  With p_ij = exp(s_ij -
+ * lse_i) and ds_ij = p_ij (grad_o_i . v_j - grad_o_i . o_i),
+ *     grad_v_j = sum_i p_ij grad_o_i,   grad_k_j = scale sum_i ds_ij q_i[:dn],
+ *     grad_k_rope_j = scale sum_h sum_i ds_ij q_i[dn:],
+ *     grad_q_i = scale sum_j ds_ij [k_j | k_rope_j].
+ *   grad_q, grad_k, grad_k_rope, grad_v : the inputs' shapes, grad_dtype
+ *   workspace : kda_latent_attention_bwd_workspace_bytes() bytes.
+ */
+typedef struct {
+    uint32_t struct_size; /* = sizeof(kda_latent_attention_bwd_args) */
+    const void *q;
+    const void *k;
+    const void *k_rope;
+    const void *v;
+    const void *o;
+    const float *lse;
+    const void *grad_o;
+    void *grad_q;
+    void *grad_k;
+    void *grad_k_rope;
+    void *grad_v;
+    const int32_t *cu_seqlens_q;
+    const int32_t *cu_seqlens_k;
+    int64_t q_stride, q_head_stride, k_stride, k_head_stride, k_rope_stride, v_stride, v_head_stride;
+    int64_t o_stride, o_head_stride, grad_o_stride, grad_o_head_stride, grad_q_stride, grad_q_head_stride;
+    int64_t grad_k_stride, grad_k_head_stride, grad_k_rope_stride, grad_v_stride, grad_v_head_stride;
+    int32_t batch, Tq, Tk, H, dn, dr, dv, num_seqs;
+    float scale;
+    kda_dtype in_dtype;
+    kda_dtype grad_dtype;
+    void *workspace;
+    size_t workspace_bytes;
+    void *stream;
+    uint32_t flags; /* KDA_ATTENTION_* */
+} kda_latent_attention_bwd_args;
+
+size_t kda_latent_attention_bwd_workspace_bytes(const kda_latent_attention_bwd_args *args);
+kda_status kda_latent_attention_bwd(const kda_latent_attention_bwd_args *args);
+
 /* Static text for a status code. */
 const char *kda_status_string(kda_status s);
 /* Thread-local text describing the last failure on this thread ("" if none):
