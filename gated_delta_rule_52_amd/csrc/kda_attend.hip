@@ -84,7 +84,7 @@ __global__ __launch_bounds__(256, 2) void attend_fwd_kernel(const AttendLaunch P
         for (int b = 0; b < BN / 32; ++b)
 #pragma unroll
             for (int i = 0; i < 16; ++i) top = fmaxf(top, s[b][i]);
-        top = fmaxf(top, other_half(top)) * c2;
+        top = halves_max(top) * c2;
         // The reference point follows the maximum only when it lags by 2^8: weights up to 2^8 lose nothing in fp32 or
         // bf16, and most tiles leave the sums as they are.
         const bool move = top > m + 8.f;
@@ -115,7 +115,7 @@ __global__ __launch_bounds__(256, 2) void attend_fwd_kernel(const AttendLaunch P
         }
     }
     if (!live) return;
-    l += other_half(l);
+    l = halves_sum(l);
     const float by = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;  // NaN stays
     const int64_t row = w.q_row + q;
     if (P.lse && lane < 32) P.lse[row * P.H + w.h] = l == 0.f ? neg_inf() : (m + __log2f(l)) * kLn2;

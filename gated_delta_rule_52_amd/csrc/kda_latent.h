@@ -56,7 +56,7 @@ struct LatentStepLaunch {
     hipStream_t stream;
 };
 int latent_step_splits(int N, int H, int dl, int64_t longest, bool bf16);
-size_t latent_step_workspace_bytes(int N, int H, int dl, int splits);
+size_t latent_step_workspace_bytes(int N, int H, int dl, int splits, bool bf16);
 hipError_t launch_latent_step(const LatentStepLaunch &P);
 int64_t latent_step_threads(int N, int H, bool bf16, int splits);
 
@@ -151,6 +151,13 @@ struct Mx<float> {
     __device__ __forceinline__ static frag zero() { return f4{0, 0, 0, 0}; }
 };
 
+// A transposing read: of four rows of 16 bf16 per 16 lanes, the lanes giving the addresses of four consecutive elements
+// each, lane i gets column i.  The restrict qualifier tells the compiler what the kernels see to themselves (by
+// loads_landed): that no load into LDS in flight writes what is read; without it every such read waits for all of them.
+__device__ __forceinline__ s4 read_columns(const char *__restrict__ p) {
+    return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4)p);
+}
+
 // Rows of W elements in LDS, in 16-byte units.  Unit u of row r lies at place u ^ swz(r): the four rows that a
 // transposing read takes 32 bytes of each, and the rows that an operand read takes 16 bytes of each, then lie in
 // different banks.  swz repeats after 8 rows.
@@ -161,7 +168,10 @@ struct LdsTile {
     __device__ __forceinline__ static int swz(int row) {
         return UNITS >= 16 ? (row & 7) << 1 : UNITS == 8 ? ((row >> 1) & 3) << 1 : ((row >> 2) & 1) << 1;
     }
-    __device__ __forceinline__ static int at(int row, int unit) { return row * ROW + ((unit ^ swz(row)) << 4); }
+    // (in long rows the swap stays within 16 units: what lies beyond is a constant distance)
+    __device__ __forceinline__ static int at(int row, int unit) {
+        return row * ROW + (unit & ~15) * 16 + (((unit & 15) ^ swz(row)) << 4);
+    }
 
     // Fills ROWS rows from rows `stride` bytes apart of a buffer, `width` bytes of each (a multiple of 16), zeros
     // behind them and behind the buffer, past the registers: the data has arrived after a wait for the wave's loads.
@@ -180,10 +190,10 @@ struct LdsTile {
     }
     // A step's operand whose rows are the tile's.
     __device__ __forceinline__ static typename Mx<E>::frag rows32(const char *lds, int row0, int step, int lane) {
-        return *reinterpret_cast<const typename Mx<E>::frag *>(lds + at(row0 + (lane & 31), 2 * step + (lane >> 5)));
+        return *reinterpret_cast<const typename Mx<E>::frag *>(lds + at(row0 + (lane & 31), 2 * step | (lane >> 5)));
     }
     __device__ __forceinline__ static typename Mx<E>::frag rows16(const char *lds, int row0, int step, int lane) {
-        return *reinterpret_cast<const typename Mx<E>::frag *>(lds + at(row0 + (lane & 15), 4 * step + (lane >> 4)));
+        return *reinterpret_cast<const typename Mx<E>::frag *>(lds + at(row0 + (lane & 15), 4 * step | (lane >> 4)));
     }
     // A step's operand whose rows are the tile's columns col0 .. + 31, contracted over the tile's rows, in the order
     // in which a lane holds the rows of a 32 x 32 result (lane half h: rows 8 b + 4 h + i): bf16 steps take 16 rows,
@@ -192,10 +202,10 @@ struct LdsTile {
         const int h = lane >> 5;
         if constexpr (sizeof(E) == 2) {
             const int i = lane & 15, row = row0 + 16 * step + 4 * h + (i >> 2);
-            const int unit = (col0 >> 3) + ((lane >> 3) & 2) + ((i >> 1) & 1);
+            const int unit = (col0 >> 3) | ((lane >> 3) & 2) | ((i >> 1) & 1);
             const char *p = lds + (i & 1) * 8;
-            const s4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4)(p + at(row, unit)));
-            const s4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4)(p + at(row, unit) + 8 * ROW));
+            const s4 lo = read_columns(p + at(row, unit));
+            const s4 hi = read_columns(p + at(row, unit) + 8 * ROW);
             return __builtin_bit_cast(b8, (__attribute__((ext_vector_type(8))) short){lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]});
         } else {
             const int col = col0 + (lane & 31);
@@ -206,22 +216,20 @@ struct LdsTile {
             return v;
         }
     }
-    // The same for 16 columns and the row order of a quarter's consecutive rows (bf16: 8 g .. + 7 of 32, fp32: 4 g .. + 3
-    // of 16).
+    // The same for 16 columns and the rows that a lane holds of 16 x 16 results (quarter g: rows 4 g + i), one result for
+    // fp32 and two, 16 rows apart, for bf16.
     __device__ __forceinline__ static typename Mx<E>::frag cols16(const char *lds, int row0, int col0, int lane) {
         const int g = lane >> 4, i = lane & 15;
         if constexpr (sizeof(E) == 2) {
-            const int row = row0 + 8 * g + (i >> 2), unit = (col0 >> 3) + ((i >> 1) & 1);
-            const char *p = lds + (i & 1) * 8;
-            const s4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4)(p + at(row, unit)));
-            const s4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4)(p + at(row + 4, unit)));
+            const char *p = lds + (i & 1) * 8 + at(row0 + 4 * g + (i >> 2), (col0 >> 3) | ((i >> 1) & 1));
+            const s4 lo = read_columns(p);
+            const s4 hi = read_columns(p + 16 * ROW);
             return __builtin_bit_cast(b8, (__attribute__((ext_vector_type(8))) short){lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]});
         } else {
             const int col = col0 + i;
             f4 v;
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                v[j] = *reinterpret_cast<const float *>(lds + at(row0 + 4 * g + j, col >> 2) + (col & 3) * 4);
+            for (int j = 0; j < 4; ++j) v[j] = *reinterpret_cast<const float *>(lds + at(row0 + 4 * g + j, col >> 2) + (col & 3) * 4);
             return v;
         }
     }
@@ -249,10 +257,29 @@ __device__ __forceinline__ typename Mx<E>::frag row_operand(const E *row, int st
     return live && c < width ? *reinterpret_cast<const typename Mx<E>::frag *>(row + c) : Mx<E>::zero();
 }
 
-// A value and that of the lane in the other half.
-__device__ __forceinline__ float other_half(float x) {
-    const u2 r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-    return __uint_as_float((threadIdx.x & 32) ? r[0] : r[1]);
+// Maximum and sum over the two halves of a wave, and over its four quarters, in every lane: a swap of rows or halves
+// between two copies of a value leaves the partners' values side by side.
+__device__ __forceinline__ u2 swap_halves(float x) {
+    return __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+}
+__device__ __forceinline__ u2 swap_rows(float x) {
+    return __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+}
+__device__ __forceinline__ float halves_max(float x) {
+    const u2 r = swap_halves(x);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float halves_sum(float x) {
+    const u2 r = swap_halves(x);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+__device__ __forceinline__ float quarters_max(float x) {
+    const u2 r = swap_rows(x);
+    return halves_max(fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1])));
+}
+__device__ __forceinline__ float quarters_sum(float x) {
+    const u2 r = swap_rows(x);
+    return halves_sum(__uint_as_float(r[0]) + __uint_as_float(r[1]));
 }
 
 // All of the wave's loads into LDS have arrived, and every wave is here.
@@ -307,6 +334,33 @@ __device__ __forceinline__ const E *head_row(const Heads &t, int64_t row, int h)
 template <class E>
 __device__ __forceinline__ rsrc_t rows_buffer(const E *p, int64_t stride, int rows, int width) {
     return buffer(p, rows > 0 ? static_cast<uint32_t>(((rows - 1) * stride + width) * static_cast<int64_t>(sizeof(E))) : 0);
+}
+
+// What a wave has written to LDS is there, and every wave is here.  Unlike __syncthreads() it does not wait for loads: those
+// into LDS for a later tile stay in flight.
+__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+// The same value, of which the compiler does not know that: what is formed from it inside a loop is formed there, and takes
+// no register from one round to the next.
+__device__ __forceinline__ int afresh(int x) {
+    asm volatile("" : "+v"(x));
+    return x;
+}
+
+// N operands, each read from LDS and then used, with DEPTH reads in flight: left alone the compiler, which prefers few
+// registers, reads one at a time and waits for it.
+template <class F, int N, int DEPTH, class Read, class Use>
+__device__ __forceinline__ void pipelined(Read read, Use use) {
+    F f[DEPTH];
+#pragma unroll
+    for (int i = 0; i < DEPTH && i < N; ++i) f[i] = read(i);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        use(i, f[i % DEPTH]);
+        if (i + DEPTH < N) f[i % DEPTH] = read(i + DEPTH);
+        __builtin_amdgcn_sched_barrier(0);
+    }
 }
 
 }  // namespace la

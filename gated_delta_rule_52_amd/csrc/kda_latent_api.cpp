@@ -155,6 +155,9 @@ size_t attend_bwd_bytes(const A *a) {
     return delta_bytes(static_cast<int64_t>(a->batch) * a->Tq, a->H) + static_cast<size_t>(a->batch) * a->Tk * a->H * a->dr * 4;
 }
 
+int step_splits(const kda_latent_step_args *a) {
+    return kda::latent_step_splits(a->N, a->H, a->dl, static_cast<int64_t>(a->max_blocks) * a->page, a->in_dtype == KDA_DTYPE_BF16);
+}
 kda_status check_step_sizes(const kda_latent_step_args *a) {
     KDA_TRY(check_struct(a));
     if (a->N < 0 || a->H < 1 || a->page < 1 || a->num_blocks < 0 || a->max_blocks < 0)
@@ -167,10 +170,7 @@ kda_status check_step_sizes(const kda_latent_step_args *a) {
     if (a->N > 65535 || a->H > 65535) return fail(KDA_ERR_UNSUPPORTED, "N=%d H=%d (at most 65535)", a->N, a->H);
     if (static_cast<int64_t>(a->max_blocks) * a->page > kMostRows || static_cast<int64_t>(a->num_blocks) * a->page > INT32_MAX)
         return fail(KDA_ERR_UNSUPPORTED, "more than 2^30 rows per sequence or 2^31 - 1 in the cache");
-    return check_grid(kda::latent_step_threads(a->N, a->H, a->in_dtype == KDA_DTYPE_BF16, 512));
-}
-int step_splits(const kda_latent_step_args *a) {
-    return kda::latent_step_splits(a->N, a->H, a->dl, static_cast<int64_t>(a->max_blocks) * a->page, a->in_dtype == KDA_DTYPE_BF16);
+    return check_grid(kda::latent_step_threads(a->N, a->H, a->in_dtype == KDA_DTYPE_BF16, step_splits(a)));
 }
 
 }  // namespace
@@ -221,7 +221,7 @@ kda_status kda_latent_cache_append(const kda_latent_append_args *a) {
 
 size_t kda_latent_attention_step_workspace_bytes(const kda_latent_step_args *a) {
     if (check_step_sizes(a) != KDA_OK) return static_cast<size_t>(-1);
-    return kda::latent_step_workspace_bytes(a->N, a->H, a->dl, step_splits(a));
+    return kda::latent_step_workspace_bytes(a->N, a->H, a->dl, step_splits(a), a->in_dtype == KDA_DTYPE_BF16);
 }
 
 kda_status kda_latent_attention_step(const kda_latent_step_args *a) {
@@ -241,7 +241,7 @@ kda_status kda_latent_attention_step(const kda_latent_step_args *a) {
     for (const Tensor *t : {&ql, &qr, &o, &cache}) KDA_TRY(check_aligned(*t));
     if (a->N > 1) KDA_TRY(check_stride("block_table", a->block_table, a->block_table_stride, a->max_blocks, a->N, kAnyStride));
     const int splits = step_splits(a);
-    const size_t need = kda::latent_step_workspace_bytes(a->N, a->H, a->dl, splits);
+    const size_t need = kda::latent_step_workspace_bytes(a->N, a->H, a->dl, splits, a->in_dtype == KDA_DTYPE_BF16);
     if (a->workspace_bytes < need || (need > 0 && !a->workspace))
         return fail(KDA_ERR_WORKSPACE_TOO_SMALL, "workspace %zu < %zu bytes", a->workspace_bytes, need);
     if (need && reinterpret_cast<uintptr_t>(a->workspace) % 16) return fail(KDA_ERR_UNSUPPORTED, "workspace has to be aligned to 16 bytes");

@@ -15,12 +15,14 @@ struct CachePages {
         const int64_t room = static_cast<int64_t>(max_blocks) * page;
         return length <= 0 ? 0 : length < room ? length : static_cast<int>(room);
     }
-    // the cache row of a sequence's row `pos` < rows(length), -1 on a block that does not exist
-    __host__ __device__ __forceinline__ int64_t at(int64_t sequence, int pos) const {
-        const unsigned p = static_cast<unsigned>(pos), block = p / static_cast<unsigned>(page);
-        const int b = table[sequence * stride + block];
-        if (b < 0 || b >= num_blocks) return -1;
-        return static_cast<int64_t>(b) * page + (p - block * static_cast<unsigned>(page));
+    // the block of a sequence's row `pos` < rows(length)
+    __host__ __device__ __forceinline__ int block(int64_t sequence, int pos) const {
+        return table[sequence * stride + static_cast<unsigned>(pos) / static_cast<unsigned>(page)];
+    }
+    // the cache row of row `pos` of a sequence on that block, -1 where there is no such block
+    __host__ __device__ __forceinline__ int64_t row(int block, int pos) const {
+        if (block < 0 || block >= num_blocks) return -1;
+        return static_cast<int64_t>(block) * page + static_cast<unsigned>(pos) % static_cast<unsigned>(page);
     }
 };
 

@@ -25,7 +25,7 @@ int main(int argc, char **argv) {
     const int n = atoi(argv[1]);
     CachePages p{table.data(), atoi(argv[2]), atoi(argv[3]), atoi(argv[4]), static_cast<int>(atoi(argv[2]))};
     const int rows = p.rows(atoi(argv[5]));
-    for (int i = 0; i < rows; ++i) printf("%lld ", (long long)p.at(n, i));
+    for (int i = 0; i < rows; ++i) printf("%lld ", (long long)p.row(p.block(n, i), i));
     printf("| %lld %lld %lld %lld\n", (long long)slot_row(-1, 7), (long long)slot_row(7, 7), (long long)slot_row(6, 7),
            (long long)slot_row(2147483647, 2147483647));
 }
