@@ -70,6 +70,7 @@ __global__ __launch_bounds__(64 * kWaves<HT>, sizeof(E) == 2 ? 2 : 1) void laten
     using RT = LdsTile<kRopePad, E>;
     constexpr int OR = BN * LT::ROW, OM = OR + BN * RT::ROW, BUF = OM + BN * 4;
     constexpr int RPW = BN / W;                // rows that a wave fetches
+    constexpr int AUX = sizeof(E) == 2 && HT <= 2 ? 2 : 0;  // rows that one workgroup reads once pass the caches by (non-temporal)
     constexpr int PROW = BN * sizeof(E) + 16;  // a head's weights, padded off the banks of the next
     __shared__ __attribute__((aligned(1024))) char lds[2 * BUF];
     __shared__ __attribute__((aligned(16))) char weights[HT * 16 * PROW];
@@ -93,7 +94,7 @@ __global__ __launch_bounds__(64 * kWaves<HT>, sizeof(E) == 2 ? 2 : 1) void laten
         int mine = 0, total;
         for (int i = first; i < min(P.N, first + chunk); ++i) mine += tiles_of(i);
         const int at = scan<W>(mine, shared, total);
-        run = max(2, (total + P.splits - 1) / P.splits);
+        run = max(1, (total + P.splits - 1) / P.splits);
         const int64_t from = static_cast<int64_t>(w) * run;
         left = static_cast<int>(min(static_cast<int64_t>(run), total - from));
         if (left <= 0) return;
@@ -143,11 +144,11 @@ __global__ __launch_bounds__(64 * kWaves<HT>, sizeof(E) == 2 ? 2 : 1) void laten
                 for (int u = 0; u < LT::UNITS; u += 64) {
                     if (LT::UNITS >= 64 || lane < LT::UNITS) {
                         const uint32_t off = static_cast<uint32_t>((u + lane) ^ LT::swz(r)) * 16;
-                        __builtin_amdgcn_raw_ptr_buffer_load_lds(row, (lds_ptr)(to + r * LT::ROW + u * 16), 16, static_cast<int>(off < latent_bytes ? off : kOutside), 0, 0, 0);
+                        __builtin_amdgcn_raw_ptr_buffer_load_lds(row, (lds_ptr)(to + r * LT::ROW + u * 16), 16, static_cast<int>(off < latent_bytes ? off : kOutside), 0, 0, AUX);
                     }
                 }
                 if (lane < RT::UNITS)
-                    __builtin_amdgcn_raw_ptr_buffer_load_lds(row, (lds_ptr)(to + OR + r * RT::ROW), 16, static_cast<int>(latent_bytes + (lane ^ RT::swz(r)) * 16), 0, 0, 0);
+                    __builtin_amdgcn_raw_ptr_buffer_load_lds(row, (lds_ptr)(to + OR + r * RT::ROW), 16, static_cast<int>(latent_bytes + (lane ^ RT::swz(r)) * 16), 0, 0, AUX);
             }
         };
 
@@ -315,32 +316,65 @@ __global__ __launch_bounds__(64 * kWaves<HT>, sizeof(E) == 2 ? 2 : 1) void laten
 }
 
 // Joins the parts of a (sequence, head): o = sum_s exp(lse_s - lse) o_s, lse = log sum_s exp(lse_s).  Sequences without rows
-// get zeros here.
-__global__ __launch_bounds__(128) void latent_join_kernel(const LatentStepLaunch P, int heads, int groups) {
+// get zeros here.  COLS columns per workgroup, COLS / 4 threads of four by those that share the parts out.
+constexpr int kJoinParts = 512;
+template <int COLS>
+__global__ __launch_bounds__(256) void latent_join_kernel(const LatentStepLaunch P, int heads, int groups) {
+    __shared__ float weight[kJoinParts];
+    constexpr int T = COLS / 4, Q = 256 / T;
+    __shared__ f4 sums[Q][T];
+    __shared__ float2 stats[4];
     const int n = blockIdx.x / P.H, h = blockIdx.x % P.H, group = h / heads, hh = h % heads;
     const int64_t head = static_cast<int64_t>(n) * P.H + h, out = n * P.o.stride + h * P.o.head_stride;
+    const int t = threadIdx.x % T, q = threadIdx.x / T, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int col = blockIdx.y * COLS + 4 * t;
     const Parts parts(P, group, groups, heads);
-    const bool empty = P.pages.rows(P.lengths[n]) == 0;
-    int2 span = int2{0, 0};
-    if (!empty) {
+    int2 span = int2{0, -1};
+    if (P.pages.rows(P.lengths[n]) > 0) {
         span = parts.span[n];
         if (span.x == span.y) return;
     }
     // part i of the sequence: slot 2 w + 1 of its first workgroup, slots 2 w of the others
     auto slot = [&](int i) { return (2 * static_cast<int64_t>(span.x + i) + (i == 0)) * heads + hh; };
-    const int count = empty ? 0 : span.y - span.x + 1;
-    float top = neg_inf(), sum = 0.f;
-    for (int i = 0; i < count; ++i) top = fmaxf(top, parts.lse[slot(i)]);
-    const float at = top == neg_inf() ? 0.f : top;
-    for (int i = 0; i < count; ++i) sum += exp2_f((parts.lse[slot(i)] - at) * kLog2e);
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    for (int d = 4 * threadIdx.x; d < P.dl; d += 512) {
-        f4 x = {0, 0, 0, 0};
-        for (int i = 0; i < count; ++i)
-            x += *reinterpret_cast<const f4 *>(parts.o + slot(i) * P.dl + d) * (exp2_f((parts.lse[slot(i)] - at) * kLog2e) * inv);
-        store4(P.o.p, out + d, P.out_bf16, x[0], x[1], x[2], x[3]);
+    const int count = min(span.y - span.x + 1, kJoinParts);
+    float lse[2], top = neg_inf(), sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const int i = threadIdx.x + 256 * k;
+        lse[k] = i < count ? parts.lse[slot(i)] : neg_inf();
+        top = fmaxf(top, lse[k]);
     }
-    if (threadIdx.x == 0 && P.lse) P.lse[head] = sum == 0.f ? neg_inf() : at + __log2f(sum) * kLn2;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) top = fmaxf(top, __shfl_xor(top, d));
+    if (lane == 0) stats[wave].x = top;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) top = fmaxf(top, stats[i].x);
+    const float at = top == neg_inf() ? 0.f : top;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const float w = exp2_f((lse[k] - at) * kLog2e);
+        weight[threadIdx.x + 256 * k] = w;
+        sum += w;
+    }
+    sum = wave_sum(sum);
+    if (lane == 0) stats[wave].y = sum;
+    __syncthreads();
+    sum = (stats[0].y + stats[1].y) + (stats[2].y + stats[3].y);
+    f4 x = {0, 0, 0, 0};
+    if (col < P.dl) {
+#pragma unroll 4
+        for (int i = q; i < count; i += Q) x += *reinterpret_cast<const f4 *>(parts.o + slot(i) * P.dl + col) * weight[i];
+    }
+    sums[q][t] = x;
+    __syncthreads();
+    if (q == 0 && col < P.dl) {
+#pragma unroll
+        for (int i = 1; i < Q; ++i) x += sums[i][t];
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        store4(P.o.p, out + col, P.out_bf16, x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
+    }
+    if (threadIdx.x == 0 && blockIdx.y == 0 && P.lse) P.lse[head] = sum == 0.f ? neg_inf() : at + __log2f(sum) * kLn2;
 }
 
 // Tiles of 16 heads per workgroup, and groups of so many heads.
@@ -376,7 +410,7 @@ void launch_heads(const LatentStepLaunch &P) {
 int latent_step_splits(int N, int H, int dl, int64_t longest, bool bf16) {
     const int groups = head_groups(H, bf16), tiles = head_tiles(H, bf16);
     if (N >= 1024) return 0;
-    int64_t s = (tiles == 4 ? 256 : 512) / groups;
+    int64_t s = (tiles == 4 ? 256 : kJoinParts) / groups;
     const int64_t most = static_cast<int64_t>(N) * ((longest + 31) / 32);
     s = s < most ? s : most;
     return s < 1 ? 1 : static_cast<int>(s);
@@ -386,15 +420,21 @@ size_t latent_step_workspace_bytes(int N, int H, int dl, int splits, bool bf16) 
     return splits == 0 ? 0 : groups * 2 * splits * heads * (static_cast<size_t>(dl) + 1) * 4 + groups * N * sizeof(int2);
 }
 int64_t latent_step_threads(int N, int H, bool bf16, int splits) {
-    const int64_t step = static_cast<int64_t>(splits ? splits : N) * head_groups(H, bf16) * 512, join = static_cast<int64_t>(N) * H * 128;
+    const int64_t step = static_cast<int64_t>(splits ? splits : N) * head_groups(H, bf16) * 512, join = static_cast<int64_t>(N) * H * 256;
     return step > join ? step : join;
 }
 
 hipError_t launch_latent_step(const LatentStepLaunch &P) {
     if (P.bf16) launch_heads<uint16_t>(P);
     else launch_heads<float>(P);
-    if (P.splits)
-        latent_join_kernel<<<static_cast<unsigned>(P.N * static_cast<int64_t>(P.H)), 128, 0, P.stream>>>(P, 16 * head_tiles(P.H, P.bf16), head_groups(P.H, P.bf16));
+    if (P.splits) {
+        const int64_t rows = P.N * static_cast<int64_t>(P.H);
+        const int heads = 16 * head_tiles(P.H, P.bf16), groups = head_groups(P.H, P.bf16);
+        // All columns at once where there are rows enough for every CU (64 sequences of 32 heads JOIN_A), a quarter where a few rows
+        // have many parts (one sequence of 65,536 rows JOIN_B).
+        if (rows >= 512) latent_join_kernel<512><<<static_cast<unsigned>(rows), 256, 0, P.stream>>>(P, heads, groups);
+        else latent_join_kernel<128><<<dim3(static_cast<unsigned>(rows), (P.dl + 127) / 128), 256, 0, P.stream>>>(P, heads, groups);
+    }
     return hipGetLastError();
 }
 
