@@ -19,7 +19,7 @@ __global__ __launch_bounds__(256, 2) void attend_fwd_kernel(const AttendLaunch P
     constexpr int OR = BN * KT::ROW, OV = OR + BN * RT::ROW, BUF = OV + BN * VT::ROW;
     __shared__ __attribute__((aligned(1024))) char lds[2 * BUF];
 
-    const Place w = place_of(P, P.q_seq);
+    const Place w = place_of<true>(P, blockIdx.x);
     if (!w.valid || w.at >= w.nq) return;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int shift = w.nk - w.nq;              // query i sees keys up to i + shift
@@ -138,13 +138,15 @@ void launch(const AttendLaunch &P, unsigned grid) {
 }  // namespace
 
 hipError_t launch_attend_fwd(const AttendLaunch &P) {
+    if (!P.bf16) {
+        launch_attend_fwd_fp32(P);
+        return hipGetLastError();
+    }
     AttendLaunch L = P;
-    L.q_seq.L = 128;
-    const int64_t grid = (L.q_seq.cu ? L.q_seq.slots() : L.q_seq.N * static_cast<int64_t>(L.q_seq.per_seq())) * P.H;
-    const bool small = P.dn <= 64 && P.dr <= 32 && P.dv <= 64;
-    const unsigned n = static_cast<unsigned>(grid);
-    if (P.bf16) small ? launch<uint16_t, 64, 32, 64>(L, n) : launch<uint16_t, 128, 64, 128>(L, n);
-    else small ? launch<float, 64, 32, 64>(L, n) : launch<float, 128, 64, 128>(L, n);
+    L.q_seq.L = kAttendTile;
+    const unsigned n = static_cast<unsigned>(tiles_of(L.q_seq) * P.H);
+    if (P.dn <= 64 && P.dr <= 32 && P.dv <= 64) launch<uint16_t, 64, 32, 64>(L, n);
+    else launch<uint16_t, 128, 64, 128>(L, n);
     return hipGetLastError();
 }
 

@@ -51,7 +51,7 @@ __global__ __launch_bounds__(256, 1) void attend_dkv_kernel(const AttendLaunch P
     constexpr int OR = BQ * NT::ROW, OV = OR + BQ * RT::ROW, OS = OV + BQ * VT::ROW, BUF = OS + 2 * BQ * 4;
     __shared__ __attribute__((aligned(1024))) char lds[2 * BUF];
 
-    const Place w = place_of(P, P.k_seq);
+    const Place w = place_of<false>(P, blockIdx.x);
     if (!w.valid || w.at >= w.nk) return;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int shift = w.nk - w.nq;
@@ -177,7 +177,7 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void attend_dq_kernel(
     constexpr int OR = BN * KT::ROW, OV = OR + BN * RT::ROW, BUF = OV + BN * VT::ROW;
     __shared__ __attribute__((aligned(1024))) char lds[2 * BUF];
 
-    const Place w = place_of(P, P.q_seq);
+    const Place w = place_of<true>(P, blockIdx.x);
     if (!w.valid || w.at >= w.nq) return;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int shift = w.nk - w.nq;
@@ -278,36 +278,38 @@ __global__ __launch_bounds__(256) void attend_rope_sum_kernel(const AttendLaunch
     store4(P.dkr.p, row * P.dkr.stride + c, P.grad_bf16, x[0], x[1], x[2], x[3]);
 }
 
-int64_t tiles_of(const SeqTiles &s) { return s.cu ? s.slots() : s.N * static_cast<int64_t>(s.per_seq()); }
-
-template <class E, int NP, int RP, int VP>
-void launch(AttendLaunch L) {
-    const int64_t rows_q = L.q_seq.rows() * L.H;
-    if (rows_q) attend_delta_kernel<E><<<static_cast<unsigned>((rows_q + 15) / 16), 256, 0, L.stream>>>(L);
-    if (L.k_seq.rows()) {
-        attend_dkv_kernel<E, NP, RP, VP><<<static_cast<unsigned>(tiles_of(L.k_seq) * L.H), 256, 0, L.stream>>>(L);
-        const int64_t n = L.k_seq.rows() * (L.dr / 4);
-        attend_rope_sum_kernel<<<static_cast<unsigned>((n + 255) / 256), 256, 0, L.stream>>>(L);
-    }
-    if (rows_q) attend_dq_kernel<E, NP, RP, VP><<<static_cast<unsigned>(tiles_of(L.q_seq) * L.H), 256, 0, L.stream>>>(L);
+template <int NP, int RP, int VP>
+void launch(const AttendLaunch &L, bool keys) {
+    if (keys) attend_dkv_kernel<uint16_t, NP, RP, VP><<<static_cast<unsigned>(tiles_of(L.k_seq) * L.H), 256, 0, L.stream>>>(L);
+    else attend_dq_kernel<uint16_t, NP, RP, VP><<<static_cast<unsigned>(tiles_of(L.q_seq) * L.H), 256, 0, L.stream>>>(L);
 }
 
 }  // namespace
 
 hipError_t launch_attend_bwd(const AttendLaunch &P) {
     AttendLaunch L = P;
-    L.q_seq.L = L.k_seq.L = 128;
+    L.q_seq.L = L.k_seq.L = kAttendTile;
     const bool small = P.dn <= 64 && P.dr <= 32 && P.dv <= 64;
-    if (P.bf16) small ? launch<uint16_t, 64, 32, 64>(L) : launch<uint16_t, 128, 64, 128>(L);
-    else small ? launch<float, 64, 32, 64>(L) : launch<float, 128, 64, 128>(L);
+    const int64_t rows_q = L.q_seq.rows() * L.H, rope = L.k_seq.rows() * (L.dr / 4);
+    if (rows_q) {
+        const unsigned n = static_cast<unsigned>((rows_q + 15) / 16);
+        if (P.bf16) attend_delta_kernel<uint16_t><<<n, 256, 0, L.stream>>>(L);
+        else attend_delta_kernel<float><<<n, 256, 0, L.stream>>>(L);
+    }
+    if (!P.bf16) launch_attend_grads_fp32(P);
+    if (rope) {
+        if (P.bf16) small ? launch<64, 32, 64>(L, true) : launch<128, 64, 128>(L, true);
+        attend_rope_sum_kernel<<<static_cast<unsigned>((rope + 255) / 256), 256, 0, L.stream>>>(L);
+    }
+    if (rows_q && P.bf16) small ? launch<64, 32, 64>(L, false) : launch<128, 64, 128>(L, false);
     return hipGetLastError();
 }
 
 // Of the largest launch.
-int64_t attend_threads(const SeqTiles &q_, const SeqTiles &k_, int H, int dr, bool backward) {
+int64_t attend_threads(const SeqTiles &q_, const SeqTiles &k_, int H, int dr, bool bf16, bool backward) {
     SeqTiles q = q_, k = k_;
-    q.L = k.L = 128;
-    int64_t n = tiles_of(q) * H * 256;
+    q.L = k.L = bf16 ? kAttendTile : kAttendTileF32;
+    int64_t n = (tiles_of(q) + (backward && !bf16 ? tiles_of(k) : 0)) * H * 256;
     if (backward) {
         const int64_t parts[] = {tiles_of(k) * H * 256, (q.rows() * H + 15) / 16 * 256, (k.rows() * (dr / 4) + 255) / 256 * 256};
         for (const int64_t p : parts) n = p > n ? p : n;

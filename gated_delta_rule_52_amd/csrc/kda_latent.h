@@ -75,9 +75,14 @@ struct AttendLaunch {
     float *delta;     // [rows_q, H]
     float *dkr_part;  // [rows_k, H, dr]
 };
+// Rows per workgroup: bf16 and fp32.
+constexpr int kAttendTile = 128, kAttendTileF32 = 32;
+inline int64_t tiles_of(const SeqTiles &s) { return s.cu ? s.slots() : s.N * static_cast<int64_t>(s.per_seq()); }
 hipError_t launch_attend_fwd(const AttendLaunch &P);
 hipError_t launch_attend_bwd(const AttendLaunch &P);
-int64_t attend_threads(const SeqTiles &q, const SeqTiles &k, int H, int dr, bool backward);
+int64_t attend_threads(const SeqTiles &q, const SeqTiles &k, int H, int dr, bool bf16, bool backward);
+void launch_attend_fwd_fp32(const AttendLaunch &P);
+void launch_attend_grads_fp32(const AttendLaunch &P);
 
 // ---- device side ---------------------------------------------------------------------------------------
 
@@ -299,12 +304,13 @@ struct Place {
     bool valid;
 };
 // Workgroups go round-robin over the 8 XCDs: heads (of sequences, where they have equal lengths) are dealt to the XCDs
-// whole where their number allows, so that an L2 fetches a head's keys once.  A head's last tiles, which see the most keys,
-// start first.
-__device__ __forceinline__ Place place_of(const AttendLaunch &P, const SeqTiles &tiled) {
+// whole where their number allows, so that an L2 fetches a head's keys once.  The tiles that meet the most start first: a
+// head's last queries, its first keys.
+template <bool QUERIES>
+__device__ __forceinline__ Place place_of(const AttendLaunch &P, int64_t id) {
+    const SeqTiles &tiled = QUERIES ? P.q_seq : P.k_seq;
     const int64_t per = tiled.cu ? tiled.slots() : tiled.per_seq();
     const int64_t groups = static_cast<int64_t>(P.H) * (tiled.cu ? 1 : tiled.N);
-    const int64_t id = blockIdx.x;
     int64_t group, k;
     if (groups % 8 == 0) {
         const int64_t r = id >> 3;
@@ -314,7 +320,7 @@ __device__ __forceinline__ Place place_of(const AttendLaunch &P, const SeqTiles 
         group = id / per;
         k = id % per;
     }
-    k = per - 1 - k;
+    if (QUERIES) k = per - 1 - k;
     Place w;
     w.h = static_cast<int>(group % P.H);
     const Tile t = tile_at(tiled, (tiled.cu ? 0 : group / P.H * per) + k);

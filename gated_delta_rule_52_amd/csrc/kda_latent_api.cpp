@@ -269,7 +269,7 @@ kda_status kda_latent_attention_fwd(const kda_latent_attention_args *a) {
     if (!valid_dtype(a->out_dtype)) return fail(KDA_ERR_UNSUPPORTED, "out_dtype=%d", a->out_dtype);
     const AttendTensors<kda_latent_attention_args> t(a);
     kda::AttendLaunch L = attend_launch(a);
-    KDA_TRY(check_grid(kda::attend_threads(L.q_seq, L.k_seq, a->H, a->dr, false)));
+    KDA_TRY(check_grid(kda::attend_threads(L.q_seq, L.k_seq, a->H, a->dr, L.bf16, false)));
     if (t.rows_q == 0 || a->num_seqs == 0) return KDA_OK;
     if (!a->q || !a->o) return fail(KDA_ERR_NULL_POINTER, "q and o are required");
     if (t.rows_k > 0 && (!a->k || !a->k_rope || !a->v)) return fail(KDA_ERR_NULL_POINTER, "k, k_rope and v are required");
@@ -297,7 +297,7 @@ kda_status kda_latent_attention_bwd(const kda_latent_attention_bwd_args *a) {
     if (!valid_dtype(a->grad_dtype)) return fail(KDA_ERR_UNSUPPORTED, "grad_dtype=%d", a->grad_dtype);
     const AttendTensors<kda_latent_attention_bwd_args> t(a);
     kda::AttendLaunch L = attend_launch(a);
-    KDA_TRY(check_grid(kda::attend_threads(L.q_seq, L.k_seq, a->H, a->dr, true)));
+    KDA_TRY(check_grid(kda::attend_threads(L.q_seq, L.k_seq, a->H, a->dr, L.bf16, true)));
     if (t.rows_q + t.rows_k == 0 || a->num_seqs == 0) return KDA_OK;
     if (t.rows_q > 0 && (!a->q || !a->o || !a->lse || !a->grad_o || !a->grad_q))
         return fail(KDA_ERR_NULL_POINTER, "q, o, lse, grad_o and grad_q are required");
