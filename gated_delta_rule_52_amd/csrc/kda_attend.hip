@@ -13,9 +13,9 @@ template <class E, int NP, int RP, int VP>
 __global__ __launch_bounds__(256, 2) void attend_fwd_kernel(const AttendLaunch P) {
     constexpr int BN = sizeof(E) == 2 ? 64 : 32;  // keys per tile
     constexpr int SN = NP / (2 * Mx<E>::PER), SR = RP / (2 * Mx<E>::PER), ST = kSteps32<E>;
-    using KT = LdsTile<NP, E>;
-    using RT = LdsTile<RP, E>;
-    using VT = LdsTile<VP, E>;
+    using KT = LdsTile<NP, E, 32>;
+    using RT = LdsTile<RP, E, 32>;
+    using VT = LdsTile<VP, E, 32>;
     constexpr int OR = BN * KT::ROW, OV = OR + BN * RT::ROW, BUF = OV + BN * VT::ROW;
     __shared__ __attribute__((aligned(1024))) char lds[2 * BUF];
 
@@ -61,6 +61,7 @@ __global__ __launch_bounds__(256, 2) void attend_fwd_kernel(const AttendLaunch P
         const char *t = lds + buf * BUF;
         if (key0 + BN < keys) fetch(key0 + BN, lds + (buf ^ 1) * BUF);
         if (key0 >= wave_keys) continue;
+        __builtin_amdgcn_s_setprio(1);
         f16 s[BN / 32];
 #pragma unroll
         for (int b = 0; b < BN / 32; ++b) {
@@ -71,6 +72,7 @@ __global__ __launch_bounds__(256, 2) void attend_fwd_kernel(const AttendLaunch P
 #pragma unroll
             for (int k = 0; k < SR; ++k) s[b] = Mx<E>::mma32(RT::rows32(t + OR, 32 * b, k, lane), qf[SN + k], s[b]);
         }
+        __builtin_amdgcn_s_setprio(0);
         // a tile that some query of the wave sees only in part
         if (key0 + BN > w.nk || (P.causal && key0 + BN > q0 + shift + 1)) {
 #pragma unroll
@@ -114,20 +116,11 @@ __global__ __launch_bounds__(256, 2) void attend_fwd_kernel(const AttendLaunch P
             }
         }
     }
-    if (!live) return;
     l = halves_sum(l);
     const float by = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;  // NaN stays
-    const int64_t row = w.q_row + q;
-    if (P.lse && lane < 32) P.lse[row * P.H + w.h] = l == 0.f ? neg_inf() : (m + __log2f(l)) * kLn2;
-    const int64_t out = row * P.o.stride + w.h * P.o.head_stride;
-#pragma unroll
-    for (int c = 0; c < VP / 32; ++c)
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-            const int col = 32 * c + 8 * b + 4 * (lane >> 5);
-            if (col < P.dv)
-                store4(P.o.p, out + col, P.out_bf16, acc[c][4 * b] * by, acc[c][4 * b + 1] * by, acc[c][4 * b + 2] * by, acc[c][4 * b + 3] * by);
-        }
+    if (P.lse && live && lane < 32) P.lse[(w.q_row + q) * P.H + w.h] = l == 0.f ? neg_inf() : (m + __log2f(l)) * kLn2;
+    __syncthreads();  // LDS holds outputs now
+    store_rows<VP>(lds + wave * 32 * kStoreRow<VP>, acc, by, out_row(P.o, P.out_bf16, w.q_row + q0, w.h), P.out_bf16, P.o.stride, w.nq - q0, P.dv, lane);
 }
 
 template <class E, int NP, int RP, int VP>

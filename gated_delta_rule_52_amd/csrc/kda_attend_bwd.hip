@@ -13,7 +13,8 @@ namespace {
 
 using namespace la;
 
-// delta: 16 lanes per (row, head), 8 elements each (dv <= 128).
+// delta: 16 lanes per (row, head), 8 elements each (dv <= 128).  For bf16 also lse in powers of two, for rows that see nothing
+// as infinity, which leaves them no weights.
 template <class E>
 __global__ __launch_bounds__(256) void attend_delta_kernel(const AttendLaunch P) {
     const int64_t rows = P.q_seq.rows() * P.H, at = static_cast<int64_t>(blockIdx.x) * 16 + (threadIdx.x >> 4);
@@ -36,20 +37,29 @@ __global__ __launch_bounds__(256) void attend_delta_kernel(const AttendLaunch P)
     x += dpp_mov<0x4E>(x);
     x += dpp_mov<0x141>(x);
     x += dpp_mov<0x140>(x);
-    if ((threadIdx.x & 15) == 0) P.delta[at] = x;
+    if ((threadIdx.x & 15) == 0) {
+        P.delta[at] = x;
+        if constexpr (sizeof(E) == 2) {
+            const float l = P.lse[at];
+            P.lse2[at] = l == neg_inf() ? __builtin_inff() : l * kLog2e;
+        }
+    }
 }
 
 // A workgroup of four waves has 128 keys, 32 per wave, whose operands and gradients stay in registers (one wave per
-// SIMD), and walks the queries that see them.
-template <class E, int NP, int RP, int VP>
+// SIMD), and walks the queries that see them, 32 at a time.  Nothing but the wave itself can fill the time that its exponentials
+// take: they are woven into the products of the block before, which wait in three buffers' worth of LDS until then.
+template <int NP, int RP, int VP>
 __global__ __launch_bounds__(256, 1) void attend_dkv_kernel(const AttendLaunch P) {
-    constexpr int BQ = sizeof(E) == 2 ? 64 : 32;  // queries per tile
-    constexpr int SN = NP / (2 * Mx<E>::PER), SR = RP / (2 * Mx<E>::PER), SV = VP / (2 * Mx<E>::PER), ST = kSteps32<E>;
-    using NT = LdsTile<NP, E>;
-    using RT = LdsTile<RP, E>;
-    using VT = LdsTile<VP, E>;
+    typedef uint16_t E;
+    typedef Mx<E>::frag frag;
+    constexpr int BQ = 64;  // queries per tile
+    constexpr int SN = NP / 16, SR = RP / 16, SV = VP / 16, CN = NP / 32, CR = RP / 32, CV = VP / 32, C = CN + CR + CV;
+    using NT = LdsTile<NP, E, 32>;
+    using RT = LdsTile<RP, E, 32>;
+    using VT = LdsTile<VP, E, 32>;
     constexpr int OR = BQ * NT::ROW, OV = OR + BQ * RT::ROW, OS = OV + BQ * VT::ROW, BUF = OS + 2 * BQ * 4;
-    __shared__ __attribute__((aligned(1024))) char lds[2 * BUF];
+    __shared__ __attribute__((aligned(1024))) char lds[3 * BUF];
 
     const Place w = place_of<false>(P, blockIdx.x);
     if (!w.valid || w.at >= w.nk) return;
@@ -58,7 +68,7 @@ __global__ __launch_bounds__(256, 1) void attend_dkv_kernel(const AttendLaunch P
     const int k0 = w.at + 32 * wave, key = k0 + (lane & 31);
     const bool live = key < w.nk;
 
-    typename Mx<E>::frag kf[SN + SR], vf[SV];
+    frag kf[SN + SR], vf[SV];
     {
         const int64_t row = w.k_row + (live ? key : 0);
         const E *kp = head_row<E>(P.k, row, w.h), *rp = head_row<E>(P.kr, row, 0), *vp = head_row<E>(P.v, row, w.h);
@@ -70,110 +80,132 @@ __global__ __launch_bounds__(256, 1) void attend_dkv_kernel(const AttendLaunch P
         for (int s = 0; s < SV; ++s) vf[s] = row_operand<E>(vp, s, P.dv, live, lane);
     }
     const E *qp = head_row<E>(P.q, w.q_row, w.h), *gp = head_row<E>(P.go, w.q_row, w.h);
-    const float *lp = P.lse + w.q_row * P.H + w.h, *dp_ = P.delta + w.q_row * P.H + w.h;
-    auto fetch = [&](int at, char *to) {
+    const float *lp = P.lse2 + w.q_row * P.H + w.h, *ep = P.delta + w.q_row * P.H + w.h;
+    auto fetch = [&](int at, char *to, int lane) {
         const int rows = min(BQ, w.nq - at);
         const E *q = qp + at * P.q.stride;
         NT::template fill<BQ, 4>(to, rows_buffer(q, P.q.stride, rows, P.dn), P.q.stride * sizeof(E), P.dn * sizeof(E), wave, lane);
         RT::template fill<BQ, 4>(to + OR, rows_buffer(q + P.dn, P.q.stride, rows, P.dr), P.q.stride * sizeof(E), P.dr * sizeof(E), wave, lane);
         VT::template fill<BQ, 4>(to + OV, rows_buffer(gp + at * P.go.stride, P.go.stride, rows, P.dv), P.go.stride * sizeof(E), P.dv * sizeof(E), wave, lane);
-        if (wave < 2 && lane < BQ) {  // the rows' statistics, behind one another; zeros behind the last row
-            const rsrc_t r = rows_buffer((wave ? dp_ : lp) + at * static_cast<int64_t>(P.H), P.H, rows, 1);
+        if (wave < 2) {  // the rows' statistics, behind one another; zeros behind the last row, where q and grad_o are too
+            const rsrc_t r = rows_buffer((wave ? ep : lp) + at * static_cast<int64_t>(P.H), P.H, rows, 1);
             __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)(to + OS + wave * BQ * 4), 4, lane * P.H * 4, 0, 0, 0);
         }
     };
 
-    f16 dk[(NP + RP) / 32], dv[VP / 32];
+    f16 d[C];  // dk, its shared part, dv
 #pragma unroll
-    for (int c = 0; c < (NP + RP) / 32; ++c)
+    for (int c = 0; c < C; ++c)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) dk[c][i] = 0.f;
-#pragma unroll
-    for (int c = 0; c < VP / 32; ++c)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) dv[c][i] = 0.f;
+        for (int i = 0; i < 16; ++i) d[c][i] = 0.f;
     const float c2 = P.scale * kLog2e;
+
+    // One block's scores become its weights p (in s) and gradients ds (in dp), element by element.
+    auto stats = [&](const char *st, int r, f4 &lse, f4 &dl) {
+        lse = *reinterpret_cast<const f4 *>(st + 32 * r);
+        dl = *reinterpret_cast<const f4 *>(st + BQ * 4 + 32 * r);
+    };
+    auto element = [&](int i, int hidden, f16 &s, f16 &dp, const f4 &lse, const f4 &dl) {
+        const int r = 8 * (i >> 2) + (i & 3);
+        const float p = r < hidden ? 0.f : exp2_f(fmaf(s[i], c2, -lse[i & 3]));
+        s[i] = p;
+        dp[i] = p * (dp[i] - dl[i & 3]);
+    };
+    auto operand = [&](const char *t, int b, int i, int lane) {
+        const int k = i / C, c = i % C;
+        return c < CN ? NT::cols32(t, 32 * b, k, 32 * c, lane) : c < CN + CR ? RT::cols32(t + OR, 32 * b, k, 32 * (c - CN), lane)
+                                                                            : VT::cols32(t + OV, 32 * b, k, 32 * (c - CN - CR), lane);
+    };
 
     // the first query that sees the workgroup's first key
     const int first = P.causal ? max(0, w.at - shift) / BQ * BQ : 0;
-    if (first < w.nq) fetch(first, lds);
-    int buf = 0;
-    for (int at = first; at < w.nq; at += BQ, buf ^= 1) {
+    if (first < w.nq) fetch(first, lds, lane);
+    // the block before: its weights and gradients as operands, its tile, its block in it; at first zeros, which meet the
+    // first block itself
+    frag pf[2], df[2];
+    pf[0] = pf[1] = df[0] = df[1] = Mx<E>::zero();
+    const char *before = nullptr;
+    int before_b = 0, buf = 0;
+    for (int at = first; at < w.nq; at += BQ, buf = buf == 2 ? 0 : buf + 1) {
         loads_landed();
         const char *t = lds + buf * BUF;
-        if (at + BQ < w.nq) fetch(at + BQ, lds + (buf ^ 1) * BUF);
-#pragma unroll 1
+        const int lane_ = lane;
+        if (at + BQ < w.nq) fetch(at + BQ, lds + (buf == 2 ? 0 : buf + 1) * BUF, lane_);
+#pragma unroll
         for (int b = 0; b < BQ / 32; ++b) {
             const int q0 = at + 32 * b;
-            if (P.causal && q0 + 31 + shift < k0) continue;  // none of them sees the wave's keys
+            if (q0 >= w.nq || (P.causal && q0 + 31 + shift < k0)) continue;  // none of them sees the wave's keys
             f16 s, dp;
 #pragma unroll
             for (int i = 0; i < 16; ++i) s[i] = dp[i] = 0.f;
+            // the two products' steps alternate while both last: a step waits for the one before it in its own product
+            auto step = [](int i) {
+                constexpr int both = 2 * (SN + SR < SV ? SN + SR : SV);
+                return i < both ? i / 2 + (i % 2 ? SN + SR : 0) : SN + SR < SV ? i : i - SV;
+            };
+            pipelined<frag, SN + SR + SV, 6>(
+                [&](int j) {
+                    const int i = step(j);
+                    return i < SN ? NT::rows32(t, 32 * b, i, lane_) : i < SN + SR ? RT::rows32(t + OR, 32 * b, i - SN, lane_)
+                                                                                 : VT::rows32(t + OV, 32 * b, i - SN - SR, lane_);
+                },
+                [&](int j, frag f) {
+                    const int i = step(j);
+                    if (i < SN + SR) s = Mx<E>::mma32(f, kf[i], s);
+                    else dp = Mx<E>::mma32(f, vf[i - SN - SR], dp);
+                });
+            before_b = before ? before_b : b;
+            before = before ? before : t;
+            const char *st = t + OS + 128 * b + 16 * (lane_ >> 5);
+            // rows of the lane's half below this one do not see the lane's key
+            const int hidden = P.causal ? key - shift - q0 - 4 * (lane_ >> 5) : 0;
+            f4 lse[2], dl[2];
+            stats(st, 0, lse[0], dl[0]);
+            pipelined<frag, 2 * C, 4>([&](int i) { return operand(before, before_b, i, lane_); },
+                                      [&](int i, frag f) {
+                                          const int k = i / C, c = i % C;
+                                          d[c] = Mx<E>::mma32(f, c < CN + CR ? df[k] : pf[k], d[c]);
+                                          // the elements spread over the products
+                                          const int from = i * 16 / (2 * C), to = (i + 1) * 16 / (2 * C);
 #pragma unroll
-            for (int k = 0; k < SN; ++k) s = Mx<E>::mma32(NT::rows32(t, 32 * b, k, lane), kf[k], s);
+                                          for (int j = from; j < to; ++j) {
+                                              const int r = j >> 2;
+                                              if ((j & 3) == 0 && r < 3) stats(st, r + 1, lse[(r + 1) & 1], dl[(r + 1) & 1]);
+                                              element(j, hidden, s, dp, lse[r & 1], dl[r & 1]);
+                                          }
+                                      });
 #pragma unroll
-            for (int k = 0; k < SR; ++k) s = Mx<E>::mma32(RT::rows32(t + OR, 32 * b, k, lane), kf[SN + k], s);
-#pragma unroll
-            for (int k = 0; k < SV; ++k) dp = Mx<E>::mma32(VT::rows32(t + OV, 32 * b, k, lane), vf[k], dp);
-            const float *st = reinterpret_cast<const float *>(t + OS) + 32 * b + 4 * (lane >> 5);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const f4 lse = *reinterpret_cast<const f4 *>(st + 8 * r), dl = *reinterpret_cast<const f4 *>(st + BQ + 8 * r);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float p = exp2_f(fmaf(s[4 * r + i], c2, -lse[i] * kLog2e));
-                    if (P.causal && q0 + 8 * r + 4 * (lane >> 5) + i + shift < key) p = 0.f;
-                    s[4 * r + i] = p;
-                    dp[4 * r + i] = p * (dp[4 * r + i] - dl[i]);
-                }
-            }
-#pragma unroll
-            for (int k = 0; k < ST; ++k) {
-                const typename Mx<E>::frag pf = result_operand<E>(s, k), df = result_operand<E>(dp, k);
-#pragma unroll
-                for (int c = 0; c < VP / 32; ++c) dv[c] = Mx<E>::mma32(VT::cols32(t + OV, 32 * b, k, 32 * c, lane), pf, dv[c]);
-#pragma unroll
-                for (int c = 0; c < NP / 32; ++c) dk[c] = Mx<E>::mma32(NT::cols32(t, 32 * b, k, 32 * c, lane), df, dk[c]);
-#pragma unroll
-                for (int c = 0; c < RP / 32; ++c)
-                    dk[NP / 32 + c] = Mx<E>::mma32(RT::cols32(t + OR, 32 * b, k, 32 * c, lane), df, dk[NP / 32 + c]);
-            }
+            for (int k = 0; k < 2; ++k) pf[k] = result_operand<E>(s, k), df[k] = result_operand<E>(dp, k);
+            before = t;
+            before_b = b;
         }
     }
-    if (!live) return;
-    const int64_t row = w.k_row + key;
-    const int64_t dk_at = row * P.dk.stride + w.h * P.dk.head_stride, dv_at = row * P.dvg.stride + w.h * P.dvg.head_stride;
-    const int64_t part = (row * P.H + w.h) * P.dr;
-#pragma unroll
-    for (int b = 0; b < 4; ++b) {
-        const int col = 8 * b + 4 * (lane >> 5);
-#pragma unroll
-        for (int c = 0; c < NP / 32; ++c)
-            if (32 * c + col < P.dn)
-                store4(P.dk.p, dk_at + 32 * c + col, P.grad_bf16, dk[c][4 * b] * P.scale, dk[c][4 * b + 1] * P.scale,
-                       dk[c][4 * b + 2] * P.scale, dk[c][4 * b + 3] * P.scale);
-#pragma unroll
-        for (int c = 0; c < RP / 32; ++c)
-            if (32 * c + col < P.dr) {
-                const f16 &d = dk[NP / 32 + c];
-                store4(P.dkr_part, part + 32 * c + col, false, d[4 * b] * P.scale, d[4 * b + 1] * P.scale, d[4 * b + 2] * P.scale,
-                       d[4 * b + 3] * P.scale);
-            }
-#pragma unroll
-        for (int c = 0; c < VP / 32; ++c)
-            if (32 * c + col < P.dv)
-                store4(P.dvg.p, dv_at + 32 * c + col, P.grad_bf16, dv[c][4 * b], dv[c][4 * b + 1], dv[c][4 * b + 2], dv[c][4 * b + 3]);
-    }
+    if (before)
+        pipelined<frag, 2 * C, 4>([&](int i) { return operand(before, before_b, i, lane); },
+                                  [&](int i, frag f) {
+                                      const int k = i / C, c = i % C;
+                                      d[c] = Mx<E>::mma32(f, c < CN + CR ? df[k] : pf[k], d[c]);
+                                  });
+    __syncthreads();  // LDS holds outputs now
+    char *mine = lds + wave * 32 * kStoreRow<(NP > VP ? NP : VP)>;
+    const int64_t row = w.k_row + k0;
+    const int rows = w.nk - k0;
+    store_rows<NP>(mine, d, P.scale, out_row(P.dk, P.grad_bf16, row, w.h), P.grad_bf16, P.dk.stride, rows, P.dn, lane);
+    store_rows<VP>(mine, d + CN + CR, 1.f, out_row(P.dvg, P.grad_bf16, row, w.h), P.grad_bf16, P.dvg.stride, rows, P.dv, lane);
+    store_rows<RP>(mine, d + CN, P.scale, P.dkr_part + (row * P.H + w.h) * P.dr, false, static_cast<int64_t>(P.H) * P.dr, rows, P.dr, lane);
 }
 
-// As the forward pass: 128 queries per workgroup, 32 per wave, over the keys that they see.
-template <class E, int NP, int RP, int VP>
-__global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void attend_dq_kernel(const AttendLaunch P) {
-    constexpr int BN = sizeof(E) == 2 ? 64 : 32;
-    constexpr int SN = NP / (2 * Mx<E>::PER), SR = RP / (2 * Mx<E>::PER), SV = VP / (2 * Mx<E>::PER), ST = kSteps32<E>;
-    using KT = LdsTile<NP, E>;
-    using RT = LdsTile<RP, E>;
-    using VT = LdsTile<VP, E>;
+// As the forward pass: 128 queries per workgroup, 32 per wave, over the keys that they see.  Two workgroups share a CU: one's
+// exponentials hide behind the other's products, so its registers count; grad_o's operands are read from LDS each time.
+template <int NP, int RP, int VP>
+__global__ __launch_bounds__(256, 2) void attend_dq_kernel(const AttendLaunch P) {
+    typedef uint16_t E;
+    typedef Mx<E>::frag frag;
+    constexpr int BN = 64;  // keys per tile
+    constexpr int SN = NP / 16, SR = RP / 16, SV = VP / 16, CN = NP / 32, CR = RP / 32, C = CN + CR;
+    using KT = LdsTile<NP, E, 32>;
+    using RT = LdsTile<RP, E, 32>;
+    using VT = LdsTile<VP, E, 32>;
     constexpr int OR = BN * KT::ROW, OV = OR + BN * RT::ROW, BUF = OV + BN * VT::ROW;
     __shared__ __attribute__((aligned(1024))) char lds[2 * BUF];
 
@@ -188,80 +220,86 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void attend_dq_kernel(
     const int wave_keys = P.causal ? min(w.nk, min(q0 + 32, w.nq) + shift) : w.nk;
     const int limit = P.causal ? min(w.nk, q + shift + 1) : w.nk;
 
-    typename Mx<E>::frag qf[SN + SR], gf[SV];
-    const int64_t row = w.q_row + (live ? q : 0);
-    {
-        const E *qp = head_row<E>(P.q, row, w.h), *gp = head_row<E>(P.go, row, w.h);
-#pragma unroll
-        for (int s = 0; s < SN; ++s) qf[s] = row_operand<E>(qp, s, P.dn, live, lane);
-#pragma unroll
-        for (int s = 0; s < SR; ++s) qf[SN + s] = row_operand<E>(qp + P.dn, s, P.dr, live, lane);
-#pragma unroll
-        for (int s = 0; s < SV; ++s) gf[s] = row_operand<E>(gp, s, P.dv, live, lane);
-    }
-    const float lse = P.lse[row * P.H + w.h] * kLog2e, delta = P.delta[row * P.H + w.h];
     const E *kp = head_row<E>(P.k, w.k_row, w.h), *rp = head_row<E>(P.kr, w.k_row, 0), *vp = head_row<E>(P.v, w.k_row, w.h);
-    auto fetch = [&](int key0, char *to) {
+    auto fetch = [&](int key0, char *to, int lane) {
         const int rows = min(BN, w.nk - key0);
         KT::template fill<BN, 4>(to, rows_buffer(kp + key0 * P.k.stride, P.k.stride, rows, P.dn), P.k.stride * sizeof(E), P.dn * sizeof(E), wave, lane);
         RT::template fill<BN, 4>(to + OR, rows_buffer(rp + key0 * P.kr.stride, P.kr.stride, rows, P.dr), P.kr.stride * sizeof(E), P.dr * sizeof(E), wave, lane);
         VT::template fill<BN, 4>(to + OV, rows_buffer(vp + key0 * P.v.stride, P.v.stride, rows, P.dv), P.v.stride * sizeof(E), P.dv * sizeof(E), wave, lane);
     };
+    if (keys > 0) fetch(0, lds, lane);
 
-    f16 dq[(NP + RP) / 32];
+    frag qf[SN + SR], gf[SV];
+    const int64_t row = w.q_row + (live ? q : 0);
+    const E *qp = head_row<E>(P.q, row, w.h);
 #pragma unroll
-    for (int c = 0; c < (NP + RP) / 32; ++c)
+    for (int s = 0; s < SN; ++s) qf[s] = row_operand<E>(qp, s, P.dn, live, lane);
+#pragma unroll
+    for (int s = 0; s < SR; ++s) qf[SN + s] = row_operand<E>(qp + P.dn, s, P.dr, live, lane);
+    const E *gp = head_row<E>(P.go, row, w.h);
+#pragma unroll
+    for (int s = 0; s < SV; ++s) gf[s] = row_operand<E>(gp, s, P.dv, live, lane);
+    const float lse = P.lse2[row * P.H + w.h], delta = P.delta[row * P.H + w.h];
+    f16 dq[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c)
 #pragma unroll
         for (int i = 0; i < 16; ++i) dq[c][i] = 0.f;
     const float c2 = P.scale * kLog2e;
 
-    if (keys > 0) fetch(0, lds);
     int buf = 0;
     for (int key0 = 0; key0 < keys; key0 += BN, buf ^= 1) {
         loads_landed();
         const char *t = lds + buf * BUF;
-        if (key0 + BN < keys) fetch(key0 + BN, lds + (buf ^ 1) * BUF);
+        if (key0 + BN < keys) fetch(key0 + BN, lds + (buf ^ 1) * BUF, afresh(lane));
 #pragma unroll 1
         for (int b = 0; b < BN / 32; ++b) {
             const int kb = key0 + 32 * b;
             if (kb >= wave_keys) break;
+            const int lane_ = afresh(lane);
             f16 s, dp;
 #pragma unroll
             for (int i = 0; i < 16; ++i) s[i] = dp[i] = 0.f;
+            __builtin_amdgcn_s_setprio(1);
+            auto row_step = [](int i) {
+                constexpr int both = 2 * (SN + SR < SV ? SN + SR : SV);
+                return i < both ? i / 2 + (i % 2 ? SN + SR : 0) : SN + SR < SV ? i : i - SV;
+            };
+            pipelined<frag, SN + SR + SV, 4>(
+                [&](int j) {
+                    const int i = row_step(j);
+                    return i < SN ? KT::rows32(t, 32 * b, i, lane_) : i < SN + SR ? RT::rows32(t + OR, 32 * b, i - SN, lane_) : VT::rows32(t + OV, 32 * b, i - SN - SR, lane_);
+                },
+                [&](int j, frag f) {
+                    const int i = row_step(j);
+                    if (i < SN + SR) s = Mx<E>::mma32(f, qf[i], s);
+                    else dp = Mx<E>::mma32(f, gf[i - SN - SR], dp);
+                });
+            __builtin_amdgcn_s_setprio(0);
+            const bool part = kb + 32 > w.nk || (P.causal && kb + 32 > q0 + shift + 1);  // some query does not see some key
+            if (part) {
 #pragma unroll
-            for (int k = 0; k < SN; ++k) s = Mx<E>::mma32(KT::rows32(t, 32 * b, k, lane), qf[k], s);
-#pragma unroll
-            for (int k = 0; k < SR; ++k) s = Mx<E>::mma32(RT::rows32(t + OR, 32 * b, k, lane), qf[SN + k], s);
-#pragma unroll
-            for (int k = 0; k < SV; ++k) dp = Mx<E>::mma32(VT::rows32(t + OV, 32 * b, k, lane), gf[k], dp);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                float p = exp2_f(fmaf(s[i], c2, -lse));
-                if (kb + 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3) >= limit) p = 0.f;
-                dp[i] = p * (dp[i] - delta);
+                for (int i = 0; i < 16; ++i)
+                    if (kb + 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3) >= limit) s[i] = neg_inf();
             }
 #pragma unroll
-            for (int k = 0; k < ST; ++k) {
-                const typename Mx<E>::frag df = result_operand<E>(dp, k);
-#pragma unroll
-                for (int c = 0; c < NP / 32; ++c) dq[c] = Mx<E>::mma32(KT::cols32(t, 32 * b, k, 32 * c, lane), df, dq[c]);
-#pragma unroll
-                for (int c = 0; c < RP / 32; ++c)
-                    dq[NP / 32 + c] = Mx<E>::mma32(RT::cols32(t + OR, 32 * b, k, 32 * c, lane), df, dq[NP / 32 + c]);
-            }
+            for (int i = 0; i < 16; ++i) dp[i] = exp2_f(fmaf(s[i], c2, -lse)) * (dp[i] - delta);
+            const frag df[2] = {result_operand<E>(dp, 0), result_operand<E>(dp, 1)};
+            __builtin_amdgcn_s_setprio(1);
+            pipelined<frag, 2 * C, 3>(
+                [&](int i) {
+                    const int k = i / C, c = i % C;
+                    return c < CN ? KT::cols32(t, 32 * b, k, 32 * c, lane_) : RT::cols32(t + OR, 32 * b, k, 32 * (c - CN), lane_);
+                },
+                [&](int i, frag f) { dq[i % C] = Mx<E>::mma32(f, df[i / C], dq[i % C]); });
+            __builtin_amdgcn_s_setprio(0);
         }
     }
-    if (!live) return;
-    const int64_t out = row * P.dq.stride + w.h * P.dq.head_stride;
-#pragma unroll
-    for (int c = 0; c < (NP + RP) / 32; ++c)
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-            const int col = (c < NP / 32 ? 32 * c : 32 * c - NP) + 8 * b + 4 * (lane >> 5);
-            if (col < (c < NP / 32 ? P.dn : P.dr))
-                store4(P.dq.p, out + col + (c < NP / 32 ? 0 : P.dn), P.grad_bf16, dq[c][4 * b] * P.scale, dq[c][4 * b + 1] * P.scale,
-                       dq[c][4 * b + 2] * P.scale, dq[c][4 * b + 3] * P.scale);
-        }
+    __syncthreads();  // LDS holds outputs now
+    char *mine = lds + wave * 32 * kStoreRow<NP>;
+    char *to = static_cast<char *>(out_row(P.dq, P.grad_bf16, w.q_row + q0, w.h));
+    store_rows<NP>(mine, dq, P.scale, to, P.grad_bf16, P.dq.stride, w.nq - q0, P.dn, lane);
+    store_rows<RP>(mine, dq + CN, P.scale, to + P.dn * (P.grad_bf16 ? 2 : 4), P.grad_bf16, P.dq.stride, w.nq - q0, P.dr, lane);
 }
 
 // k_rope's gradient: the heads' parts in their order, four columns per thread.
@@ -280,8 +318,8 @@ __global__ __launch_bounds__(256) void attend_rope_sum_kernel(const AttendLaunch
 
 template <int NP, int RP, int VP>
 void launch(const AttendLaunch &L, bool keys) {
-    if (keys) attend_dkv_kernel<uint16_t, NP, RP, VP><<<static_cast<unsigned>(tiles_of(L.k_seq) * L.H), 256, 0, L.stream>>>(L);
-    else attend_dq_kernel<uint16_t, NP, RP, VP><<<static_cast<unsigned>(tiles_of(L.q_seq) * L.H), 256, 0, L.stream>>>(L);
+    if (keys) attend_dkv_kernel<NP, RP, VP><<<static_cast<unsigned>(tiles_of(L.k_seq) * L.H), 256, 0, L.stream>>>(L);
+    else attend_dq_kernel<NP, RP, VP><<<static_cast<unsigned>(tiles_of(L.q_seq) * L.H), 256, 0, L.stream>>>(L);
 }
 
 }  // namespace

@@ -73,6 +73,7 @@ struct AttendLaunch {
     Heads go, dq, dk, dkr, dvg;
     int grad_bf16;
     float *delta;     // [rows_q, H]
+    float *lse2;      // [rows_q, H], lse in powers of two (bf16)
     float *dkr_part;  // [rows_k, H, dr]
 };
 // Rows per workgroup: bf16 and fp32.
@@ -163,17 +164,19 @@ __device__ __forceinline__ s4 read_columns(const char *__restrict__ p) {
     return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4)p);
 }
 
-// Rows of W elements in LDS, in 16-byte units.  Unit u of row r lies at place u ^ swz(r): the four rows that a
-// transposing read takes 32 bytes of each, and the rows that an operand read takes 16 bytes of each, then lie in
-// different banks.  swz repeats after 8 rows.
-template <int W, class E>
+// Rows of W elements in LDS, in 16-byte units.  Unit u of row r lies at place u ^ swz(r), so that what LDS serves at once, 256
+// bytes, comes from all of its 64 banks: an operand read takes 16 bytes of 16 consecutive rows, and a transposing read 32
+// COLS bytes of consecutive rows, four of them for COLS = 32 and eight for COLS = 16.  swz repeats after 16 rows.  In long
+// rows the swap stays within 16 units: what lies beyond is a constant distance.
+template <int W, class E, int COLS>
 struct LdsTile {
     static constexpr int ROW = W * static_cast<int>(sizeof(E)), UNITS = ROW / 16;
     static_assert(UNITS >= 4 && (UNITS & (UNITS - 1)) == 0, "rows of 64 bytes or a power of two more");
     __device__ __forceinline__ static int swz(int row) {
-        return UNITS >= 16 ? (row & 7) << 1 : UNITS == 8 ? ((row >> 1) & 3) << 1 : ((row >> 2) & 1) << 1;
+        if (UNITS == 4) return (row >> 2) & 3;                                           // four rows in 256 bytes
+        if (UNITS == 8) return ((row >> 1) & 1) << 2 | ((row >> 2) & 3);                 // two
+        return COLS == 32 ? (row & 3) << 2 | ((row >> 2) & 3) : (row & 7) << 1 | ((row >> 3) & 1);
     }
-    // (in long rows the swap stays within 16 units: what lies beyond is a constant distance)
     __device__ __forceinline__ static int at(int row, int unit) {
         return row * ROW + (unit & ~15) * 16 + (((unit & 15) ^ swz(row)) << 4);
     }
@@ -210,7 +213,7 @@ struct LdsTile {
             const int unit = (col0 >> 3) | ((lane >> 3) & 2) | ((i >> 1) & 1);
             const char *p = lds + (i & 1) * 8;
             const s4 lo = read_columns(p + at(row, unit));
-            const s4 hi = read_columns(p + at(row, unit) + 8 * ROW);
+            const s4 hi = read_columns(p + at(row + 8, unit));
             return __builtin_bit_cast(b8, (__attribute__((ext_vector_type(8))) short){lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]});
         } else {
             const int col = col0 + (lane & 31);
@@ -291,6 +294,41 @@ __device__ __forceinline__ float quarters_sum(float x) {
 __device__ __forceinline__ void loads_landed() {
     __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
     __syncthreads();
+}
+
+// The rows of a wave's results: row lane % 32 has, in tile c, columns 32 c + 8 b + 4 (lane / 32) .. + 3 as elements 4 b .. + 3.
+// Rows of bf16 are put together in LDS (32 * kStoreRow<W> bytes of the wave's own) and leave 16 bytes per lane and whole rows at
+// a time: eight bytes from each of 64 places cost the gradients' key kernel STORE_A.  `to`: the wave's first row.
+template <int W>
+constexpr int kStoreRow = 2 * W + 16;
+template <int W>
+__device__ __forceinline__ void store_rows(char *lds, const f16 *x, float by, void *to, bool bf16, int64_t stride, int rows, int width, int lane) {
+    const int r = lane & 31, h = lane >> 5;
+    if (!bf16) {
+        if (r < rows)
+#pragma unroll
+            for (int c = 0; c < W / 32; ++c)
+#pragma unroll
+                for (int b = 0; b < 4; ++b)
+                    if (32 * c + 8 * b + 4 * h < width)
+                        store4(to, r * stride + 32 * c + 8 * b + 4 * h, false, x[c][4 * b] * by, x[c][4 * b + 1] * by, x[c][4 * b + 2] * by, x[c][4 * b + 3] * by);
+        return;
+    }
+#pragma unroll
+    for (int c = 0; c < W / 32; ++c)
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+            store4(lds + r * kStoreRow<W> + (32 * c + 8 * b + 4 * h) * 2, 0, true, x[c][4 * b] * by, x[c][4 * b + 1] * by, x[c][4 * b + 2] * by, x[c][4 * b + 3] * by);
+    constexpr int PER = 512 / W;  // rows at a time
+#pragma unroll
+    for (int i = 0; i < 32 / PER; ++i) {
+        const int row = PER * i + lane / (W / 8), col = lane % (W / 8) * 8;
+        const u4 v = *reinterpret_cast<const u4 *>(lds + row * kStoreRow<W> + col * 2);
+        if (row < rows && col < width) *reinterpret_cast<u4 *>(static_cast<uint16_t *>(to) + row * stride + col) = v;
+    }
+}
+__device__ __forceinline__ void *out_row(const Heads &t, bool bf16, int64_t row, int h) {
+    return static_cast<char *>(t.p) + (row * t.stride + h * t.head_stride) * (bf16 ? 2 : 4);
 }
 
 // ---- attention over expanded keys and values -------------------------------------------------------------

@@ -152,7 +152,7 @@ kda_status check_attend_tensor(const Tensor &t) {
 size_t delta_bytes(int64_t rows_q, int H) { return (static_cast<size_t>(rows_q) * H * 4 + 15) / 16 * 16; }
 template <class A>
 size_t attend_bwd_bytes(const A *a) {
-    return delta_bytes(static_cast<int64_t>(a->batch) * a->Tq, a->H) + static_cast<size_t>(a->batch) * a->Tk * a->H * a->dr * 4;
+    return (a->in_dtype == KDA_DTYPE_BF16 ? 2 : 1) * delta_bytes(static_cast<int64_t>(a->batch) * a->Tq, a->H) + static_cast<size_t>(a->batch) * a->Tk * a->H * a->dr * 4;
 }
 
 int step_splits(const kda_latent_step_args *a) {
@@ -326,7 +326,9 @@ kda_status kda_latent_attention_bwd(const kda_latent_attention_bwd_args *a) {
     L.go = heads_of(go); L.dq = heads_of(dq); L.dk = heads_of(dk); L.dkr = heads_of(dkr); L.dvg = heads_of(dv);
     L.grad_bf16 = g == KDA_DTYPE_BF16;
     L.delta = static_cast<float *>(a->workspace);
-    L.dkr_part = reinterpret_cast<float *>(static_cast<char *>(a->workspace) + delta_bytes(t.rows_q, a->H));
+    const size_t stats = delta_bytes(t.rows_q, a->H);
+    L.lse2 = reinterpret_cast<float *>(static_cast<char *>(a->workspace) + stats);
+    L.dkr_part = reinterpret_cast<float *>(static_cast<char *>(a->workspace) + (L.bf16 ? 2 : 1) * stats);
     return hip_status(kda::launch_attend_bwd(L), "kda_latent_attention_bwd launch");
 }
 

@@ -66,8 +66,8 @@ __global__ __launch_bounds__(64 * kWaves<HT>, sizeof(E) == 2 ? 2 : 1) void laten
     using S = Shape<E, HT>;
     constexpr int BN = S::BN, KG = S::KG, KPW = S::KPW, W = S::W;
     constexpr int KC = 4 * Mx<E>::PER, SL = DLP / KC, SR = kRopePad / KC, CT = DLP / (16 * W), ST = BN / KC;
-    using LT = LdsTile<DLP, E>;
-    using RT = LdsTile<kRopePad, E>;
+    using LT = LdsTile<DLP, E, 16>;
+    using RT = LdsTile<kRopePad, E, 16>;
     constexpr int OR = BN * LT::ROW, OM = OR + BN * RT::ROW, BUF = OM + BN * 4;
     constexpr int RPW = BN / W;                // rows that a wave fetches
     constexpr int AUX = sizeof(E) == 2 && HT <= 2 ? 2 : 0;  // rows that one workgroup reads once pass the caches by (non-temporal)

@@ -127,7 +127,8 @@ def test_workspace_queries():
         assert 0 < _lib.layer_raw(name, make()) < 1 << 30
         assert _lib.layer_raw(name, make(H=0)) == 2 ** 64 - 1
     # the rows' statistics and the heads' parts of the shared key's gradient
-    assert _lib.layer_raw("kda_latent_attention_bwd_workspace_bytes", attend_bwd()) == 2 * 50 * 4 * 4 + 2 * 60 * 4 * 64 * 4
+    for dtype, stats in ((BF16, 2), (FP32, 1)):
+        assert _lib.layer_raw("kda_latent_attention_bwd_workspace_bytes", attend_bwd(in_dtype=dtype)) == stats * 2 * 50 * 4 * 4 + 2 * 60 * 4 * 64 * 4
 
 
 def test_slices_of_one_buffer_may_interleave():
