@@ -55,7 +55,7 @@ struct LatentStepLaunch {
     float *ws;
     hipStream_t stream;
 };
-int latent_step_splits(int N, int H, int dl, int64_t longest, bool bf16);
+int latent_step_splits(int N, int H, int64_t longest, bool bf16);
 size_t latent_step_workspace_bytes(int N, int H, int dl, int splits, bool bf16);
 hipError_t launch_latent_step(const LatentStepLaunch &P);
 int64_t latent_step_threads(int N, int H, bool bf16, int splits);
@@ -98,6 +98,7 @@ typedef unsigned u4 __attribute__((ext_vector_type(4)));
 typedef unsigned u2 __attribute__((ext_vector_type(2)));
 typedef __amdgpu_buffer_rsrc_t rsrc_t;
 typedef __attribute__((address_space(3))) void *lds_ptr;
+typedef __attribute__((address_space(1))) void *glb_ptr;
 typedef __attribute__((address_space(3))) s4 *lds_s4;
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -290,9 +291,11 @@ __device__ __forceinline__ float quarters_sum(float x) {
     return halves_sum(__uint_as_float(r[0]) + __uint_as_float(r[1]));
 }
 
-// All of the wave's loads into LDS have arrived, and every wave is here.
+// All of the wave's loads have arrived.
+__device__ __forceinline__ void loads_done() { __builtin_amdgcn_s_waitcnt(0x0f70); }  // vmcnt(0)
+// Those into LDS too, and every wave is here.
 __device__ __forceinline__ void loads_landed() {
-    __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
+    loads_done();
     __syncthreads();
 }
 

@@ -156,7 +156,7 @@ size_t attend_bwd_bytes(const A *a) {
 }
 
 int step_splits(const kda_latent_step_args *a) {
-    return kda::latent_step_splits(a->N, a->H, a->dl, static_cast<int64_t>(a->max_blocks) * a->page, a->in_dtype == KDA_DTYPE_BF16);
+    return kda::latent_step_splits(a->N, a->H, static_cast<int64_t>(a->max_blocks) * a->page, a->in_dtype == KDA_DTYPE_BF16);
 }
 kda_status check_step_sizes(const kda_latent_step_args *a) {
     KDA_TRY(check_struct(a));

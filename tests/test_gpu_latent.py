@@ -335,6 +335,18 @@ def test_step_over_sizes(kda, dtype, dl, dr):
     check_step(kda, 91, [33, 150], 40, dl, dr, 5, dtype, layout="sliced", wider=3)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("N,longest,H,page", [(1100, 40, 4, 16), (1024, 130, 33, 5), (1500, 2100, 4, 64), (700, 70, 20, 16), (513, 2, 40, 1), (1023, 33, 17, 64)])
+def test_step_of_many_sequences(kda, dtype, N, longest, H, page):
+    """A workgroup per sequence, and runs of tiles that pass over several sequences, some without rows."""
+    r = np.random.default_rng(N)
+    lengths = r.integers(0, min(longest, 100) + 1, N) * (r.random(N) < 0.8)
+    lengths[r.integers(N)] = longest
+    lengths[-3:] = 0, 1, 0
+    lengths[:2] = 0, -3
+    check_step(kda, 96, [int(n) for n in lengths], H, 64, 16, page, dtype)
+
+
 def test_step_layouts_types_and_large_scores(kda):
     check_step(kda, 92, [100, 40], 16, 512, 64, 16, "bf16", out="fp32", layout="heads")
     check_step(kda, 93, [100, 40], 16, 512, 64, 16, "fp32", out="bf16", layout="heads")
