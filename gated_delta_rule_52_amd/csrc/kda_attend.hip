@@ -9,10 +9,22 @@ namespace {
 
 using namespace la;
 
-template <class E, int NP, int RP, int VP>
+// A workgroup has 128 queries, 32 per wave, and walks the keys that its last query sees, 64 at a time: q's operands, the scores of
+// a tile and the output's sums stay in registers, keys and values come through two buffers in LDS (80 KiB at the full head sizes: two
+// workgroups per CU, so that one's exponentials hide behind the other's products).  Scores are formed transposed, keys down and
+// queries across: a lane then has 32 scores of one query, its maximum and sum need one exchange between the wave's halves, and
+// the weights are the next product's operand as they lie.
+//
+// The matrix unit bounds it: 8,192 rows of 32 heads, causal, 128 + 64 and 128 wide (687 GFLOP), take 670 us, 1.03 PFLOP/s, and
+// 16,384 rows of 16 heads 1,226 us, 1.12 PFLOP/s, where the same instructions with nothing beside them reach 1.7 to 1.9; what is
+// between is exponentials that meet no other wave's products.  Waves that are at the scores' products go first (s_setprio): the
+// first of these took 694 us without and 658 with, before rows were stored whole.
+template <int NP, int RP, int VP>
 __global__ __launch_bounds__(256, 2) void attend_fwd_kernel(const AttendLaunch P) {
-    constexpr int BN = sizeof(E) == 2 ? 64 : 32;  // keys per tile
-    constexpr int SN = NP / (2 * Mx<E>::PER), SR = RP / (2 * Mx<E>::PER), ST = kSteps32<E>;
+    typedef uint16_t E;
+    typedef Mx<E>::frag frag;
+    constexpr int BN = 64;  // keys per tile
+    constexpr int SN = NP / 16, SR = RP / 16;
     using KT = LdsTile<NP, E, 32>;
     using RT = LdsTile<RP, E, 32>;
     using VT = LdsTile<VP, E, 32>;
@@ -30,7 +42,7 @@ __global__ __launch_bounds__(256, 2) void attend_fwd_kernel(const AttendLaunch P
     const int wave_keys = P.causal ? min(w.nk, min(q0 + 32, w.nq) + shift) : w.nk;
     const int limit = P.causal ? min(w.nk, q + shift + 1) : w.nk;  // the lane's query sees keys below it
 
-    typename Mx<E>::frag qf[SN + SR];
+    frag qf[SN + SR];
     {
         const E *row = head_row<E>(P.q, w.q_row + (live ? q : 0), w.h);
 #pragma unroll
@@ -108,8 +120,8 @@ __global__ __launch_bounds__(256, 2) void attend_fwd_kernel(const AttendLaunch P
                 l += s[b][i];
             }
 #pragma unroll
-            for (int k = 0; k < ST; ++k) {
-                const typename Mx<E>::frag p = result_operand<E>(s[b], k);
+            for (int k = 0; k < 2; ++k) {
+                const frag p = result_operand(s[b], k);
 #pragma unroll
                 for (int c = 0; c < VP / 32; ++c)
                     acc[c] = Mx<E>::mma32(VT::cols32(t + OV, 32 * b, k, 32 * c, lane), p, acc[c]);
@@ -123,11 +135,6 @@ __global__ __launch_bounds__(256, 2) void attend_fwd_kernel(const AttendLaunch P
     store_rows<VP>(lds + wave * 32 * kStoreRow<VP>, acc, by, out_row(P.o, P.out_bf16, w.q_row + q0, w.h), P.out_bf16, P.o.stride, w.nq - q0, P.dv, lane);
 }
 
-template <class E, int NP, int RP, int VP>
-void launch(const AttendLaunch &P, unsigned grid) {
-    attend_fwd_kernel<E, NP, RP, VP><<<grid, 256, 0, P.stream>>>(P);
-}
-
 }  // namespace
 
 hipError_t launch_attend_fwd(const AttendLaunch &P) {
@@ -138,8 +145,9 @@ hipError_t launch_attend_fwd(const AttendLaunch &P) {
     AttendLaunch L = P;
     L.q_seq.L = kAttendTile;
     const unsigned n = static_cast<unsigned>(tiles_of(L.q_seq) * P.H);
-    if (P.dn <= 64 && P.dr <= 32 && P.dv <= 64) launch<uint16_t, 64, 32, 64>(L, n);
-    else launch<uint16_t, 128, 64, 128>(L, n);
+    // Heads are padded with zeros to one of two sizes (2,048 rows of 32 heads of 64 + 32 and 64: 49 us, padded to the larger one 69).
+    if (P.dn <= 64 && P.dr <= 32 && P.dv <= 64) attend_fwd_kernel<64, 32, 64><<<n, 256, 0, P.stream>>>(L);
+    else attend_fwd_kernel<128, 64, 128><<<n, 256, 0, P.stream>>>(L);
     return hipGetLastError();
 }
 

@@ -48,7 +48,10 @@ __global__ __launch_bounds__(256) void attend_delta_kernel(const AttendLaunch P)
 
 // A workgroup of four waves has 128 keys, 32 per wave, whose operands and gradients stay in registers (one wave per
 // SIMD), and walks the queries that see them, 32 at a time.  Nothing but the wave itself can fill the time that its exponentials
-// take: they are woven into the products of the block before, which wait in three buffers' worth of LDS until then.
+// take: they are woven into the products of the block before, which wait in three buffers' worth of LDS until then (2
+// sequences of 4,096 rows of 32 heads, 687 GFLOP: 790 us, 0.87 PFLOP/s, against 816 one after the other).  What is left beside the
+// products is theirs to wait for: LDS delivers an operand per product, and the same kernel without those reads takes 623 us, without
+// the next tile's loads 723, without the exponentials 715.
 template <int NP, int RP, int VP>
 __global__ __launch_bounds__(256, 1) void attend_dkv_kernel(const AttendLaunch P) {
     typedef uint16_t E;
@@ -129,8 +132,7 @@ __global__ __launch_bounds__(256, 1) void attend_dkv_kernel(const AttendLaunch P
     for (int at = first; at < w.nq; at += BQ, buf = buf == 2 ? 0 : buf + 1) {
         loads_landed();
         const char *t = lds + buf * BUF;
-        const int lane_ = lane;
-        if (at + BQ < w.nq) fetch(at + BQ, lds + (buf == 2 ? 0 : buf + 1) * BUF, lane_);
+        if (at + BQ < w.nq) fetch(at + BQ, lds + (buf == 2 ? 0 : buf + 1) * BUF, lane);
 #pragma unroll
         for (int b = 0; b < BQ / 32; ++b) {
             const int q0 = at + 32 * b;
@@ -146,8 +148,8 @@ __global__ __launch_bounds__(256, 1) void attend_dkv_kernel(const AttendLaunch P
             pipelined<frag, SN + SR + SV, 6>(
                 [&](int j) {
                     const int i = step(j);
-                    return i < SN ? NT::rows32(t, 32 * b, i, lane_) : i < SN + SR ? RT::rows32(t + OR, 32 * b, i - SN, lane_)
-                                                                                 : VT::rows32(t + OV, 32 * b, i - SN - SR, lane_);
+                    return i < SN ? NT::rows32(t, 32 * b, i, lane) : i < SN + SR ? RT::rows32(t + OR, 32 * b, i - SN, lane)
+                                                                                 : VT::rows32(t + OV, 32 * b, i - SN - SR, lane);
                 },
                 [&](int j, frag f) {
                     const int i = step(j);
@@ -156,12 +158,12 @@ __global__ __launch_bounds__(256, 1) void attend_dkv_kernel(const AttendLaunch P
                 });
             before_b = before ? before_b : b;
             before = before ? before : t;
-            const char *st = t + OS + 128 * b + 16 * (lane_ >> 5);
+            const char *st = t + OS + 128 * b + 16 * (lane >> 5);
             // rows of the lane's half below this one do not see the lane's key
-            const int hidden = P.causal ? key - shift - q0 - 4 * (lane_ >> 5) : 0;
+            const int hidden = P.causal ? key - shift - q0 - 4 * (lane >> 5) : 0;
             f4 lse[2], dl[2];
             stats(st, 0, lse[0], dl[0]);
-            pipelined<frag, 2 * C, 4>([&](int i) { return operand(before, before_b, i, lane_); },
+            pipelined<frag, 2 * C, 4>([&](int i) { return operand(before, before_b, i, lane); },
                                       [&](int i, frag f) {
                                           const int k = i / C, c = i % C;
                                           d[c] = Mx<E>::mma32(f, c < CN + CR ? df[k] : pf[k], d[c]);
@@ -175,7 +177,7 @@ __global__ __launch_bounds__(256, 1) void attend_dkv_kernel(const AttendLaunch P
                                           }
                                       });
 #pragma unroll
-            for (int k = 0; k < 2; ++k) pf[k] = result_operand<E>(s, k), df[k] = result_operand<E>(dp, k);
+            for (int k = 0; k < 2; ++k) pf[k] = result_operand(s, k), df[k] = result_operand(dp, k);
             before = t;
             before_b = b;
         }
@@ -196,7 +198,10 @@ __global__ __launch_bounds__(256, 1) void attend_dkv_kernel(const AttendLaunch P
 }
 
 // As the forward pass: 128 queries per workgroup, 32 per wave, over the keys that they see.  Two workgroups share a CU: one's
-// exponentials hide behind the other's products, so its registers count; grad_o's operands are read from LDS each time.
+// exponentials hide behind the other's products, and waves that are at a product go first (s_setprio: 600 us against 608 for 2
+// sequences of 4,096 rows of 32 heads).  Blocks of 32 keys one after the other, not unrolled: two at a time do not fit the 256
+// registers beside q's, grad_o's and the sums'.   The same
+// sequences: 590 us for 550 GFLOP, 0.93 PFLOP/s.
 template <int NP, int RP, int VP>
 __global__ __launch_bounds__(256, 2) void attend_dq_kernel(const AttendLaunch P) {
     typedef uint16_t E;
@@ -284,7 +289,7 @@ __global__ __launch_bounds__(256, 2) void attend_dq_kernel(const AttendLaunch P)
             }
 #pragma unroll
             for (int i = 0; i < 16; ++i) dp[i] = exp2_f(fmaf(s[i], c2, -lse)) * (dp[i] - delta);
-            const frag df[2] = {result_operand<E>(dp, 0), result_operand<E>(dp, 1)};
+            const frag df[2] = {result_operand(dp, 0), result_operand(dp, 1)};
             __builtin_amdgcn_s_setprio(1);
             pipelined<frag, 2 * C, 3>(
                 [&](int i) {
@@ -327,6 +332,7 @@ void launch(const AttendLaunch &L, bool keys) {
 hipError_t launch_attend_bwd(const AttendLaunch &P) {
     AttendLaunch L = P;
     L.q_seq.L = L.k_seq.L = kAttendTile;
+    // as in the forward pass (2,048 rows of 32 heads of 64 + 32 and 64: 183 us, padded to the larger size 279)
     const bool small = P.dn <= 64 && P.dr <= 32 && P.dv <= 64;
     const int64_t rows_q = L.q_seq.rows() * L.H, rope = L.k_seq.rows() * (L.dr / 4);
     if (rows_q) {

@@ -5,7 +5,10 @@
 // the full head sizes, its operands 40 to 80 KiB.  So the operands come straight from the caches, without LDS, a few steps
 // ahead of their products; what counts is that all waves have work.  A workgroup has 32 queries (or keys), and its four
 // waves share out the tiles of keys (or queries) that they meet and add up their results through LDS at the end, in the
-// waves' order.
+// waves' order.  (Tiles in LDS, 64 rows to a workgroup: 256 rows of 8 heads 61 us forward against 21, 1,024 of 16 223 against 100,
+// 4,096 of 16 1,326 against 741; gradients of the last 3,506 against 3,280.)  At 4,096 rows of 16 heads that is 116 TFLOP/s forward
+// and 68 for the gradients (94 with the products that are formed twice) of the unit's 157: the loads of operands that
+// no product hides.
 #include "kda_latent.h"
 
 namespace kda {
@@ -317,6 +320,8 @@ __global__ __launch_bounds__(256, NP > 64 ? 1 : 2) void attend_grads_fp32_kernel
     else dq_fp32<NP, RP, VP>(P, blockIdx.x - key_groups, sums);
 }
 
+// Heads are padded with zeros to one of two sizes (2 sequences of 2,048 rows of 16 heads of 64 + 32 and 64: the gradients 808 us, padded
+// to the larger one 1,280).
 bool small(const AttendLaunch &P) { return P.dn <= 64 && P.dr <= 32 && P.dv <= 64; }
 
 }  // namespace

@@ -205,25 +205,15 @@ struct LdsTile {
         return *reinterpret_cast<const typename Mx<E>::frag *>(lds + at(row0 + (lane & 15), 4 * step | (lane >> 4)));
     }
     // A step's operand whose rows are the tile's columns col0 .. + 31, contracted over the tile's rows, in the order
-    // in which a lane holds the rows of a 32 x 32 result (lane half h: rows 8 b + 4 h + i): bf16 steps take 16 rows,
-    // fp32 steps 8.
-    __device__ __forceinline__ static typename Mx<E>::frag cols32(const char *lds, int row0, int step, int col0, int lane) {
-        const int h = lane >> 5;
-        if constexpr (sizeof(E) == 2) {
-            const int i = lane & 15, row = row0 + 16 * step + 4 * h + (i >> 2);
-            const int unit = (col0 >> 3) | ((lane >> 3) & 2) | ((i >> 1) & 1);
-            const char *p = lds + (i & 1) * 8;
-            const s4 lo = read_columns(p + at(row, unit));
-            const s4 hi = read_columns(p + at(row + 8, unit));
-            return __builtin_bit_cast(b8, (__attribute__((ext_vector_type(8))) short){lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]});
-        } else {
-            const int col = col0 + (lane & 31);
-            f4 v;
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                v[j] = *reinterpret_cast<const float *>(lds + at(row0 + 8 * step + 4 * h + j, col >> 2) + (col & 3) * 4);
-            return v;
-        }
+    // in which a lane holds the rows of a 32 x 32 result (lane half h: rows 8 b + 4 h + i), 16 rows a step.
+    __device__ __forceinline__ static b8 cols32(const char *lds, int row0, int step, int col0, int lane) {
+        static_assert(sizeof(E) == 2, "");
+        const int h = lane >> 5, i = lane & 15, row = row0 + 16 * step + 4 * h + (i >> 2);
+        const int unit = (col0 >> 3) | ((lane >> 3) & 2) | ((i >> 1) & 1);
+        const char *p = lds + (i & 1) * 8;
+        const s4 lo = read_columns(p + at(row, unit));
+        const s4 hi = read_columns(p + at(row + 8, unit));
+        return __builtin_bit_cast(b8, (__attribute__((ext_vector_type(8))) short){lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]});
     }
     // The same for 16 columns and the rows that a lane holds of 16 x 16 results (quarter g: rows 4 g + i), one result for
     // fp32 and two, 16 rows apart, for bf16.
@@ -245,19 +235,12 @@ struct LdsTile {
 };
 
 // Rows of a 32 x 32 result as a step's operand (the order that cols32 reads in).
-template <class E>
-__device__ __forceinline__ typename Mx<E>::frag result_operand(const f16 &s, int step) {
-    if constexpr (sizeof(E) == 2) {
-        b8 v;
+__device__ __forceinline__ b8 result_operand(const f16 &s, int step) {
+    b8 v;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = static_cast<__bf16>(s[8 * step + j]);
-        return v;
-    } else {
-        return f4{s[4 * step], s[4 * step + 1], s[4 * step + 2], s[4 * step + 3]};
-    }
+    for (int j = 0; j < 8; ++j) v[j] = static_cast<__bf16>(s[8 * step + j]);
+    return v;
 }
-template <class E>
-constexpr int kSteps32 = 32 / (2 * Mx<E>::PER);  // steps that contract 32 rows
 
 // A row's operands straight from memory: element 2 PER step + PER h on; zeros from `width` on or where !live.
 template <class E>
@@ -301,7 +284,8 @@ __device__ __forceinline__ void loads_landed() {
 
 // The rows of a wave's results: row lane % 32 has, in tile c, columns 32 c + 8 b + 4 (lane / 32) .. + 3 as elements 4 b .. + 3.
 // Rows of bf16 are put together in LDS (32 * kStoreRow<W> bytes of the wave's own) and leave 16 bytes per lane and whole rows at
-// a time: eight bytes from each of 64 places cost the gradients' key kernel STORE_A.  `to`: the wave's first row.
+// a time (the forward kernel at 8,192 rows of 32 heads takes 646 us so and 658 with eight bytes to each of 64 places, the
+// gradients' query kernel at 2 sequences of 4,096 rows 590 and 600).  `to`: the wave's first row.
 template <int W>
 constexpr int kStoreRow = 2 * W + 16;
 template <int W>

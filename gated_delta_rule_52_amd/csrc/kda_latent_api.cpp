@@ -67,7 +67,7 @@ kda_status rotary(const kda_rotary_args *a, bool inverse, const char *what) {
         a->offset > a->dim - a->rot)
         return fail(KDA_ERR_BAD_SHAPE, "rows=%lld heads=%d dim=%d rot=%d offset=%d", static_cast<long long>(a->rows), a->heads,
                     a->dim, a->rot, a->offset);
-    if (a->rows > INT32_MAX || a->rot > 4096 || a->dim > 1 << 20 || a->heads > 1 << 20)
+    if (a->rows > INT32_MAX || a->rot > 4096 || a->dim > 1 << 15 || a->heads > 1 << 20)
         return fail(KDA_ERR_UNSUPPORTED, "rows=%lld heads=%d dim=%d rot=%d", static_cast<long long>(a->rows), a->heads, a->dim, a->rot);
     if (!valid_dtype(a->dtype)) return fail(KDA_ERR_UNSUPPORTED, "dtype=%d", a->dtype);
     if (a->flags & ~KDA_ROTARY_INTERLEAVED) return fail(KDA_ERR_UNSUPPORTED, "unknown flags 0x%x", a->flags);
@@ -170,6 +170,9 @@ kda_status check_step_sizes(const kda_latent_step_args *a) {
     if (a->N > 65535 || a->H > 65535) return fail(KDA_ERR_UNSUPPORTED, "N=%d H=%d (at most 65535)", a->N, a->H);
     if (static_cast<int64_t>(a->max_blocks) * a->page > kMostRows || static_cast<int64_t>(a->num_blocks) * a->page > INT32_MAX)
         return fail(KDA_ERR_UNSUPPORTED, "more than 2^30 rows per sequence or 2^31 - 1 in the cache");
+    // the sequences' tiles, of 16 rows or more, are counted in 32 bits
+    if (((static_cast<int64_t>(a->max_blocks) * a->page + 15) / 16) * a->N > INT32_MAX)
+        return fail(KDA_ERR_UNSUPPORTED, "N * max_blocks * page is more than 2^35 rows");
     return check_grid(kda::latent_step_threads(a->N, a->H, a->in_dtype == KDA_DTYPE_BF16, step_splits(a)));
 }
 

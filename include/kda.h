@@ -746,6 +746,10 @@ kda_status kda_layer_norm_bwd(const kda_layer_norm_bwd_args *args);
  *    max) and the scores' gradients are rounded to bf16 where a matrix product
  *    takes them.
  *  - A query that sees no key gets o = 0 and lse = -inf, and no gradient.
+ *  - What a query does not see has weight 0, and is multiplied with it: an
+ *    infinite or NaN value of a key that is hidden from a query of the same
+ *    sequence may make that query's result NaN.  Rows of other sequences, rows
+ *    behind the last one and cache rows behind a sequence's end never count.
  *  - Rows outside the sequences of a packed batch are left as they were.
  */
 
@@ -762,7 +766,7 @@ kda_status kda_layer_norm_bwd(const kda_layer_norm_bwd_args *args);
  * nothing.  Long contexts are a matter of inv_freq and scale.
  *   x, y : [rows, heads, dim] dtype; y may be x (same strides): only the
  *          turned part is touched then.  positions : [rows] int32, inv_freq :
- *          [rot / 2] fp32.  rot is even, at most 4096; dim at most 2^20.
+ *          [rot / 2] fp32.  rot is even, at most 4096; dim at most 2^15.
  * kda_rotary_bwd: the gradient (x: of y, y: of x), which turns the other way.
  */
 typedef struct {
@@ -824,7 +828,8 @@ kda_status kda_latent_cache_append(const kda_latent_append_args *args);
  *   [N] int32.  Lengths are held to 0 .. max_blocks * page; rows on blocks
  *   that do not exist are left out, and entries behind a sequence's last row
  *   are not read.
- *   dl : at most 512, dr : at most 64.  scale > 0.
+ *   dl : at most 512, dr : at most 64.  scale > 0.  A sequence has at most 2^30
+ *   rows, the cache 2^31 - 1, N * max_blocks * page at most 2^35.
  *   workspace : kda_latent_attention_step_workspace_bytes() bytes.
  */
 typedef struct {

@@ -76,7 +76,7 @@ def check_rotary(kda, seed, lead, H, D, rot, offset, interleaved, dtype, scale=1
 @pytest.mark.parametrize("interleaved", [True, False])
 @pytest.mark.parametrize("lead,H,D,rot,offset", [
     ((1,), 1, 2, 2, 0), ((3,), 2, 64, 64, 0), ((2, 5), 3, 192, 64, 128), ((1, 301), 4, 128, 32, 40), ((7,), 5, 37, 10, 3),
-    ((513,), 1, 256, 128, 0), ((2,), 130, 96, 48, 16), ((2, 3, 4), 2, 80, 80, 0), ((3,), 1, 5000, 4096, 8), ((1,), 40, 1200, 16, 1184)])
+    ((513,), 1, 256, 128, 0), ((2,), 130, 96, 48, 16), ((2, 3, 4), 2, 80, 80, 0), ((3,), 1, 5000, 4096, 8), ((1,), 40, 1200, 16, 1184), ((2,), 2, 32767, 64, 903)])
 def test_rotary(kda, dtype, interleaved, lead, H, D, rot, offset):
     check_rotary(kda, 1, lead, H, D, rot, offset, interleaved, dtype)
     check_rotary(kda, 2, lead, H, D, rot, offset, interleaved, dtype, scale=1.25, in_place=True)

@@ -64,6 +64,7 @@ CASES = [
         (dict(positions=None), NULL), (dict(inv_freq=None), NULL), (dict(x_stride=599), SHAPE),
         (dict(x_head_stride=149), SHAPE), (dict(y_head_stride=600), SHAPE), (dict(rows=1 << 31), UNSUP),
         (dict(rot=4098, dim=5000, x_stride=20000, x_head_stride=5000), UNSUP), (dict(heads=1 << 21), UNSUP),
+        (dict(dim=(1 << 15) + 2, x_stride=300000, x_head_stride=40000, y_stride=300000, y_head_stride=40000), UNSUP),
         (dict(rows=1 << 24, heads=1, x_stride=150, y_stride=150), UNSUP), (dict(y=F, y_stride=900), ALIAS),
         (dict(y=F + 2), ALIAS), (dict(y=3 * F), ALIAS), (dict(y=4 * F + 64), ALIAS)]),
     ("kda_rotary_bwd", rotary, [(dict(x=None), NULL), (dict(y=F + 64), ALIAS)]),
@@ -79,6 +80,7 @@ CASES = [
         (dict(dl=0), SHAPE), (dict(dl=520), UNSUP), (dict(dl=100), UNSUP), (dict(dr=72), UNSUP), (dict(dr=4), UNSUP),
         (dict(scale=0.0), SHAPE), (dict(scale=NAN), SHAPE), (dict(in_dtype=2), UNSUP), (dict(out_dtype=2), UNSUP),
         (dict(N=70000), UNSUP), (dict(H=70000), UNSUP), (dict(page=1 << 20, max_blocks=1 << 12), UNSUP),
+        (dict(N=2000, page=1 << 10, max_blocks=1 << 20, block_table_stride=1 << 20), UNSUP),
         (dict(q_latent=None), NULL), (dict(q_rope=None), NULL), (dict(cache=None), NULL), (dict(block_table=None), NULL),
         (dict(lengths=None), NULL), (dict(o=None), NULL), (dict(q_latent_stride=100), SHAPE),
         (dict(q_rope_head_stride=56), SHAPE), (dict(block_table_stride=39), SHAPE), (dict(q_latent=F + 2), UNSUP),
