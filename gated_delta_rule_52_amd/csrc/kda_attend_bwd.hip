@@ -13,9 +13,7 @@ namespace {
 
 using namespace la;
 
-// delta: 16 lanes per (row, head), 8 elements each (dv <= 128).  For bf16 also lse in powers of two, for rows that see nothing
-// as infinity, which leaves them no weights.
-template <class E>
+// delta for fp32 (the bf16 kernel for dq forms its own): 16 lanes per (row, head), 8 elements each (dv <= 128).
 __global__ __launch_bounds__(256) void attend_delta_kernel(const AttendLaunch P) {
     const int64_t rows = P.q_seq.rows() * P.H, at = static_cast<int64_t>(blockIdx.x) * 16 + (threadIdx.x >> 4);
     if (at >= rows) return;
@@ -23,27 +21,19 @@ __global__ __launch_bounds__(256) void attend_delta_kernel(const AttendLaunch P)
     const int h = static_cast<int>(at % P.H), c = 8 * (threadIdx.x & 15);
     float x = 0.f;
     if (c < P.dv) {
-        const E *o = head_row<E>(P.o, row, h) + c, *g = head_row<E>(P.go, row, h) + c;
-        constexpr int PER = Mx<E>::PER;
+        const float *o = head_row<float>(P.o, row, h) + c, *g = head_row<float>(P.go, row, h) + c;
 #pragma unroll
-        for (int k = 0; k < 8; k += PER) {
-            const typename Mx<E>::frag a = *reinterpret_cast<const typename Mx<E>::frag *>(o + k);
-            const typename Mx<E>::frag b = *reinterpret_cast<const typename Mx<E>::frag *>(g + k);
+        for (int k = 0; k < 8; k += 4) {
+            const f4 a = *reinterpret_cast<const f4 *>(o + k), b = *reinterpret_cast<const f4 *>(g + k);
 #pragma unroll
-            for (int j = 0; j < PER; ++j) x = fmaf(static_cast<float>(a[j]), static_cast<float>(b[j]), x);
+            for (int j = 0; j < 4; ++j) x = fmaf(a[j], b[j], x);
         }
     }
     x += dpp_mov<0xB1>(x);
     x += dpp_mov<0x4E>(x);
     x += dpp_mov<0x141>(x);
     x += dpp_mov<0x140>(x);
-    if ((threadIdx.x & 15) == 0) {
-        P.delta[at] = x;
-        if constexpr (sizeof(E) == 2) {
-            const float l = P.lse[at];
-            P.lse2[at] = l == neg_inf() ? __builtin_inff() : l * kLog2e;
-        }
-    }
+    if ((threadIdx.x & 15) == 0) P.delta[at] = x;
 }
 
 // A workgroup of four waves has 128 keys, 32 per wave, whose operands and gradients stay in registers (one wave per
@@ -244,7 +234,23 @@ __global__ __launch_bounds__(256, 2) void attend_dq_kernel(const AttendLaunch P)
     const E *gp = head_row<E>(P.go, row, w.h);
 #pragma unroll
     for (int s = 0; s < SV; ++s) gf[s] = row_operand<E>(gp, s, P.dv, live, lane);
-    const float lse = P.lse2[row * P.H + w.h], delta = P.delta[row * P.H + w.h];
+    // The row's statistics, for the keys' kernel too: delta, and lse in powers of two, infinite for rows that see nothing, which
+    // leaves them no weights.  In a kernel of their own they take 28 us more at 2 sequences of 4,096 rows of 32 heads.
+    float delta = 0.f;
+    const E *op = head_row<E>(P.o, row, w.h);
+#pragma unroll
+    for (int s = 0; s < SV; ++s) {
+        const frag x = row_operand<E>(op, s, P.dv, live, lane);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) delta = fmaf(static_cast<float>(x[j]), static_cast<float>(gf[s][j]), delta);
+    }
+    delta = halves_sum(delta);
+    const int64_t stat = row * P.H + w.h;
+    const float lse = P.lse[stat] == neg_inf() ? __builtin_inff() : P.lse[stat] * kLog2e;
+    if (live && lane < 32) {
+        P.lse2[stat] = lse;
+        P.delta[stat] = delta;
+    }
     f16 dq[C];
 #pragma unroll
     for (int c = 0; c < C; ++c)
@@ -335,17 +341,14 @@ hipError_t launch_attend_bwd(const AttendLaunch &P) {
     // as in the forward pass (2,048 rows of 32 heads of 64 + 32 and 64: 183 us, padded to the larger size 279)
     const bool small = P.dn <= 64 && P.dr <= 32 && P.dv <= 64;
     const int64_t rows_q = L.q_seq.rows() * L.H, rope = L.k_seq.rows() * (L.dr / 4);
-    if (rows_q) {
-        const unsigned n = static_cast<unsigned>((rows_q + 15) / 16);
-        if (P.bf16) attend_delta_kernel<uint16_t><<<n, 256, 0, L.stream>>>(L);
-        else attend_delta_kernel<float><<<n, 256, 0, L.stream>>>(L);
+    if (P.bf16) {
+        if (rows_q) small ? launch<64, 32, 64>(L, false) : launch<128, 64, 128>(L, false);
+        if (rope) small ? launch<64, 32, 64>(L, true) : launch<128, 64, 128>(L, true);
+    } else {
+        if (rows_q) attend_delta_kernel<<<static_cast<unsigned>((rows_q + 15) / 16), 256, 0, L.stream>>>(L);
+        launch_attend_grads_fp32(P);
     }
-    if (!P.bf16) launch_attend_grads_fp32(P);
-    if (rope) {
-        if (P.bf16) small ? launch<64, 32, 64>(L, true) : launch<128, 64, 128>(L, true);
-        attend_rope_sum_kernel<<<static_cast<unsigned>((rope + 255) / 256), 256, 0, L.stream>>>(L);
-    }
-    if (rows_q && P.bf16) small ? launch<64, 32, 64>(L, false) : launch<128, 64, 128>(L, false);
+    if (rope) attend_rope_sum_kernel<<<static_cast<unsigned>((rope + 255) / 256), 256, 0, L.stream>>>(L);
     return hipGetLastError();
 }
 
@@ -353,7 +356,7 @@ hipError_t launch_attend_bwd(const AttendLaunch &P) {
 int64_t attend_threads(const SeqTiles &q_, const SeqTiles &k_, int H, int dr, bool bf16, bool backward) {
     SeqTiles q = q_, k = k_;
     q.L = k.L = bf16 ? kAttendTile : kAttendTileF32;
-    int64_t n = (tiles_of(q) + (backward && !bf16 ? tiles_of(k) : 0)) * H * 256;
+    int64_t n = (tiles_of(q) + (backward && !bf16 ? tiles_of(k) : 0)) * H * (bf16 ? 256 : 512);
     if (backward) {
         const int64_t parts[] = {tiles_of(k) * H * 256, (q.rows() * H + 15) / 16 * 256, (k.rows() * (dr / 4) + 255) / 256 * 256};
         for (const int64_t p : parts) n = p > n ? p : n;

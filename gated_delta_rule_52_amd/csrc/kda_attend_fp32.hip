@@ -17,7 +17,7 @@ namespace {
 using namespace la;
 typedef Mx<float> M;
 
-constexpr int kWavesF = 4, kAhead = 4;  // waves that share a tile's work; steps between an operand's load and its use
+constexpr int kAhead = 4;  // steps between an operand's load and its use
 
 __device__ __forceinline__ void clear(f16 &x) {
 #pragma unroll
@@ -71,8 +71,8 @@ __device__ __forceinline__ void load_rows(f4 *f, const float *row, int width, bo
     for (int s = 0; s < STEPS; ++s) f[s] = row_operand<float>(row, s, width, live, lane);
 }
 
-// Adds up N tiles over the waves, PART at a time through LDS, and gives wave c % 4 the sum of tile c.
-template <int N, int PART, class Store>
+// Adds up N tiles over the waves, PART at a time through LDS, and gives wave c % WAVES the sum of tile c.
+template <int WAVES, int N, int PART, class Store>
 __device__ __forceinline__ void join_waves(const f16 *acc, float *lds, int wave, int lane, Store store) {
 #pragma unroll
     for (int first = 0; first < N; first += PART) {
@@ -86,24 +86,24 @@ __device__ __forceinline__ void join_waves(const f16 *acc, float *lds, int wave,
         __syncthreads();
 #pragma unroll
         for (int c = 0; c < PART; ++c)
-            if (first + c < N && (first + c) % kWavesF == wave) {
+            if (first + c < N && (first + c) % WAVES == wave) {
                 f16 x;
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     x[i] = lds[(c * 16 + i) * 64 + lane];
 #pragma unroll
-                    for (int w = 1; w < kWavesF; ++w) x[i] += lds[((w * PART + c) * 16 + i) * 64 + lane];
+                    for (int w = 1; w < WAVES; ++w) x[i] += lds[((w * PART + c) * 16 + i) * 64 + lane];
                 }
                 store(first + c, x);
             }
     }
 }
 
-template <int NP, int RP, int VP>
-__global__ __launch_bounds__(256, 2) void attend_fwd_fp32_kernel(const AttendLaunch P) {
+template <int WAVES, int NP, int RP, int VP>
+__global__ __launch_bounds__(64 * WAVES, 2) void attend_fwd_fp32_kernel(const AttendLaunch P) {
     constexpr int SN = NP / 8, SR = RP / 8, CV = VP / 32;
-    __shared__ float sums[kWavesF * CV * 1024];
-    __shared__ float2 stats[kWavesF][32];
+    __shared__ float sums[WAVES * CV * 1024];
+    __shared__ float2 stats[WAVES][32];
     const Place w = place_of<true>(P, blockIdx.x);
     if (!w.valid || w.at >= w.nq) return;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -123,7 +123,7 @@ __global__ __launch_bounds__(256, 2) void attend_fwd_fp32_kernel(const AttendLau
     for (int c = 0; c < CV; ++c) clear(acc[c]);
     float m = neg_inf(), l = 0.f;
     const float c2 = P.scale * kLog2e;
-    for (int key0 = 32 * wave; key0 < keys; key0 += 32 * kWavesF) {
+    for (int key0 = 32 * wave; key0 < keys; key0 += 32 * WAVES) {
         const int lane_ = afresh(lane);
         const TileRows K(kp, key0, P.k.stride, w.nk, P.dn), R(rp, key0, P.kr.stride, w.nk, P.dr), V(vp, key0, P.v.stride, w.nk, P.dv);
         f16 s;
@@ -163,10 +163,10 @@ __global__ __launch_bounds__(256, 2) void attend_fwd_fp32_kernel(const AttendLau
     __syncthreads();
     float top = neg_inf(), total = 0.f;
 #pragma unroll
-    for (int i = 0; i < kWavesF; ++i) top = fmaxf(top, stats[i][lane & 31].x);
+    for (int i = 0; i < WAVES; ++i) top = fmaxf(top, stats[i][lane & 31].x);
     const float at = top == neg_inf() ? 0.f : top;
 #pragma unroll
-    for (int i = 0; i < kWavesF; ++i) total = fmaf(stats[i][lane & 31].y, exp2_f(stats[i][lane & 31].x - at), total);
+    for (int i = 0; i < WAVES; ++i) total = fmaf(stats[i][lane & 31].y, exp2_f(stats[i][lane & 31].x - at), total);
     const float by = exp2_f(m - at), inv = total > 0.f ? 1.f / total : total == 0.f ? 0.f : total;  // NaN stays
 #pragma unroll
     for (int c = 0; c < CV; ++c)
@@ -174,7 +174,7 @@ __global__ __launch_bounds__(256, 2) void attend_fwd_fp32_kernel(const AttendLau
         for (int i = 0; i < 16; ++i) acc[c][i] *= by;
     const int64_t row = w.q_row + q, out = row * P.o.stride + w.h * P.o.head_stride;
     if (P.lse && live && threadIdx.x < 32) P.lse[row * P.H + w.h] = total == 0.f ? neg_inf() : (at + __log2f(total)) * kLn2;
-    join_waves<CV, CV>(acc, sums, wave, lane, [&](int c, const f16 &x) {
+    join_waves<WAVES, CV, CV>(acc, sums, wave, lane, [&](int c, const f16 &x) {
         if (!live) return;
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
@@ -184,7 +184,7 @@ __global__ __launch_bounds__(256, 2) void attend_fwd_fp32_kernel(const AttendLau
     });
 }
 
-template <int NP, int RP, int VP>
+template <int WAVES, int NP, int RP, int VP>
 __device__ __forceinline__ void dkv_fp32(const AttendLaunch &P, int64_t id, float *sums) {
     constexpr int SN = NP / 8, SR = RP / 8, SV = VP / 8, CN = NP / 32, CR = RP / 32, CV = VP / 32, PART = (CN + CR + CV + 1) / 2;
     const Place w = place_of<false>(P, id);
@@ -206,7 +206,7 @@ __device__ __forceinline__ void dkv_fp32(const AttendLaunch &P, int64_t id, floa
     for (int c = 0; c < CN + CR + CV; ++c) clear(d[c]);
     const float c2 = P.scale * kLog2e;
     const int first = P.causal ? max(0, w.at - shift) / 32 : 0;  // the tile of the first query that sees the first key
-    for (int q0 = 32 * (first + wave); q0 < w.nq; q0 += 32 * kWavesF) {
+    for (int q0 = 32 * (first + wave); q0 < w.nq; q0 += 32 * WAVES) {
         const int lane_ = afresh(lane);
         const TileRows Q(qp, q0, P.q.stride, w.nq, P.dn), R(qp + P.dn, q0, P.q.stride, w.nq, P.dr), G(gp, q0, P.go.stride, w.nq, P.dv);
         f16 s, dp;
@@ -236,7 +236,7 @@ __device__ __forceinline__ void dkv_fp32(const AttendLaunch &P, int64_t id, floa
     }
     const int64_t dk_at = row * P.dk.stride + w.h * P.dk.head_stride, dv_at = row * P.dvg.stride + w.h * P.dvg.head_stride;
     const int64_t part = (row * P.H + w.h) * P.dr;
-    join_waves<CN + CR + CV, PART>(d, sums, wave, lane, [&](int c, const f16 &x) {
+    join_waves<WAVES, CN + CR + CV, PART>(d, sums, wave, lane, [&](int c, const f16 &x) {
         if (!live) return;
         const bool v = c >= CN + CR, r = !v && c >= CN;
         const float by = v ? 1.f : P.scale;
@@ -250,7 +250,7 @@ __device__ __forceinline__ void dkv_fp32(const AttendLaunch &P, int64_t id, floa
     });
 }
 
-template <int NP, int RP, int VP>
+template <int WAVES, int NP, int RP, int VP>
 __device__ __forceinline__ void dq_fp32(const AttendLaunch &P, int64_t id, float *sums) {
     constexpr int SN = NP / 8, SR = RP / 8, SV = VP / 8, CN = NP / 32, CR = RP / 32;
     const Place w = place_of<true>(P, id);
@@ -274,7 +274,7 @@ __device__ __forceinline__ void dq_fp32(const AttendLaunch &P, int64_t id, float
 #pragma unroll
     for (int c = 0; c < CN + CR; ++c) clear(dq[c]);
     const float c2 = P.scale * kLog2e;
-    for (int key0 = 32 * wave; key0 < keys; key0 += 32 * kWavesF) {
+    for (int key0 = 32 * wave; key0 < keys; key0 += 32 * WAVES) {
         const int lane_ = afresh(lane);
         const TileRows K(kp, key0, P.k.stride, w.nk, P.dn), R(rp, key0, P.kr.stride, w.nk, P.dr), V(vp, key0, P.v.stride, w.nk, P.dv);
         f16 s, dp;
@@ -299,7 +299,7 @@ __device__ __forceinline__ void dq_fp32(const AttendLaunch &P, int64_t id, float
             });
     }
     const int64_t out = row * P.dq.stride + w.h * P.dq.head_stride;
-    join_waves<CN + CR, CN + CR>(dq, sums, wave, lane, [&](int c, const f16 &x) {
+    join_waves<WAVES, CN + CR, CN + CR>(dq, sums, wave, lane, [&](int c, const f16 &x) {
         if (!live) return;
         const bool r = c >= CN;
 #pragma unroll
@@ -312,17 +312,31 @@ __device__ __forceinline__ void dq_fp32(const AttendLaunch &P, int64_t id, float
 }
 
 // Both in one launch: where there are few tiles they run side by side.  Keys' tiles first, each takes longer.
-template <int NP, int RP, int VP>
-__global__ __launch_bounds__(256, NP > 64 ? 1 : 2) void attend_grads_fp32_kernel(const AttendLaunch P, unsigned key_groups) {
+template <int WAVES, int NP, int RP, int VP>
+__global__ __launch_bounds__(64 * WAVES, NP > 64 ? 1 : 2) void attend_grads_fp32_kernel(const AttendLaunch P, unsigned key_groups) {
     constexpr int N = (NP + RP) / 32, PART = (N + VP / 32 + 1) / 2;
-    __shared__ float sums[kWavesF * (N > PART ? N : PART) * 1024];
-    if (blockIdx.x < key_groups) dkv_fp32<NP, RP, VP>(P, blockIdx.x, sums);
-    else dq_fp32<NP, RP, VP>(P, blockIdx.x - key_groups, sums);
+    __shared__ float sums[WAVES * (N > PART ? N : PART) * 1024];
+    if (blockIdx.x < key_groups) dkv_fp32<WAVES, NP, RP, VP>(P, blockIdx.x, sums);
+    else dq_fp32<WAVES, NP, RP, VP>(P, blockIdx.x - key_groups, sums);
 }
 
 // Heads are padded with zeros to one of two sizes (2 sequences of 2,048 rows of 16 heads of 64 + 32 and 64: the gradients 808 us, padded
 // to the larger one 1,280).
 bool small(const AttendLaunch &P) { return P.dn <= 64 && P.dr <= 32 && P.dv <= 64; }
+
+// Eight waves share a tile's work where there are few workgroups, and so the longest sequence's tiles decide; where there are
+// many, more results to add up only cost (four waves and eight, forward at the full head sizes: 1,024 rows of 16 heads 98 and 75
+// us, 1,536 rows 127 and 143; gradients at the small ones: 1,024 rows of 8 heads 114 and 90 us, 1,536 of 16 261 and 285).
+bool few(unsigned n) { return n <= 512; }
+
+template <int WAVES, int NP, int RP, int VP>
+void fwd(const AttendLaunch &L, unsigned n) {
+    attend_fwd_fp32_kernel<WAVES, NP, RP, VP><<<n, 64 * WAVES, 0, L.stream>>>(L);
+}
+template <int WAVES, int NP, int RP, int VP>
+void grads(const AttendLaunch &L, unsigned n, unsigned k) {
+    attend_grads_fp32_kernel<WAVES, NP, RP, VP><<<n, 64 * WAVES, 0, L.stream>>>(L, k);
+}
 
 }  // namespace
 
@@ -330,16 +344,16 @@ void launch_attend_fwd_fp32(const AttendLaunch &P) {
     AttendLaunch L = P;
     L.q_seq.L = kAttendTileF32;
     const unsigned n = static_cast<unsigned>(tiles_of(L.q_seq) * L.H);
-    if (small(L)) attend_fwd_fp32_kernel<64, 32, 64><<<n, 256, 0, L.stream>>>(L);
-    else attend_fwd_fp32_kernel<128, 64, 128><<<n, 256, 0, L.stream>>>(L);
+    if (small(L)) few(n) ? fwd<8, 64, 32, 64>(L, n) : fwd<4, 64, 32, 64>(L, n);
+    else few(n) ? fwd<8, 128, 64, 128>(L, n) : fwd<4, 128, 64, 128>(L, n);
 }
 void launch_attend_grads_fp32(const AttendLaunch &P) {
     AttendLaunch L = P;
     L.q_seq.L = L.k_seq.L = kAttendTileF32;
     const unsigned k = L.k_seq.rows() ? static_cast<unsigned>(tiles_of(L.k_seq) * L.H) : 0;
     const unsigned n = k + (L.q_seq.rows() ? static_cast<unsigned>(tiles_of(L.q_seq) * L.H) : 0);
-    if (small(L)) attend_grads_fp32_kernel<64, 32, 64><<<n, 256, 0, L.stream>>>(L, k);
-    else attend_grads_fp32_kernel<128, 64, 128><<<n, 256, 0, L.stream>>>(L, k);
+    if (small(L)) few(n) ? grads<8, 64, 32, 64>(L, n, k) : grads<4, 64, 32, 64>(L, n, k);
+    else grads<4, 128, 64, 128>(L, n, k);  // one wave per SIMD has the registers
 }
 
 }  // namespace kda
