@@ -247,7 +247,7 @@ def latent_attention_bwd(q: torch.Tensor, k: torch.Tensor, k_rope: torch.Tensor,
                          out: Optional[dict] = None) -> dict:
     """Gradients of ``latent_attention_fwd`` for grad_o [B,Tq,H,dv] (dtype of q), given its inputs, its o (dtype of q) and its
     lse.  Returns a dict dq, dk, dk_rope, dv of the inputs' shapes in ``grad_dtype``; ``out`` may supply them (dk and dv
-    may be slices of one [B,Tk,H,dn+dv] tensor)."""
+    may be slices of one [B,Tk,H,dn+dv] tensor).  Rows outside the sequences of packed input are left as they were."""
     device, dtype, kind, sizes, strides, cu_q, cu_k = _attend(q, k, k_rope, v, scale, cu_seqlens_q, cu_seqlens_k)
     B, Tq, Tk, H, dn, dr, dv = sizes[:7]
     grad_kind = _grad_dtype(grad_dtype)
