@@ -894,7 +894,9 @@ kda_status kda_latent_attention_fwd(const kda_latent_attention_args *args);
 /*
  * Its gradients for grad_o [rows_q, H, dv] (in_dtype), from the inputs and
  * what the forward pass left: o (in_dtype) and lse.  With p_ij = exp(s_ij -
- * lse_i) and ds_ij = p_ij (grad_o_i . v_j - grad_o_i . o_i),
+ * lse_i) and ds_ij = p_ij (grad_o_i . v_j - grad_o_i . o_i) (in bf16, where a
+ * query sees few keys, with sum_j p_ij grad_o_i . v_j for the last product,
+ * of which o's rounding would be a large part),
  *     grad_v_j = sum_i p_ij grad_o_i,   grad_k_j = scale sum_i ds_ij q_i[:dn],
  *     grad_k_rope_j = scale sum_h sum_i ds_ij q_i[dn:],
  *     grad_q_i = scale sum_j ds_ij [k_j | k_rope_j].

@@ -86,7 +86,12 @@ def attend(q, k, kr, v, off_q, off_k, scale, causal, kind="fp32", out="fp32"):
 
 def attend_grads(q, k, kr, v, o, lse, go, off_q, off_k, scale, causal, kind="fp32", out="fp32"):
     """The gradients from given o and lse, as the entry point takes them, and their bounds: name -> (value, element bound,
-    norm bound)."""
+    norm bound).
+
+    delta_i = grad_o_i . o_i = sum_j p_ij dp_ij.  Where o is bf16 the two differ by what o's roundings make of it, a number
+    that is known here.  A kernel may take either, or what lies between: ds is linear in delta, so with the second as the
+    value the bound of ds has that number times p.  The second is a sum over weights that are each off by ep, so it is off
+    by at most sum_j p_ij ep_ij (|dp_ij| + |delta_i|)."""
     H, d = q.shape[1:]
     dn = k.shape[-1]
     z = np.zeros_like
@@ -106,8 +111,12 @@ def attend_grads(q, k, kr, v, o, lse, go, off_q, off_k, scale, causal, kind="fp3
             x = np.abs(qh) @ np.abs(kk).T * scale
             ep = (d + 8) * U32 * x + 4 * U32 * np.abs(l) + 6 * U32  # relative, of a weight
             dp, delta = gh @ vh.T, (gh * oh).sum(-1)[:, None]
+            between = 0.0
+            if kind == "bf16":
+                given, delta = delta, (p * dp).sum(-1)[:, None]
+                between = np.abs(given - delta) + (p * ep * (np.abs(dp) + np.abs(delta))).sum(-1)[:, None]
             ds = p * (dp - delta)
-            eds = p * (v.shape[-1] + 6) * U32 * (np.abs(gh) @ np.abs(vh).T + (np.abs(gh) * np.abs(oh)).sum(-1)[:, None]) + np.abs(ds) * (ep + 2 * U32)
+            eds = p * between + p * (v.shape[-1] + 6) * U32 * (np.abs(gh) @ np.abs(vh).T + (np.abs(gh) * np.abs(oh)).sum(-1)[:, None]) + np.abs(ds) * (ep + 2 * U32)
             for name, a, ea, b, f, at in (("dv", p.T, (p * ep).T, gh, 1.0, sk), ("dk", ds.T, eds.T, qh, scale, sk), ("dq", ds, eds, kk, scale, sq)):
                 ab, n = np.abs(b), a.shape[1]
                 g[name][at, h] = f * (a @ b)
