@@ -401,7 +401,7 @@ __global__ __launch_bounds__(64 * kWaves<HT>, sizeof(E) == 2 ? 2 : 1) void laten
 
 // Joins the parts of a (sequence, head): o = sum_s exp(lse_s - lse) o_s, lse = log sum_s exp(lse_s).  Sequences without rows
 // get zeros here.  COLS columns per workgroup, COLS / 4 threads of four by those that share the parts out.
-constexpr int kJoinParts = 512;
+constexpr int kJoinParts = 512, kJoinWhole = 512;  // the most parts; rows from which a workgroup has all columns
 template <int COLS>
 __global__ __launch_bounds__(256) void latent_join_kernel(const LatentStepLaunch P, int heads, int groups) {
     __shared__ float weight[kJoinParts];
@@ -503,7 +503,8 @@ size_t latent_step_workspace_bytes(int N, int H, int dl, int splits, bool bf16) 
     return splits == 0 ? 0 : groups * 2 * splits * heads * (static_cast<size_t>(dl) + 1) * 4 + groups * N * sizeof(int2);
 }
 int64_t latent_step_threads(int N, int H, bool bf16, int splits) {
-    const int64_t step = static_cast<int64_t>(splits ? splits : N) * head_groups(H, bf16) * 512, join = static_cast<int64_t>(N) * H * 256 * 4;
+    const int64_t step = static_cast<int64_t>(splits ? splits : N) * head_groups(H, bf16) * 512, rows = static_cast<int64_t>(N) * H;
+    const int64_t join = splits == 0 ? 0 : rows * (rows >= kJoinWhole ? 256 : 256 * 4);
     return step > join ? step : join;
 }
 
@@ -516,7 +517,7 @@ hipError_t launch_latent_step(const LatentStepLaunch &P) {
         // All columns at once where there are rows enough for every CU (64 sequences of 32 heads 9 us against 16), a quarter where a few rows
         // have many parts (one sequence of 65,536 rows 43 us
         // against 60 for both kernels).
-        if (rows >= 512) latent_join_kernel<512><<<static_cast<unsigned>(rows), 256, 0, P.stream>>>(P, heads, groups);
+        if (rows >= kJoinWhole) latent_join_kernel<512><<<static_cast<unsigned>(rows), 256, 0, P.stream>>>(P, heads, groups);
         else latent_join_kernel<128><<<dim3(static_cast<unsigned>(rows), (P.dl + 127) / 128), 256, 0, P.stream>>>(P, heads, groups);
     }
     return hipGetLastError();

@@ -347,6 +347,24 @@ def test_step_of_many_sequences(kda, dtype, N, longest, H, page):
     check_step(kda, 96, [int(n) for n in lengths], H, 64, 16, page, dtype)
 
 
+def test_step_of_the_most_sequences(kda):
+    """65,535 sequences of 128 heads, of one row each or none: the row itself, and its scaled score (a sum of 16 products of
+    bf16 in fp32, off by at most 20 half steps of their absolute sum)."""
+    import torch
+    N, H, dl, dr = 65535, 128, 8, 8
+    ql, qr, cache = make(97, (N, H, dl), "bf16"), make(98, (N, H, dr), "bf16"), make(99, (N, 1, dl + dr), "bf16")
+    table = torch.randperm(N, device="cuda", dtype=torch.int32)[:, None]
+    lengths = torch.ones(N, device="cuda", dtype=torch.int32)
+    lengths[::7] = 0
+    o, lse = kda.latent_attention_step(ql, qr, cache, table, lengths, 0.25)
+    rows = cache[table[:, 0].long(), 0]
+    some = lengths > 0
+    assert torch.equal(o[some], rows[some][:, None, :dl].expand(-1, H, -1)) and (o[~some] == 0).all() and (lse[~some] == -float("inf")).all()
+    products = torch.cat([ql, qr], -1)[some].double() * rows[some].double()[:, None]
+    bound = 0.25 * 20 * 2.0 ** -24 * products.abs().sum(-1) + 4 * 2.0 ** -24
+    assert ((lse[some].double() - 0.25 * products.sum(-1)).abs() <= bound).all()
+
+
 def test_step_layouts_types_and_large_scores(kda):
     check_step(kda, 92, [100, 40], 16, 512, 64, 16, "bf16", out="fp32", layout="heads")
     check_step(kda, 93, [100, 40], 16, 512, 64, 16, "fp32", out="bf16", layout="heads")

@@ -128,6 +128,8 @@ def test_workspace_queries():
     for name, make in (("kda_latent_attention_step_workspace_bytes", step), ("kda_latent_attention_bwd_workspace_bytes", attend_bwd)):
         assert 0 < _lib.layer_raw(name, make()) < 1 << 30
         assert _lib.layer_raw(name, make(H=0)) == 2 ** 64 - 1
+    # many sequences and heads: a workgroup per sequence, no parts
+    assert _lib.layer_raw("kda_latent_attention_step_workspace_bytes", step(N=65535, H=128, page=16, max_blocks=4)) == 0
     # the rows' statistics and the heads' parts of the shared key's gradient
     for dtype, stats in ((BF16, 2), (FP32, 1)):
         assert _lib.layer_raw("kda_latent_attention_bwd_workspace_bytes", attend_bwd(in_dtype=dtype)) == stats * 2 * 50 * 4 * 4 + 2 * 60 * 4 * 64 * 4
