@@ -141,12 +141,11 @@ struct Fetch {
             for (int i = threadIdx.x * 16; i < BN * RT::ROW; i += 64 * W * 16) *reinterpret_cast<f4 *>(buffers + b * BUF + OR + i) = f4{0, 0, 0, 0};
         __syncthreads();
     }
-    __device__ __forceinline__ void load(int64_t at, char *to, int lane) const {
-        const int unit = lane % RT::UNITS, mine = own(lane);
-        // in front of the loads: a write to LDS would wait for those on their way there
-        if (unit == 0) reinterpret_cast<float *>(to + OM)[mine] = at < 0 ? neg_inf() : 0.f;
+    // Latent parts of the wave's rows from the first one to the last.
+    template <int FIRST, int LAST>
+    __device__ __forceinline__ void load_latent(int64_t at, char *to, int lane) const {
 #pragma unroll
-        for (int i = 0; i < RPW; ++i) {
+        for (int i = FIRST; i < LAST; ++i) {
             const int r = wave * RPW + i;
             const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(at), RT::UNITS * i);
             const int hi = __builtin_amdgcn_readlane(static_cast<int>(at >> 32), RT::UNITS * i);
@@ -160,6 +159,19 @@ struct Fetch {
                 }
             }
         }
+    }
+    // A tile in two parts, the second behind the scores of the tile before: all at once take their time to issue, and the products
+    // wait (128 heads, 4 sequences of 65,536 rows: 137 us against 145; 64 of 8,192 rows of 64 heads 114 against 120).
+    __device__ __forceinline__ void load(int64_t at, char *to, int lane) const {
+        load_front(at, to, lane);
+        load_back(at, to, lane);
+    }
+    __device__ __forceinline__ void load_back(int64_t at, char *to, int lane) const { load_latent<RPW / 2, RPW>(at, to, lane); }
+    __device__ __forceinline__ void load_front(int64_t at, char *to, int lane) const {
+        const int unit = lane % RT::UNITS, mine = own(lane);
+        // in front of the loads: a write to LDS would wait for those on their way there
+        if (unit == 0) reinterpret_cast<float *>(to + OM)[mine] = at < 0 ? neg_inf() : 0.f;
+        load_latent<0, RPW / 2>(at, to, lane);
         // The rotated parts of all these rows at once.  Where there is no row the scores are not used: what is in LDS may stay.
         if (lane < RPW * RT::UNITS) {
             const uint32_t off = latent + (unit ^ RT::swz(mine)) * 16;
@@ -223,8 +235,8 @@ __device__ __forceinline__ void store_empty(const LatentStepLaunch &P, int n, in
 // after it, whether or not it is of the same sequence.  With 32 heads of 512 + 64 in bf16, 64 ragged sequences of up to 8,192 rows
 // (302 MB) take 87 us with the join (3.6 TB/s), of up to 32,768 252 us (4.9 TB/s; 5.5 from one to the other): the cache's bandwidth
 // bounds it, and what a call costs that reads little, 17 us for 2,000 rows, where the lengths, the block numbers, the rows and the
-// join follow each other.  With 128 heads, 4 of 65,536 rows take 152 us (480 TFLOP/s): there each tile's scores, softmax and
-// products follow each other in waves that meet twice.
+// join follow each other.  With 128 heads, 4 of 65,536 rows take 147 us (500 TFLOP/s; 110 with the loads alone, 121 without
+// them): there each tile's scores, softmax and products follow each other in waves that meet twice.
 template <class E, int DLP, int HT>
 __global__ __launch_bounds__(64 * kWaves<HT>, sizeof(E) == 2 ? 2 : 1) void latent_step_kernel(const LatentStepLaunch P) {
     using S = Shape<E, HT>;
@@ -292,7 +304,8 @@ __global__ __launch_bounds__(64 * kWaves<HT>, sizeof(E) == 2 ? 2 : 1) void laten
             loads_done();  // here, or every tile's first product would wait for all loads
             begin_sequence();
         }
-        if (i + 1 < left) fetch.load(next, lds + (buf ^ 1) * F::BUF, lane_);
+        char *to = lds + (buf ^ 1) * F::BUF;
+        if (i + 1 < left) fetch.load_front(next, to, lane_);
         f4 s[KPW];
         if (scores) {
             float top = neg_inf();
@@ -316,6 +329,7 @@ __global__ __launch_bounds__(64 * kWaves<HT>, sizeof(E) == 2 ? 2 : 1) void laten
             top = quarters_max(top);
             if (g == 0) tops[(16 * ht + col) * KG + wave / HT] = top;
         }
+        if (i + 1 < left) fetch.load_back(next, to, lane_);
         lds_barrier();
         bool moved = false;
         float by[HT];
