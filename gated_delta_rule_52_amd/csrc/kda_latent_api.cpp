@@ -172,7 +172,7 @@ kda_status check_step_sizes(const kda_latent_step_args *a) {
         return fail(KDA_ERR_UNSUPPORTED, "more than 2^30 rows per sequence or 2^31 - 1 in the cache");
     // the sequences' tiles, of 16 rows or more, are counted in 32 bits
     if (((static_cast<int64_t>(a->max_blocks) * a->page + 15) / 16) * a->N > INT32_MAX)
-        return fail(KDA_ERR_UNSUPPORTED, "N * max_blocks * page is more than 2^35 rows");
+        return fail(KDA_ERR_UNSUPPORTED, "N * max_blocks * page is 2^35 rows or more");
     return check_grid(kda::latent_step_threads(a->N, a->H, a->in_dtype == KDA_DTYPE_BF16, step_splits(a)));
 }
 

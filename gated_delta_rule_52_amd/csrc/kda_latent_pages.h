@@ -1,5 +1,5 @@
-// kda_latent_pages.h - where a sequence's rows lie in the paged cache: plain arithmetic that the kernels and a program on
-// the CPU share.
+// kda_latent_pages.h - where a sequence's rows lie in the paged cache, and how tiles of rows are shared out over workgroups:
+// plain arithmetic that the kernels and a program on the CPU share.
 #pragma once
 
 #include <cstdint>
@@ -30,5 +30,19 @@ struct CachePages {
 __host__ __device__ __forceinline__ int64_t slot_row(int32_t slot, int64_t cache_rows) {
     return slot >= 0 && slot < cache_rows ? slot : -1;
 }
+
+// n in pieces of d, the last one smaller: n goes up to 2^31 - 1, where n + d - 1 would pass 32 bits.
+__host__ __device__ __forceinline__ int pieces(int n, int d) { return n > 0 ? (n - 1) / d + 1 : 0; }
+
+// Workgroup w's part of `total` tiles that `splits` workgroups share out evenly: the first `begin` lie in front of it.
+struct TileRun {
+    int run;          // tiles in a whole part
+    int begin, left;  // left: tiles in this one
+    __host__ __device__ __forceinline__ TileRun(int total, int splits, int w) : run(total > 0 ? pieces(total, splits) : 1) {
+        const int64_t at = static_cast<int64_t>(w) * run;
+        begin = at < total ? static_cast<int>(at) : total;
+        left = total - begin < run ? total - begin : run;
+    }
+};
 
 }  // namespace kda

@@ -64,7 +64,7 @@ struct Where {
 template <int BN>
 struct Tiles {
     const LatentStepLaunch &P;
-    __device__ __forceinline__ static int of(int length) { return length > 0 ? (length - 1) / BN + 1 : 0; }
+    __device__ __forceinline__ static int of(int length) { return pieces(length, BN); }
     __device__ __forceinline__ int length(int n) const { return P.pages.rows(P.lengths[n]); }
     __device__ __forceinline__ void next(Where &x) const {
         if (++x.tile < of(x.length)) return;
@@ -86,10 +86,10 @@ struct Tiles {
         int mine = 0, total;
         for (int i = from; i < min(P.N, from + chunk); ++i) mine += of(length(i));
         const int at = scan<W>(mine, shared, total);
-        run = max(1, (total + P.splits - 1) / P.splits);
-        const int64_t begin = static_cast<int64_t>(w) * run;
-        left = static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(run), total - begin)));
-        const int lo = static_cast<int>(min(begin, static_cast<int64_t>(total)));
+        const TileRun part(total, P.splits, w);
+        run = part.run;
+        left = part.left;
+        const int lo = part.begin;
         if (left > 0 && lo >= at && lo < at + mine) {
             int i = from, b = at, rows = length(i);
             while (i + 1 < P.N && lo >= b + of(rows)) {
@@ -297,7 +297,7 @@ __global__ __launch_bounds__(64 * kWaves<HT>, sizeof(E) == 2 ? 2 : 1) void laten
         const int64_t next = fetch.place(y, block, lane_);
         Where z = y;
         tiles.next(z);
-        block = i + 2 < left ? fetch.block(z, lane_) : -1;
+        block = i < left - 2 ? fetch.block(z, lane_) : -1;
         if (i > 0 && x.tile == 0) {
             const int lane_ = afresh(lane);  // or its addresses would be kept from tile to tile
             load_query<E, SL, SR>(qf, P, x.n, h0 + 16 * ht + (lane_ & 15), lane_);
@@ -391,7 +391,7 @@ __global__ __launch_bounds__(64 * kWaves<HT>, sizeof(E) == 2 ? 2 : 1) void laten
             lds_barrier();
             const int count = x.tile + 1 - t0, all = Tiles<BN>::of(x.length);
             const Parts parts(P, group, gridDim.y, HEADS);
-            if (P.splits && t0 == 0 && threadIdx.x == 0) parts.span[x.n] = int2{w, w + (all - count + run - 1) / run};
+            if (P.splits && t0 == 0 && threadIdx.x == 0) parts.span[x.n] = int2{w, w + pieces(all - count, run)};
 #pragma unroll
             for (int a = 0; a < HT; ++a) {
                 const int h = h0 + 16 * a + col;

@@ -829,7 +829,8 @@ kda_status kda_latent_cache_append(const kda_latent_append_args *args);
  *   that do not exist are left out, and entries behind a sequence's last row
  *   are not read.
  *   dl : at most 512, dr : at most 64.  scale > 0.  A sequence has at most 2^30
- *   rows, the cache 2^31 - 1, N * max_blocks * page at most 2^35.
+ *   rows, the cache 2^31 - 1; N times max_blocks * page, rounded up to 16, is
+ *   below 2^35.
  *   workspace : kda_latent_attention_step_workspace_bytes() bytes.
  */
 typedef struct {
