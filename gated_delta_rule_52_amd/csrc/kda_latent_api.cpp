@@ -46,7 +46,11 @@ Span span(const Tensor &t) {
     if (t.heads_inside()) return strided(t.name, t.p, t.rows, t.inner(), t.stride, t.dtype);
     return strided(t.name, t.p, t.heads, t.inner(), t.head_stride, t.dtype);
 }
-kda::Heads heads_of(const Tensor &t) { return {const_cast<void *>(t.p), t.stride, t.head_stride}; }
+// A stride that is not looked at (of one row, or one head) may hold anything; the kernels, whose tiles reach behind the last row and
+// take what a buffer's end makes zero there, get the width.
+kda::Heads heads_of(const Tensor &t) {
+    return {const_cast<void *>(t.p), t.rows > 1 ? t.stride : t.width, t.heads > 1 ? t.head_stride : t.width};
+}
 
 kda_status check_scale(float scale) {
     if (!(std::isfinite(scale) && scale > 0.f)) return fail(KDA_ERR_BAD_SHAPE, "scale must be finite and positive");
