@@ -9,6 +9,7 @@
 
 #include "kda.h"
 #include "kda_internal.h"
+#include "kda_spans.h"
 
 namespace {
 
@@ -31,27 +32,13 @@ kda_status hip_status(hipError_t e, const char *what) {
 bool valid_dtype(kda_dtype d) { return d == KDA_DTYPE_BF16 || d == KDA_DTYPE_FP32; }
 int64_t dsize(kda_dtype d) { return d == KDA_DTYPE_BF16 ? 2 : 4; }
 
-// The memory of a tensor: `rows` rows of `width` bytes, `stride` bytes apart.
-struct Span {
-    const char *name;
-    uintptr_t at;
-    int64_t rows, width, stride;
-    bool empty() const { return !at || rows <= 0 || width <= 0; }
-    uintptr_t end() const { return at + static_cast<uintptr_t>((rows - 1) * stride + width); }
-};
+using kda::Span;
+using kda::overlap;
 Span flat(const char *name, const void *p, int64_t bytes) {
     return {name, reinterpret_cast<uintptr_t>(p), 1, bytes, bytes};
 }
 Span strided(const char *name, const void *p, int64_t rows, int64_t width, int64_t stride, kda_dtype d) {
     return {name, reinterpret_cast<uintptr_t>(p), rows, width * dsize(d), stride * dsize(d)};
-}
-bool overlap(const Span &a, const Span &b) {
-    if (a.empty() || b.empty() || a.at >= b.end() || b.at >= a.end()) return false;
-    if (a.stride == b.stride && a.rows > 1 && b.rows > 1) {  // column slices of one buffer may interleave
-        const int64_t m = a.stride, d = ((static_cast<int64_t>(b.at - a.at) % m) + m) % m;
-        if (d >= a.width && d + b.width <= m) return false;
-    }
-    return true;
 }
 // Every output against every input and the other outputs.
 template <size_t NI, size_t NO>

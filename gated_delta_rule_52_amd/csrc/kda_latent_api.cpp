@@ -42,9 +42,10 @@ Span span(const Tensor &t) {
     if (t.heads <= 0) return flat(t.name, nullptr, 0);
     if (t.heads == 1) return strided(t.name, t.p, t.rows, t.width, t.rows > 1 ? t.stride : t.width, t.dtype);
     if (t.rows == 1) return strided(t.name, t.p, t.heads, t.width, t.head_stride, t.dtype);
-    if (t.stride == t.heads * t.head_stride) return strided(t.name, t.p, t.rows * t.heads, t.width, t.head_stride, t.dtype);
-    if (t.heads_inside()) return strided(t.name, t.p, t.rows, t.inner(), t.stride, t.dtype);
-    return strided(t.name, t.p, t.heads, t.inner(), t.head_stride, t.dtype);
+    Span s = t.heads_inside() ? strided(t.name, t.p, t.rows, t.width, t.stride, t.dtype) : strided(t.name, t.p, t.heads, t.width, t.head_stride, t.dtype);
+    s.parts = t.heads_inside() ? t.heads : t.rows;
+    s.part_stride = (t.heads_inside() ? t.head_stride : t.stride) * dsize(t.dtype);
+    return s;
 }
 // A stride that is not looked at (of one row, or one head) may hold anything; the kernels, whose tiles reach behind the last row and
 // take what a buffer's end makes zero there, get the width.
