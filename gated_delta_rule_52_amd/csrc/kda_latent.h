@@ -27,7 +27,7 @@ struct RotaryLaunch {
     hipStream_t stream;
 };
 hipError_t launch_rotary(const RotaryLaunch &P);
-int64_t rotary_threads(int64_t rows, int heads, int dim);
+int64_t rotary_threads(const RotaryLaunch &P);
 
 struct AppendLaunch {
     Heads latent, rope;  // head_stride unused

@@ -84,13 +84,6 @@ kda_status rotary(const kda_rotary_args *a, bool inverse, const char *what) {
     const Tensor y{"y", a->y, a->rows, a->heads, a->dim, a->y_stride, a->y_head_stride, a->dtype};
     KDA_TRY(check_tensor(x, kAnyStride));
     KDA_TRY(check_tensor(y, kAnyStride));
-    KDA_TRY(check_grid(kda::rotary_threads(a->rows, a->heads, a->dim)));
-    const bool in_place = a->x == a->y && (a->rows == 1 || a->x_stride == a->y_stride) &&
-                          (a->heads == 1 || a->x_head_stride == a->y_head_stride);
-    const Span ins[] = {in_place ? flat("x", nullptr, 0) : span(x), flat("positions", a->positions, a->rows * 4),
-                        flat("inv_freq", a->inv_freq, a->rot * 2)};
-    const Span outs[] = {span(y)};
-    KDA_TRY(check_overlaps(ins, outs));
     kda::RotaryLaunch L{};
     L.x = heads_of(x); L.y = heads_of(y);
     L.positions = a->positions; L.inv_freq = a->inv_freq;
@@ -100,6 +93,13 @@ kda_status rotary(const kda_rotary_args *a, bool inverse, const char *what) {
     L.inverse = inverse;
     L.bf16 = a->dtype == KDA_DTYPE_BF16;
     L.stream = static_cast<hipStream_t>(a->stream);
+    KDA_TRY(check_grid(kda::rotary_threads(L)));
+    const bool in_place = a->x == a->y && (a->rows == 1 || a->x_stride == a->y_stride) &&
+                          (a->heads == 1 || a->x_head_stride == a->y_head_stride);
+    const Span ins[] = {in_place ? flat("x", nullptr, 0) : span(x), flat("positions", a->positions, a->rows * 4),
+                        flat("inv_freq", a->inv_freq, a->rot * 2)};
+    const Span outs[] = {span(y)};
+    KDA_TRY(check_overlaps(ins, outs));
     return hip_status(kda::launch_rotary(L), what);
 }
 

@@ -152,10 +152,14 @@ RotaryCut rotary_cut(int64_t rows, int heads, int dim, int rot, int v, bool inte
     return c;
 }
 
+RotaryCut rotary_cut(const RotaryLaunch &P) {
+    const bool in_place = P.x.p == P.y.p;  // then nothing is copied
+    return rotary_cut(P.rows, P.heads, in_place ? P.rot : P.dim, P.rot, !rotary_wide(P) ? 1 : P.bf16 ? 8 : 4, P.interleaved);
+}
+
 template <class E, int V>
 hipError_t launch(const RotaryLaunch &P) {
-    const bool in_place = P.x.p == P.y.p;  // then nothing is copied
-    const RotaryCut c = rotary_cut(P.rows, P.heads, in_place ? P.rot : P.dim, P.rot, V, P.interleaved);
+    const RotaryCut c = rotary_cut(P);
     const int64_t grid = (P.rows + c.rows - 1) / c.rows * c.groups;
     rotary_kernel<E, V><<<static_cast<unsigned>(grid), 256, 0, P.stream>>>(P, c);
     return hipGetLastError();
@@ -203,11 +207,7 @@ hipError_t launch_rotary(const RotaryLaunch &P) {
     if (P.bf16) return wide_ ? launch<uint16_t, 8>(P) : launch<uint16_t, 1>(P);
     return wide_ ? launch<float, 4>(P) : launch<float, 1>(P);
 }
-int64_t rotary_threads(int64_t rows, int heads, int dim) {
-    // at most a workgroup per row and 1,024 units of its heads, or per head of more
-    const int64_t units = dim > 1024 ? 1024 : dim, per = 1024 / (units > 0 ? units : 1);
-    return rows * ((heads + per - 1) / per) * 256;
-}
+int64_t rotary_threads(const RotaryLaunch &P) { return P.rows * rotary_cut(P).groups * 256; }  // as if each row had its own workgroups
 
 hipError_t launch_append(const AppendLaunch &P) {
     const int v = P.bf16 ? 8 : 4;

@@ -767,6 +767,9 @@ kda_status kda_layer_norm_bwd(const kda_layer_norm_bwd_args *args);
  *   x, y : [rows, heads, dim] dtype; y may be x (same strides): only the
  *          turned part is touched then.  positions : [rows] int32, inv_freq :
  *          [rot / 2] fp32.  rot is even, at most 4096; dim at most 2^15.
+ *   A row's heads are worked on in groups of about 1,024 units, a unit being 16
+ *   bytes, or one element where a part, a stride or an address is not whole 16
+ *   bytes; rows times groups is below 2^24.
  * kda_rotary_bwd: the gradient (x: of y, y: of x), which turns the other way.
  */
 typedef struct {
@@ -793,7 +796,8 @@ kda_status kda_rotary_bwd(const kda_rotary_args *args);
  *   latent : [rows, dl], rope : [rows, dr], cache : [num_blocks, page, dl + dr]
  *   dtype;  slots : [rows] int32, a block times `page` plus the place in it.
  *   Rows whose slot is negative or behind the cache are skipped.  Slots of
- *   one call differ: a slot given twice holds elements of either row.
+ *   one call differ: a slot given twice holds elements of either row.  rows is
+ *   below 2^26.
  *   positions : [rows] int32, inv_freq : [dr / 2] fp32, both or neither.
  */
 typedef struct {
