@@ -34,3 +34,28 @@ def test_bf16_over_many_keys(kda, dims, causal):  # noqa: F811
 def test_long_prompts(kda, dtype):  # noqa: F811
     check_fwd(kda, 340, (1, 130, 4100), 2, LARGE, dtype, True)
     check_bwd(kda, 350, (1, 2100, 2100), 1, SMALL, dtype, True)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_rows_in_front_of_the_first_sequence(kda, dtype):  # noqa: F811
+    """NaN there enters nothing, and outputs keep what they hold there: the bits of a call without those rows elsewhere."""
+    import torch
+    from test_gpu_latent import ints, make, tdtype
+    H, (dn, dr, dv), front = 3, LARGE, 141
+    off_q, off_k = [0, 150, 150, 331], [0, 130, 140, 333]
+    x = {n: make(360 + i, (1, T, *s), dtype) for i, (n, T, s) in enumerate((
+        ("q", 331, (H, dn + dr)), ("k", 333, (H, dn)), ("kr", 333, (dr,)), ("v", 333, (H, dv)), ("go", 331, (H, dv))))}
+    moved = {n: torch.cat([torch.full_like(t[:, :front], float("nan")), t], 1) for n, t in x.items()}
+
+    def both(t, shift):
+        new = lambda *s: torch.full((1, *s), 7.0, dtype=tdtype(dtype), device="cuda")  # noqa: E731
+        Tq, Tk = t["q"].shape[1], t["k"].shape[1]
+        kw = dict(cu_seqlens_q=ints(off_q) + shift, cu_seqlens_k=ints(off_k) + shift)
+        args = (t["q"], t["k"], t["kr"], t["v"])
+        o, lse = kda.latent_attention_fwd(*args, o=new(Tq, H, dv), lse=torch.full((1, Tq, H), 7.0, device="cuda"), **kw)
+        out = dict(dq=new(Tq, H, dn + dr), dk=new(Tk, H, dn), dk_rope=new(Tk, dr), dv=new(Tk, H, dv))
+        return [o, lse, *kda.latent_attention_bwd(*args, o, lse, t["go"], grad_dtype=tdtype(dtype), out=out, **kw).values()]
+    a, b = both(x, 0), both(moved, front)
+    for m, n in zip(a, b):
+        assert (n[:, :front] == 7).all()
+        assert torch.isfinite(n[:, front:]).sum() == torch.isfinite(m).sum() and torch.equal(m, n[:, front:])
