@@ -381,7 +381,7 @@ int64_t attend_threads(const SeqTiles &q_, const SeqTiles &k_, int H, int dr, bo
     q.L = k.L = bf16 ? kAttendTile : kAttendTileF32;
     int64_t n = (tiles_of(q) + (backward && !bf16 ? tiles_of(k) : 0)) * H * (bf16 ? 256 : 512);
     if (backward) {
-        const int64_t parts[] = {tiles_of(k) * H * 256, (q.rows() * H + 15) / 16 * 256, (k.rows() * (dr / 4) + 255) / 256 * 256};
+        const int64_t parts[] = {tiles_of(k) * H * 256, bf16 ? 0 : (q.rows() * H + 15) / 16 * 256, (k.rows() * (dr / 4) + 255) / 256 * 256};
         for (const int64_t p : parts) n = p > n ? p : n;
     }
     return n;

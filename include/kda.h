@@ -873,6 +873,8 @@ kda_status kda_latent_attention_step(const kda_latent_step_args *args);
  *   queries and of the keys (both; then batch is 1).
  *   dn, dv : at most 128, dr : at most 64.  scale > 0.  Row strides are below
  *   2^22 elements; at most 2^30 rows.
+ *   A call has fewer than 2^24 tiles of 128 rows of a head in bf16, in fp32 2^23 of
+ *   32 rows, the gradients' of queries and keys together.
  */
 typedef struct {
     uint32_t struct_size; /* = sizeof(kda_latent_attention_args) */

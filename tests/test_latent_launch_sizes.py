@@ -1,9 +1,9 @@
-"""CPU test of how large a rotation one launch holds: counted in the workgroups that it makes, and refused beyond.  The addresses are
-made up; a call that is not refused for its size is refused for the output that lies on its positions."""
+"""CPU tests of how large a rotation and how large gradients one launch holds: counted in the workgroups that it makes, and refused
+beyond.  The addresses are made up; a call that is not refused for its size is refused for an output that lies on an input."""
 import pytest
 
 from gated_delta_rule_52_amd import _lib
-from test_latent_abi import ALIAS, F, FP32, S, UNSUP, rotary
+from test_latent_abi import ALIAS, BF16, F, FP32, S, UNSUP, attend_bwd, rotary
 
 
 def call(rows, heads, dim, rot, offset, dtype=0, **kw):
@@ -28,3 +28,22 @@ def test_held(rows, heads, dim, rot, offset, dtype):
 def test_refused(rows, heads, dim, rot, offset, dtype):
     assert call(rows, heads, dim, rot, offset, dtype) == S[UNSUP]
     assert _lib.load().kda_last_error().decode() == "problem too large for one launch"
+
+
+def gradients(T, H, dtype):
+    """Heads of 8 + 8 and 8, causal."""
+    G = 1 << 48
+    names = ("q", "k", "k_rope", "v", "o", "grad_o", "grad_q", "grad_k", "grad_k_rope", "grad_v")
+    width = dict(q=16, grad_q=16)
+    kw = {n: (i + 1) * G for i, n in enumerate(names)}
+    kw.update({n + "_stride": 8 if "rope" in n else H * width.get(n, 8) for n in names})
+    kw.update({n + "_head_stride": width.get(n, 8) for n in names if "rope" not in n})
+    kw.update(lse=20 * G, workspace=30 * G, workspace_bytes=1 << 46, grad_q=G, batch=1, num_seqs=1, Tq=T, Tk=T, H=H, dn=8, dr=8, dv=8,
+              in_dtype=dtype, grad_dtype=dtype)
+    return _lib.layer_raw("kda_latent_attention_bwd", attend_bwd(**kw))
+
+
+@pytest.mark.parametrize("T,H,dtype,status", [
+    (1 << 26, 4, BF16, ALIAS), ((1 << 30) - 128, 1, BF16, ALIAS), (1 << 30, 2, BF16, UNSUP), ((1 << 27) - 32, 1, FP32, ALIAS), (1 << 27, 1, FP32, UNSUP)])
+def test_gradients(T, H, dtype, status):
+    assert gradients(T, H, dtype) == S[status], _lib.load().kda_last_error()
