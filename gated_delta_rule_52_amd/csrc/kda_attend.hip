@@ -15,10 +15,10 @@ using namespace la;
 // queries across: a lane then has 32 scores of one query, its maximum and sum need one exchange between the wave's halves, and
 // the weights are the next product's operand as they lie.
 //
-// The matrix unit bounds it: 8,192 rows of 32 heads, causal, 128 + 64 and 128 wide (687 GFLOP), take 670 us, 1.03 PFLOP/s, and
-// 16,384 rows of 16 heads 1,226 us, 1.12 PFLOP/s, where the same instructions with nothing beside them reach 1.7 to 1.9; what is
-// between is exponentials that meet no other wave's products.  Waves that are at the scores' products go first (s_setprio): the
-// first of these took 694 us without and 658 with, before rows were stored whole.
+// The matrix unit bounds it: 8,192 rows of 32 heads, causal, 128 + 64 and 128 wide (687 GFLOP), take 636 to 690 us on several
+// cards, 1.0 to 1.08 PFLOP/s, and 16,384 rows of 16 heads 1,240 us, 1.11 PFLOP/s, where the same instructions with nothing beside
+// them reach 1.7 to 1.9; what is between is exponentials that meet no other wave's products.  Waves that are at the scores' products
+// go first (s_setprio): the first of these takes 641 us so and 670 without.
 template <int NP, int RP, int VP>
 __global__ __launch_bounds__(256, 2) void attend_fwd_kernel(const AttendLaunch P) {
     typedef uint16_t E;
@@ -145,7 +145,10 @@ hipError_t launch_attend_fwd(const AttendLaunch &P) {
     AttendLaunch L = P;
     L.q_seq.L = kAttendTile;
     const unsigned n = static_cast<unsigned>(tiles_of(L.q_seq) * P.H);
-    // Heads are padded with zeros to one of two sizes (2,048 rows of 32 heads of 64 + 32 and 64: 49 us, padded to the larger one 69).
+    // Heads are padded with zeros to one of two sizes (2,048 rows of 32 heads of 64 + 32 and 64: 44 us, padded to the larger one 61).
+    // At the smaller one a product has twice the exponentials beside it, and 512 workgroups are all there at once, of which the last has
+    // twice the average's keys: the matrix unit is busy for 23% of the cycles, vector instructions for 34%.  At 8,192 rows, with
+    // workgroups to follow, it is 390 us, 0.88 PFLOP/s.
     if (P.dn <= 64 && P.dr <= 32 && P.dv <= 64) attend_fwd_kernel<64, 32, 64><<<n, 256, 0, P.stream>>>(L);
     else attend_fwd_kernel<128, 64, 128><<<n, 256, 0, P.stream>>>(L);
     return hipGetLastError();

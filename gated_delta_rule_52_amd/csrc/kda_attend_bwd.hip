@@ -188,10 +188,9 @@ __global__ __launch_bounds__(256, 1) void attend_dkv_kernel(const AttendLaunch P
 }
 
 // As the forward pass: 128 queries per workgroup, 32 per wave, over the keys that they see.  Two workgroups share a CU: one's
-// exponentials hide behind the other's products, and waves that are at a product go first (s_setprio: 600 us against 608 for 2
-// sequences of 4,096 rows of 32 heads).  Blocks of 32 keys one after the other, not unrolled: two at a time do not fit the 256
-// registers beside q's, grad_o's and the sums'.   The same
-// sequences: 590 us for 550 GFLOP, 0.93 PFLOP/s.
+// exponentials hide behind the other's products, and waves that are at a product go first (s_setprio: for 2 sequences of 4,096 rows of
+// 32 heads all gradients take 1,416 us so and 1,445 without).  Blocks of 32 keys one after the other, not unrolled: two at a time do
+// not fit the 256 registers beside q's, grad_o's and the sums'.  The same sequences: 590 us for 550 GFLOP, 0.93 PFLOP/s.
 template <int NP, int RP, int VP>
 __global__ __launch_bounds__(256, 2) void attend_dq_kernel(const AttendLaunch P) {
     typedef uint16_t E;
@@ -257,7 +256,7 @@ __global__ __launch_bounds__(256, 2) void attend_dq_kernel(const AttendLaunch P)
     // o is rounded to bf16, and where few keys share the weights that rounding is of the size of dp - delta itself.  There a
     // walk over the keys in front of the other finds what delta is off by: sum_j p_j (dp_j - delta), which is 0 for the right one
     // (dq's errors relative to 64 bits, causal: sequences of 16 rows 0.0030 without and 0.0024 with it, 1,000 rows 0.0025 and 0.0024;
-    // 256 rows of 8 heads take 49 us for 42, 1,024 of 16 104 for 102).
+    // 256 rows of 8 heads take 46 us for 38, 1,024 of 16 98 for 97).
     bool exact = keys > 256;
     float off = 0.f;
     auto store_statistics = [&]() {
@@ -361,7 +360,9 @@ void launch(const AttendLaunch &L, bool keys) {
 hipError_t launch_attend_bwd(const AttendLaunch &P) {
     AttendLaunch L = P;
     L.q_seq.L = L.k_seq.L = kAttendTile;
-    // as in the forward pass (2,048 rows of 32 heads of 64 + 32 and 64: 183 us, padded to the larger size 279)
+    // as in the forward pass (2,048 rows of 32 heads of 64 + 32 and 64: 169 us, padded to the larger size 260; 90 of them
+    // in each kernel, the matrix unit busy for 19% of dq's cycles and 24% of dk/dv's: twice the exponentials per product, and 512 workgroups
+    // are one round of dq's and two of dk/dv's, whose longest decide)
     const bool small = P.dn <= 64 && P.dr <= 32 && P.dv <= 64;
     const int64_t rows_q = L.q_seq.rows() * L.H, rope = L.k_seq.rows() * (L.dr / 4);
     if (P.bf16) {

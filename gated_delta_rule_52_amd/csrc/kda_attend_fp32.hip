@@ -3,12 +3,12 @@
 //
 // The fp32 matrix unit bounds these kernels: a 32 x 32 tile of pairs takes a wave 10,000 cycles forward and 20,000 backward at
 // the full head sizes, its operands 40 to 80 KiB.  So the operands come straight from the caches, without LDS, a few steps
-// ahead of their products; what counts is that all waves have work.  A workgroup has 32 queries (or keys), and its four
-// waves share out the tiles of keys (or queries) that they meet and add up their results through LDS at the end, in the
-// waves' order.  (Tiles in LDS, 64 rows to a workgroup: 256 rows of 8 heads 61 us forward against 21, 1,024 of 16 223 against 100,
-// 4,096 of 16 1,326 against 741; gradients of the last 3,506 against 3,280.)  At 4,096 rows of 16 heads that is 116 TFLOP/s forward
-// and 68 for the gradients (94 with the products that are formed twice) of the unit's 157: the loads of operands that
-// no product hides.
+// ahead of their products; what counts is that all waves have work.  A workgroup has 32 queries (or keys), and its waves,
+// four of them or eight where there are few workgroups (`few`), share out the tiles of keys (or queries) that they meet and add up their
+// results through LDS at the end, in the waves' order.  (With tiles in LDS, 64 rows to a workgroup of four waves, 256 rows of 8 heads
+// took 61 us forward, 1,024 of 16 223, 4,096 of 16 1,326, and gradients of the last 3,506; so they take 21, 67, 730 and 3,330.)  At
+// 4,096 rows of 16 heads that is 118 TFLOP/s forward and 67 for the gradients (93 with the products that are formed twice) of the
+// unit's 157: the loads of operands that no product hides.
 #include "kda_latent.h"
 
 namespace kda {
@@ -320,13 +320,14 @@ __global__ __launch_bounds__(64 * WAVES, NP > 64 ? 1 : 2) void attend_grads_fp32
     else dq_fp32<WAVES, NP, RP, VP>(P, blockIdx.x - key_groups, sums);
 }
 
-// Heads are padded with zeros to one of two sizes (2 sequences of 2,048 rows of 16 heads of 64 + 32 and 64: the gradients 808 us, padded
-// to the larger one 1,280).
+// Heads are padded with zeros to one of two sizes (2 sequences of 2,048 rows of 16 heads of 64 + 32 and 64: the gradients 800 us, padded
+// to the larger one 1,300).
 bool small(const AttendLaunch &P) { return P.dn <= 64 && P.dr <= 32 && P.dv <= 64; }
 
 // Eight waves share a tile's work where there are few workgroups, and so the longest sequence's tiles decide; where there are
-// many, more results to add up only cost (four waves and eight, forward at the full head sizes: 1,024 rows of 16 heads 98 and 75
-// us, 1,536 rows 127 and 143; gradients at the small ones: 1,024 rows of 8 heads 114 and 90 us, 1,536 of 16 261 and 285).
+// many, more results to add up only cost (four waves and eight, forward at the full head sizes: 1,024 rows of 16 heads 91 and 67
+// us, 1,536 rows 120 and 136; gradients at the small ones: 1,024 rows of 8 heads 105 and 80 us, 1,536 of 16 255 and 280).  Of packed
+// sequences the launch's slots count, up to one more for each than it has tiles: what the lengths are the host does not know.
 bool few(unsigned n) { return n <= 512; }
 
 template <int WAVES, int NP, int RP, int VP>

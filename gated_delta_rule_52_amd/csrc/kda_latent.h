@@ -241,7 +241,9 @@ struct LdsTile {
     }
 };
 
-// Rows of a 32 x 32 result as a step's operand (the order that cols32 reads in).
+// Rows of a 32 x 32 result as a step's operand (the order that cols32 reads in): weights and their gradients, rounded to bf16 as the
+// matrix unit takes them.  Each is off by 2^-8 of itself at most, about what the result's own rounding to bf16 costs; operands in
+// two parts would take that away for as many products again.
 __device__ __forceinline__ b8 result_operand(const f16 &s, int step) {
     b8 v;
 #pragma unroll
@@ -291,8 +293,8 @@ __device__ __forceinline__ void loads_landed() {
 
 // The rows of a wave's results: row lane % 32 has, in tile c, columns 32 c + 8 b + 4 (lane / 32) .. + 3 as elements 4 b .. + 3.
 // Rows of bf16 are put together in LDS (32 * kStoreRow<W> bytes of the wave's own) and leave 16 bytes per lane and whole rows at
-// a time (the forward kernel at 8,192 rows of 32 heads takes 646 us so and 658 with eight bytes to each of 64 places, the
-// gradients' query kernel at 2 sequences of 4,096 rows 590 and 600).  `to`: the wave's first row.
+// a time (measured together: the forward kernel at 8,192 rows of 32 heads 646 us so and 658 with eight bytes to each of 64 places,
+// the gradients' query kernel at 2 sequences of 4,096 rows 590 and 600).  `to`: the wave's first row.
 template <int W>
 constexpr int kStoreRow = 2 * W + 16;
 template <int W>

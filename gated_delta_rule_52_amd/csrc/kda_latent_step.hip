@@ -161,7 +161,7 @@ struct Fetch {
         }
     }
     // A tile in two parts, the second behind the scores of the tile before: all at once take their time to issue, and the products
-    // wait (128 heads, 4 sequences of 65,536 rows: 137 us against 145; 64 of 8,192 rows of 64 heads 114 against 120).
+    // wait (128 heads, 4 sequences of 65,536 rows: 138 us against 145; 64 of 8,192 rows of 64 heads 108 against 114).
     __device__ __forceinline__ void load(int64_t at, char *to, int lane) const {
         load_front(at, to, lane);
         load_back(at, to, lane);
@@ -233,10 +233,12 @@ __device__ __forceinline__ void store_empty(const LatentStepLaunch &P, int n, in
 //
 // A workgroup goes through its run of tiles as one stream: the next tile's rows are on their way, and the block numbers of the one
 // after it, whether or not it is of the same sequence.  With 32 heads of 512 + 64 in bf16, 64 ragged sequences of up to 8,192 rows
-// (302 MB) take 87 us with the join (3.6 TB/s), of up to 32,768 252 us (4.9 TB/s; 5.5 from one to the other): the cache's bandwidth
-// bounds it, and what a call costs that reads little, 17 us for 2,000 rows, where the lengths, the block numbers, the rows and the
-// join follow each other.  With 128 heads, 4 of 65,536 rows take 147 us (500 TFLOP/s; 110 with the loads alone, 121 without
-// them): there each tile's scores, softmax and products follow each other in waves that meet twice.
+// (302 MB) take 79 us with the join (3.9 TB/s; 73 with the loads alone, 55 without them), of up to 32,768 219 us (5.6 TB/s; 6.6 from
+// one to the other): the cache's bandwidth bounds it, and what a call costs that reads little, 16 us for 2,000 rows, where the
+// lengths, the block numbers, the rows and the join follow each other.  With 128 heads, 4 of 65,536 rows take 139 us (530 TFLOP/s; 99
+// with the loads alone, 110 without them): there each tile's scores, softmax and products follow each other in waves that meet
+// twice.  In fp32 a tile has 16 rows and its scores come from one wave for 16 heads and two for 32 while the others wait: 64 ragged
+// sequences of 16 heads 220 us (2.8 TB/s), of 32 heads 379.
 template <class E, int DLP, int HT>
 __global__ __launch_bounds__(64 * kWaves<HT>, sizeof(E) == 2 ? 2 : 1) void latent_step_kernel(const LatentStepLaunch P) {
     using S = Shape<E, HT>;
@@ -350,7 +352,8 @@ __global__ __launch_bounds__(64 * kWaves<HT>, sizeof(E) == 2 ? 2 : 1) void laten
 #pragma unroll
             for (int a = 1; a < HT; ++a) at = a == ht ? m[a] : at;
             at = at == neg_inf() ? 0.f : at;
-            // in the order in which a step's operand takes them: of each 32 keys, 4 g .. + 3 of either half together
+            // in the order in which a step's operand takes them: of each 32 keys, 4 g .. + 3 of either half together; in bf16 rounded as
+            // the matrix unit takes them (result_operand), while l sums them as they are
             char *to = weights + (16 * ht + col) * PROW + g * 16;
 #pragma unroll
             for (int b = 0; b < KPW; ++b) {
@@ -475,9 +478,10 @@ __global__ __launch_bounds__(256) void latent_join_kernel(const LatentStepLaunch
     if (threadIdx.x == 0 && blockIdx.y == 0 && P.lse) P.lse[head] = sum == 0.f ? neg_inf() : at + __log2f(sum) * kLn2;
 }
 
-// Tiles of 16 heads per workgroup, and groups of so many heads.  Fewer tiles than the heads fill save time (64 sequences of 16 heads
-// 78 us, of 32 heads 87, of 64 heads 122), more than four cost more to join than they save on rows (128 heads as one group,
-// 4 sequences of 16,384 rows: 70 us against 57; of 65,536 rows 145 against 152).
+// Tiles of 16 heads per workgroup, and groups of so many heads.  No more tiles than the heads fill: 64 sequences of 16 heads
+// take 72 us, of 32 heads 79, of 64 heads 108.  More than four were slower at short contexts, with twice the parts to join (measured
+// before a tile's rows were loaded in two parts, 128 heads as one group and as two: 4 sequences of 16,384 rows 70 us and 57, of
+// 65,536 rows 145 and 152; as two groups they take 52 and 138 now).
 int head_tiles(int H, bool bf16) { return H <= 16 ? 1 : H <= 32 || !bf16 ? 2 : 4; }
 int head_groups(int H, bool bf16) {
     const int per = 16 * head_tiles(H, bf16);
@@ -502,9 +506,10 @@ void launch_dl(const LatentStepLaunch &P) {
 }  // namespace
 
 // Workgroups over which the sequences' tiles are shared out: what the CUs hold at once (two workgroups each, one where it has eight
-// waves), no more than there can be tiles.  0: a workgroup per sequence and no parts, where there are enough of them and none is so
-// long that the others wait for it (32 heads, ragged, that way and shared out: 1,024 sequences of up to 256 rows 63 and 102 us,
-// of up to 1,024 177 and 194, of up to 4,096 618 and 520; 4,096 of up to 512 327 and 436).
+// waves), no more than there can be tiles.  0: a workgroup per sequence and no parts, where there are enough of them and none can be
+// so long that the others wait for it (32 heads, ragged, that way and shared out: 1,024 sequences of up to 256 rows 58 and 97 us,
+// of up to 1,024 170 and 186, of up to 4,096 591 and 500; 4,096 of up to 512 324 and 432).  `longest` is what the block table has
+// room for: the lengths are on the device.  A caller whose sequences are all much shorter gives the table's first columns.
 int latent_step_splits(int N, int H, int64_t longest, bool bf16) {
     if (N >= 1024 && longest <= 2048) return 0;
     int64_t s = (head_tiles(H, bf16) == 4 ? 256 : kJoinParts) / head_groups(H, bf16);
@@ -528,9 +533,8 @@ hipError_t launch_latent_step(const LatentStepLaunch &P) {
     if (P.splits) {
         const int64_t rows = P.N * static_cast<int64_t>(P.H);
         const int heads = 16 * head_tiles(P.H, P.bf16), groups = head_groups(P.H, P.bf16);
-        // All columns at once where there are rows enough for every CU (64 sequences of 32 heads 9 us against 16), a quarter where a few rows
-        // have many parts (one sequence of 65,536 rows 43 us
-        // against 60 for both kernels).
+        // All columns at once where there are rows enough for every CU (64 sequences of 32 heads 79 us for both kernels against 84), a
+        // quarter where a few rows have many parts (one sequence of 65,536 rows 41 us against 59).
         if (rows >= kJoinWhole) latent_join_kernel<512><<<static_cast<unsigned>(rows), 256, 0, P.stream>>>(P, heads, groups);
         else latent_join_kernel<128><<<dim3(static_cast<unsigned>(rows), (P.dl + 127) / 128), 256, 0, P.stream>>>(P, heads, groups);
     }

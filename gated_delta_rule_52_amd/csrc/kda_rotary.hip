@@ -122,7 +122,8 @@ __global__ __launch_bounds__(256) void rotary_kernel(const RotaryLaunch P, const
 
 bool aligned(const void *p, int bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
 
-// 16 bytes per access where every head's parts allow it, single elements elsewhere.
+// 16 bytes per access where every head's parts allow it, single elements elsewhere: the rotation above with its part from element 126
+// on takes 244 us against 77, two thirds of its cycles for 87 million vector instructions against 20.
 bool rotary_wide(const RotaryLaunch &P) {
     const int v = P.bf16 ? 8 : 4;
     auto whole = [&](int64_t n) { return n % v == 0; };
@@ -168,7 +169,7 @@ hipError_t launch(const RotaryLaunch &P) {
 // ---- the cache ------------------------------------------------------------------------------------------
 
 // A wave per row: its latent part is copied while the angles of the rest are formed.  One decode step's 64 rows take 2.8 us, less
-// than a launch; 16,384 rows (38 MB both ways) 9 us.
+// than a launch; 16,384 rows (38 MB both ways) 9.1 us, what lies above those 2.8 at 6.0 TB/s.
 template <class E, int V>
 __global__ __launch_bounds__(256) void append_kernel(const AppendLaunch P) {
     const int lane = threadIdx.x & 63;

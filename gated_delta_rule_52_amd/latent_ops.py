@@ -154,7 +154,8 @@ def latent_attention_step(q_latent: torch.Tensor, q_rope: torch.Tensor, cache: t
 
     q_latent [N,H,dl], q_rope [N,H,dr], cache [blocks,page,dl+dr]: one type, bf16 or fp32; block_table [N,max_blocks],
     lengths [N]: int32.  Lengths are held to 0 .. max_blocks * page; rows on blocks that do not exist are left out.  A
-    sequence without rows gets o = 0 and lse = -inf.  Returns (o [N,H,dl], lse [N,H] fp32)."""
+    sequence without rows gets o = 0 and lse = -inf.  Where all sequences are much shorter than the table,
+    block_table[:, :k] with the k columns in use may be faster.  Returns (o [N,H,dl], lse [N,H] fp32)."""
     device = _first(q_latent, "q_latent", (3,))
     kind, dtype = _kind(q_latent, "q_latent"), q_latent.dtype
     if q_rope.dim() != 3 or cache.dim() != 3 or block_table.dim() != 2:
@@ -216,8 +217,9 @@ def latent_attention_fwd(q: torch.Tensor, k: torch.Tensor, k_rope: torch.Tensor,
     q [B,Tq,H,dn+dr], k [B,Tk,H,dn], k_rope [B,Tk,dr] (one for all heads), v [B,Tk,H,dv]: one type, bf16 or fp32; k and v
     may be slices of one [B,Tk,H,dn+dv] tensor.  ``causal``: query i of nq sees keys 0 .. i + nk - nq.  Packed input:
     B == 1 and int32 [N+1] offsets of the queries and of the keys; rows at and behind the last are left as they were.
-    scale defaults to (dn + dr)^-0.5.  A query that sees no key gets o = 0 and lse = -inf.
-    Returns (o [B,Tq,H,dv], lse [B,Tq,H] fp32, which the gradients take)."""
+    scale defaults to (dn + dr)^-0.5.  A query that sees no key gets o = 0 and lse = -inf.  Infinite or NaN values of a key
+    that is hidden from a query of its sequence may reach that query's result.
+    Returns (o [B,Tq,H,dv], lse [B,Tq,H] fp32); the gradients take both, o in q's type (``out_dtype`` left out)."""
     device, dtype, kind, sizes, strides, cu_q, cu_k = _attend(q, k, k_rope, v, scale, cu_seqlens_q, cu_seqlens_k)
     B, Tq, H, dv = sizes[0], sizes[1], sizes[3], sizes[6]
     if o is None:

@@ -748,8 +748,9 @@ kda_status kda_layer_norm_bwd(const kda_layer_norm_bwd_args *args);
  *  - A query that sees no key gets o = 0 and lse = -inf, and no gradient.
  *  - What a query does not see has weight 0, and is multiplied with it: an
  *    infinite or NaN value of a key that is hidden from a query of the same
- *    sequence may make that query's result NaN.  Rows of other sequences, rows
- *    behind the last one and cache rows behind a sequence's end never count.
+ *    sequence may make that query's result NaN, and one of such a query the
+ *    key's gradients.  Rows of other sequences, rows behind the last one and
+ *    cache rows behind a sequence's end never count.
  *  - Rows outside the sequences of a packed batch are left as they were.
  */
 
@@ -831,7 +832,9 @@ kda_status kda_latent_cache_append(const kda_latent_append_args *args);
  *   block_table : [N, max_blocks] int32, block_table_stride apart;  lengths :
  *   [N] int32.  Lengths are held to 0 .. max_blocks * page; rows on blocks
  *   that do not exist are left out, and entries behind a sequence's last row
- *   are not read.
+ *   are not read.  How the work is shared out follows max_blocks, as lengths
+ *   are not known to the host: where all sequences are much shorter than the
+ *   table, max_blocks may be its columns in use (with the table's stride).
  *   dl : at most 512, dr : at most 64.  scale > 0.  A sequence has at most 2^30
  *   rows, the cache 2^31 - 1; N times max_blocks * page, rounded up to 16, is
  *   below 2^35.
