@@ -38,19 +38,17 @@ kda_status check_aligned(const Tensor &t) {
         return fail(KDA_ERR_UNSUPPORTED, "%s: base and strides have to be multiples of 16 bytes", t.name);
     return KDA_OK;
 }
-Span span(const Tensor &t) {
-    if (t.heads <= 0) return flat(t.name, nullptr, 0);
-    if (t.heads == 1) return strided(t.name, t.p, t.rows, t.width, t.rows > 1 ? t.stride : t.width, t.dtype);
-    if (t.rows == 1) return strided(t.name, t.p, t.heads, t.width, t.head_stride, t.dtype);
-    Span s = t.heads_inside() ? strided(t.name, t.p, t.rows, t.width, t.stride, t.dtype) : strided(t.name, t.p, t.heads, t.width, t.head_stride, t.dtype);
-    s.parts = t.heads_inside() ? t.heads : t.rows;
-    s.part_stride = (t.heads_inside() ? t.head_stride : t.stride) * dsize(t.dtype);
-    return s;
-}
-// A stride that is not looked at (of one row, or one head) may hold anything; the kernels, whose tiles reach behind the last row and
-// take what a buffer's end makes zero there, get the width.
+// A stride that is not looked at (of one row, or one head) may hold anything: the width takes its place, as the kernels' tiles reach
+// behind the last row and count on the zeros that a buffer gives past its end.
 kda::Heads heads_of(const Tensor &t) {
     return {const_cast<void *>(t.p), t.rows > 1 ? t.stride : t.width, t.heads > 1 ? t.head_stride : t.width};
+}
+Span span(const Tensor &t) {
+    const kda::Heads at = heads_of(t);
+    Span s = t.heads_inside() ? strided(t.name, t.p, t.rows, t.width, at.stride, t.dtype) : strided(t.name, t.p, t.heads, t.width, at.head_stride, t.dtype);
+    s.parts = t.heads_inside() ? t.heads : t.rows;
+    s.part_stride = (t.heads_inside() ? at.head_stride : at.stride) * dsize(t.dtype);
+    return s;
 }
 
 kda_status check_scale(float scale) {

@@ -6,8 +6,8 @@
 
 namespace kda {
 
-// The memory of a tensor: `rows` rows `stride` bytes apart, each of `parts` parts of `width` bytes, `part_stride` apart, that end
-// within the stride.
+// The memory of a tensor: `rows` rows `stride` bytes apart (not looked at for one), each of `parts` parts of `width` bytes,
+// `part_stride` apart (the same).
 struct Span {
     const char *name;
     uintptr_t at;
@@ -21,9 +21,11 @@ struct Span {
 // False only where no byte is in both: apart as a whole, or slices of one buffer that interleave.
 inline bool overlap(const Span &a, const Span &b) {
     if (a.empty() || b.empty() || a.at >= b.end() || b.at >= a.end()) return false;
-    if (a.stride != b.stride || a.rows <= 1 || b.rows <= 1) return true;
+    // a single row lies in any distance of rows that holds it
+    const int64_t s = a.rows > 1 ? a.stride : b.rows > 1 ? b.stride : int64_t{1} << 60;
+    if ((b.rows > 1 && b.stride != s) || a.row() > s || b.row() > s) return true;
     // b's rows begin `off` bytes behind a's and may reach into a's next one
-    const int64_t s = a.stride, m = a.parts > 1 ? a.part_stride : b.part_stride;
+    const int64_t m = a.parts > 1 ? a.part_stride : b.part_stride;
     const int64_t off = ((static_cast<int64_t>(b.at - a.at) % s) + s) % s;
     // b's parts between a's, the rows this far apart
     auto between = [&](int64_t d) {

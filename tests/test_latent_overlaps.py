@@ -77,6 +77,16 @@ def test_slices_of_one_buffer_share_nothing(overlaps, pad, rows, parts):
     assert overlaps([(a, b), (b, a), (a, a)]) == [False, False, True]
 
 
+@pytest.mark.parametrize("odd", [0, -5, 10 ** 9])
+def test_a_single_row_between_the_parts_of_many(overlaps, odd):
+    """Its own stride is not looked at, nor that of a single part."""
+    many, one = (100, 5, 7, 40, 3, 12), (187, 1, 5, odd, 3, 12)
+    part = (187, 1, 5, odd, 1, odd)
+    assert overlaps([(many, one), (one, many), (many, part), (part, many), (one, (192, 1, 7, odd, 2, 12)), (one, (191, 1, 7, odd, 2, 12)),
+                     (many, (186, 1, 5, odd, 3, 12)), (part, (180, 1, 8, odd, 1, odd)), (part, (180, 1, 7, odd, 1, odd))]) \
+        == [False, False, False, False, False, True, True, True, False]
+
+
 # [rows, heads] strides of one buffer [rows, heads, 256] in bf16 or fp32: dense, padded rows, padded by less than a head, heads in front
 @pytest.mark.parametrize("stride,head_stride", [(1024, 256), (2048, 256), (1032, 256), (1024 + 64, 256), (256, 256 * 120), (264, 264 * 120)])
 def test_gradients_as_slices_of_one_buffer(stride, head_stride):
