@@ -6,7 +6,7 @@
 // ahead of their products; what counts is that all waves have work.  A workgroup has 32 queries (or keys), and its waves,
 // four of them or eight where there are few workgroups (`few`), share out the tiles of keys (or queries) that they meet and add up their
 // results through LDS at the end, in the waves' order.  (With tiles in LDS, 64 rows to a workgroup of four waves, 256 rows of 8 heads
-// took 61 us forward, 1,024 of 16 223, 4,096 of 16 1,326, and gradients of the last 3,506; so they take 21, 67, 730 and 3,330.)  At
+// took 61 us forward, 1,024 of 16 223, 4,096 of 16 1,326, and gradients of the last 3,506; as they are they take 21, 67, 730 and 3,330.)  At
 // 4,096 rows of 16 heads that is 118 TFLOP/s forward and 67 for the gradients (93 with the products that are formed twice) of the
 // unit's 157: the loads of operands that no product hides.
 #include "kda_latent.h"
